@@ -21,3 +21,11 @@ from .bitdelta import (  # noqa: F401
     library,
 )
 from .cache import Busy, bd_cache  # noqa: F401
+from .step import (  # noqa: F401
+    bd_attend,
+    bd_kv_cache,
+    bd_kv_read,
+    bd_kv_write,
+    bd_rms_norm,
+    bd_rms_norm_e4m3,
+)

@@ -77,7 +77,9 @@ bd_status finish(hipError_t e) { return e == hipSuccess ? BD_OK : hip_fail(e); }
 }  // namespace
 
 namespace bd {
+bd_status check_current_device(int* num_cu);  // step_internal.h
 void note_hip_error(hipError_t e) { g_last_hip_error = static_cast<int32_t>(e); }
+bd_status check_current_device(int* num_cu) { return check_device(num_cu); }
 }  // namespace bd
 
 extern "C" {
@@ -88,10 +90,10 @@ const char* bd_status_string(bd_status s) {
     switch (s) {
         case BD_OK: return "ok";
         case BD_ERR_NULL: return "a required pointer is NULL";
-        case BD_ERR_SHAPE: return "invalid shape (need d_out >= 1, d_in >= 8, d_in % 8 == 0, M >= 0)";
-        case BD_ERR_ALIGN: return "misaligned pointer (x, w_base, delta, y need 16-byte alignment)";
+        case BD_ERR_SHAPE: return "invalid shape (linears: d_out >= 1, d_in >= 8, d_in % 8 == 0, M >= 0)";
+        case BD_ERR_ALIGN: return "misaligned pointer or stride (x, w_base, delta, y need 16-byte alignment)";
         case BD_ERR_WORKSPACE: return "workspace too small or misaligned";
-        case BD_ERR_MODE: return "unknown alpha mode";
+        case BD_ERR_MODE: return "unknown alpha mode or type";
         case BD_ERR_HIP: return "HIP call failed";
         case BD_ERR_DEVICE: return "current device is not a gfx950 GPU";
     }

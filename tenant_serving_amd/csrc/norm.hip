@@ -1,0 +1,181 @@
+// RMS norm with the residual's addition in front, a bf16 or an e4m3 result.
+//
+//   h = x + residual, kept as residual_out; y = h / sqrt(mean(h^2) + eps) * g
+//
+// Bound by HBM: a row is read once, stays in the registers of the lanes that
+// read it (8 consecutive values per lane and chunk) while its sum of squares
+// is taken, and is written once.  The mean is over the values that the
+// residual stream holds afterwards, so a rounding to bf16 comes before it.
+// Sums are fp32: each lane's own values in order, then a butterfly over the
+// wave, then the waves' sums in wave order.
+//
+// A group of 32 columns of the e4m3 result is four neighbouring lanes, whose
+// largest magnitude two lane exchanges give.
+#include "step_internal.h"
+
+namespace bd {
+namespace {
+
+template <int NT>
+constexpr int kNormBlock = NT == 64 ? 256 : NT;
+
+// kRes: 0 no residual, 1 bf16, 2 fp32.  NT lanes own a row (64: four rows to a
+// workgroup, one per wave), C chunks of 8 values each.
+template <bool kX32, int kRes, bool kE4m3, int NT, int C>
+__global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, int64_t row0) {
+    const int tid = NT == 64 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+    const int64_t row = row0 + (NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x);
+    if (NT == 64 && row >= a.M) return;  // a whole wave; this form has no barrier
+    const int64_t base = row * a.d;
+
+    Raw8<kX32> xr[C];
+    Raw8<kRes == 2> rr[C];
+    Raw8<false> gb[C];
+    const int id = a.ids ? a.ids[row] : 0;
+    const bool known = id >= 0 && id < a.num_gains;
+    const int64_t gbase = known ? (int64_t)id * a.d : 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (c * NT + tid) * 8;
+        xr[c].zero();
+        rr[c].zero();
+        if (e < a.d) {
+            xr[c].load(a.x, base + e);
+            if (kRes) rr[c].load(a.residual, base + e);
+        }
+    }
+    if (!a.gain_fp32) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = (c * NT + tid) * 8;
+            gb[c].zero();
+            if (e < a.d) gb[c].load(a.gain, gbase + e);
+        }
+    }
+
+    float h[C][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (c * NT + tid) * 8;
+        xr[c].widen(h[c]);
+        if (kRes) {
+            float r[8];
+            rr[c].widen(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[c][i] += r[i];
+            if (kRes == 1) {
+                const uint4 w = narrow_bf16x8(h[c]);
+                if (e < a.d) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.residual_out) + base + e) = w;
+                widen_bf16x8(w, h[c]);
+            } else if (e < a.d) {
+                float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.residual_out) + base + e);
+                p[0] = make_float4(h[c][0], h[c][1], h[c][2], h[c][3]);
+                p[1] = make_float4(h[c][4], h[c][5], h[c][6], h[c][7]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[c][i], h[c][i], sum);
+    }
+    sum = wave_sum(sum);
+    if (NT > 64) {
+        __shared__ float part[NT / 64];
+        if ((tid & 63) == 0) part[tid >> 6] = sum;
+        __syncthreads();
+        sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w) sum += part[w];
+    }
+    const float rstd = known ? 1.0f / sqrtf(sum / (float)a.d + a.eps) : __builtin_nanf("");
+
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = (c * NT + tid) * 8;
+        float g[8];
+        if (a.gain_fp32) {
+            Raw8<true> gw;
+            gw.zero();
+            if (e < a.d) gw.load(a.gain, gbase + e);
+            gw.widen(g);
+        } else {
+            gb[c].widen(g);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[c][i] = h[c][i] * rstd * g[i];
+        if (kE4m3) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = finite_bits(h[c][i]);
+                top = b > top ? b : top;
+            }
+            // lanes past d hold zeros (or NaN, which counts as 0)
+#pragma unroll
+            for (int off = 1; off <= 2; off <<= 1) {
+                const uint32_t o = (uint32_t)__shfl_xor((int)top, off, 64);
+                top = o > top ? o : top;
+            }
+            const int byte = known ? scale_byte(top) : 127;
+            const float inv = inv_scale_of(byte);
+            if (e < a.d) {
+                const uint2 w = make_uint2(pack_e4m3x4(h[c][0], h[c][1], h[c][2], h[c][3], inv),
+                                           pack_e4m3x4(h[c][4], h[c][5], h[c][6], h[c][7], inv));
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + base + e) = w;
+                if ((tid & 3) == 0) a.scales[row * ((a.d + 31) / 32) + e / 32] = (uint8_t)byte;
+            }
+        } else if (e < a.d) {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + base + e) = narrow_bf16x8(h[c]);
+        }
+    }
+}
+
+template <bool kX32, int kRes, bool kE4m3, int NT, int C>
+void go(const NormArgs& a, hipStream_t s) {
+    constexpr int64_t most = int64_t(1) << 21;  // rows of one launch: its threads number below 2^32
+    for (int64_t row0 = 0; row0 < a.M; row0 += most) {
+        const int64_t n = a.M - row0 < most ? a.M - row0 : most;
+        const unsigned grid = (unsigned)(NT == 64 ? (n + 3) / 4 : n);
+        hipLaunchKernelGGL((norm_kernel<kX32, kRes, kE4m3, NT, C>), dim3(grid), dim3(kNormBlock<NT>), 0, s, a, row0);
+    }
+}
+
+template <bool kX32, int kRes, bool kE4m3>
+void pick(const NormArgs& a, hipStream_t s) {
+    if (a.d <= 512) return go<kX32, kRes, kE4m3, 64, 1>(a, s);
+    if (a.d <= 2048) return go<kX32, kRes, kE4m3, 256, 1>(a, s);
+    if (a.d <= 4096) return go<kX32, kRes, kE4m3, 256, 2>(a, s);
+    if (a.d <= 8192) return go<kX32, kRes, kE4m3, 256, 4>(a, s);
+    if (a.d <= 16384) return go<kX32, kRes, kE4m3, 1024, 2>(a, s);
+    if (a.d <= 32768) return go<kX32, kRes, kE4m3, 1024, 4>(a, s);
+    return go<kX32, kRes, kE4m3, 1024, 8>(a, s);
+}
+
+template <bool kX32, int kRes>
+void pick_out(const NormArgs& a, bool e4m3, hipStream_t s) {
+    if (e4m3)
+        pick<kX32, kRes, true>(a, s);
+    else
+        pick<kX32, kRes, false>(a, s);
+}
+
+template <bool kX32>
+void pick_res(const NormArgs& a, int residual, bool e4m3, hipStream_t s) {
+    if (residual == 0)
+        pick_out<kX32, 0>(a, e4m3, s);
+    else if (residual == 1)
+        pick_out<kX32, 1>(a, e4m3, s);
+    else
+        pick_out<kX32, 2>(a, e4m3, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, bool x_fp32, int residual, bool e4m3, hipStream_t stream) {
+    if (x_fp32)
+        pick_res<true>(a, residual, e4m3, stream);
+    else
+        pick_res<false>(a, residual, e4m3, stream);
+    return hipGetLastError();
+}
+
+}  // namespace bd

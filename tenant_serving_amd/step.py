@@ -1,0 +1,381 @@
+"""Python binding of the operators between the linears of a step
+(include/bitdelta_step.h), same names.
+
+Argument marshalling only: shape, dtype, stride and device checks, output and
+workspace allocation with torch, and the current HIP stream of the tensors'
+device.  Every step of the computation runs in the library's HIP kernels;
+there is no fallback.
+
+A step of a served model runs, per layer: ``bd_rms_norm`` (the residual added,
+each token normed with its variant's gain), the q, k, v linears,
+``bd_kv_write``, ``bd_attend``, the output linear, ``bd_rms_norm`` again and
+the remaining linears.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+import torch
+
+from .bitdelta import _check, _workspace, library
+
+BD_BF16, BD_FP32, BD_E4M3 = 0, 1, 2
+_IN = {torch.bfloat16: BD_BF16, torch.float32: BD_FP32}
+_HELD = {torch.bfloat16: BD_BF16, torch.float8_e4m3fn: BD_E4M3}
+_declared = None
+
+
+class _KV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("type", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+_Pair = ctypes.c_int64 * 2
+
+
+def declare(lib):
+    p, i32, i64, f, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    lib.bd_rms_norm.argtypes = [p, i32, p, p, i32, p, i32, i32, p, f, p, i32, p, i64, i64, p]
+    lib.bd_kv_write.argtypes = [p, p, p, p, p, i32, p, i64, p]
+    lib.bd_kv_read.argtypes = [p, p, i64, p, p, p]
+    lib.bd_attend.argtypes = [p, p, i32, p, i32, p, i64, i64, p, i64, f, p, p, p, sz, p]
+    for n in ("rms_norm", "kv_write", "kv_read", "attend"):
+        getattr(lib, "bd_" + n).restype = ctypes.c_int
+    lib.bd_attend_workspace_bytes.argtypes = [i64] * 6
+    lib.bd_attend_workspace_bytes.restype = sz
+    return lib
+
+
+def _library():
+    global _declared
+    if _declared is None:
+        _declared = declare(library())
+    return _declared
+
+
+def _tensor(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+
+
+def _typed(name, t, types):
+    _tensor(name, t)
+    got = types.get(t.dtype)
+    if got is None:
+        raise TypeError("%s must be one of %s (got %s)" % (name, ", ".join(str(d) for d in types), t.dtype))
+    return got
+
+
+def _plain(name, t, dtype, shape):
+    """A contiguous tensor of this dtype and shape."""
+    _tensor(name, t)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _same_gpu(device, named):
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU (got %s); there is no CPU path" % device)
+    for name, t in named:
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+
+
+def _on(device):
+    """Makes the tensors' device the current one for the call, where it is not."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _overlap(a, b):
+    """Whether the memory of two contiguous tensors overlaps."""
+    return (a.data_ptr() < b.data_ptr() + b.numel() * b.element_size()
+            and b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
+
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales):
+    lib = _library()
+    x_type = _typed("x", x, _IN)
+    gain_type = _typed("gain", gain, _IN)
+    if x.dim() < 1 or not x.is_contiguous():
+        raise ValueError("x must be contiguous [..., d]")
+    d = x.shape[-1]
+    if gain.dim() not in (1, 2) or gain.shape[-1] != d or not gain.is_contiguous():
+        raise ValueError("gain must be contiguous [d] or [num_gains, d] with d=%d (got %s)" % (d, tuple(gain.shape)))
+    num_gains = 1 if gain.dim() == 1 else gain.shape[0]
+    if d < 8 or d % 8 or d > 65536 or num_gains < 1:
+        raise ValueError("d must be a multiple of 8, 8..65536, and there must be a gain (got d=%d, %d gains)"
+                         % (d, num_gains))
+    eps = float(eps)
+    if not eps >= 0.0:
+        raise ValueError("eps must be >= 0 (got %r)" % eps)
+    lead = x.shape[:-1]
+    M = math.prod(lead)
+    if variant_ids is not None:
+        _plain("variant_ids", variant_ids, torch.int32, lead)
+    res_type = BD_BF16
+    if residual is not None:
+        res_type = _typed("residual", residual, _IN)
+        _plain("residual", residual, residual.dtype, x.shape)
+        if residual_out is not None and residual_out is not residual:
+            _plain("residual_out", residual_out, residual.dtype, x.shape)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    held = torch.bfloat16 if out_type == BD_BF16 else torch.float8_e4m3fn
+    if out is not None:
+        _plain("out", out, held, x.shape)
+    if scales is not None:
+        _plain("scales", scales, torch.uint8, (*lead, (d + 31) // 32))
+    _same_gpu(x.device, (("gain", gain), ("residual", residual), ("variant_ids", variant_ids),
+                         ("residual_out", residual_out), ("out", out), ("scales", scales)))
+    written = [("out", out), ("scales", scales)]
+    if residual_out is not None and residual is not None and residual_out.data_ptr() != residual.data_ptr():
+        written.append(("residual_out", residual_out))
+    read = [("x", x), ("gain", gain), ("residual", residual), ("variant_ids", variant_ids),
+            ("residual_out", residual_out)]
+    for name, t in written:
+        for other, o in read + written:
+            if t is not None and o is not None and other != name and t.numel() and o.numel() and _overlap(t, o):
+                raise ValueError("%s overlaps %s" % (name, other))
+    if residual_out is not None and residual_out.data_ptr() == residual.data_ptr():
+        for other, o in (("x", x), ("gain", gain)):
+            if o.numel() and residual_out.numel() and _overlap(residual_out, o):
+                raise ValueError("residual_out overlaps %s" % other)
+    with _on(x.device):
+        if out is None:
+            out = torch.empty_like(x, dtype=held)
+        if out_type == BD_E4M3 and scales is None:
+            scales = torch.empty((*lead, (d + 31) // 32), dtype=torch.uint8, device=x.device)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(residual)
+        st = lib.bd_rms_norm(x.data_ptr(), x_type, _at(residual), _at(residual_out), res_type, gain.data_ptr(),
+                             gain_type, num_gains, _at(variant_ids), eps, out.data_ptr(), out_type, _at(scales), M,
+                             d, torch.cuda.current_stream(x.device).cuda_stream)
+        _check(lib, "bd_rms_norm", st)
+    return out, scales, residual_out
+
+
+def bd_rms_norm(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+                variant_ids: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                out: torch.Tensor | None = None):
+    """h = x + residual (kept in the residual's type); y = h / sqrt(mean(h²) + eps) · gain, as bf16.
+
+    x [..., d] is bf16 or fp32, gain [d] or, with variant_ids (int32 [...]), [num_gains, d]: each token takes its
+    variant's.  Returns y, or (y, residual_out) with a residual; residual_out may be the residual itself (updated in
+    place) and is allocated where it is not given."""
+    out, _, res = _rms_norm(BD_BF16, x, gain, eps, residual, variant_ids, residual_out, out, None)
+    return out if residual is None else (out, res)
+
+
+def bd_rms_norm_e4m3(x: torch.Tensor, gain: torch.Tensor, eps: float = 1e-5, residual: torch.Tensor | None = None,
+                     variant_ids: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """bd_rms_norm with y held in 8 bits: (codes float8_e4m3fn [..., d], scales uint8 [..., ceil(d/32)]), one scale
+    2^(byte − 127) per 32 columns, and residual_out after them with a residual."""
+    out, scales, res = _rms_norm(BD_E4M3, x, gain, eps, residual, variant_ids, residual_out, out, scales)
+    return (out, scales) if residual is None else (out, scales, res)
+
+
+class bd_kv_cache:
+    """A paged key-value cache over the caller's tensors.
+
+    k, v: [num_pages, num_heads, page_size, head_dim], bf16 or float8_e4m3fn, alike in shape, dtype and strides,
+    head_dim contiguous (a [num_pages, page_size, num_heads, head_dim] buffer goes in as its transpose(1, 2)).
+    k_scales, v_scales: uint8 [num_pages, num_heads, page_size] for float8_e4m3fn, one scale byte per row.
+    The tensors are kept by reference; the checks run once, here."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor | None = None,
+                 v_scales: torch.Tensor | None = None):
+        kind = _typed("k", k, _HELD)
+        _tensor("v", v)
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
+            raise ValueError("k and v must be alike: [num_pages, num_heads, page_size, head_dim], one dtype, one layout")
+        pages, heads, page, dim = k.shape
+        if pages < 1 or not 1 <= heads <= 65535 or page % 8 or not 8 <= page <= 4096:
+            raise ValueError("need pages, 1..65535 heads and a page size that is a multiple of 8, 8..4096 (got %s)"
+                             % (tuple(k.shape),))
+        if dim % 16 or not 16 <= dim <= 256:
+            raise ValueError("head_dim must be a multiple of 16, 16..256 (got %d)" % dim)
+        if pages * page > 2 ** 31 - 1:
+            raise ValueError("more than 2^31 - 1 slots")
+        stride = list(k.stride())
+        for i, n in enumerate(k.shape):
+            if n == 1:
+                stride[i] = 0 if i < 3 else 1  # never stepped over
+        if stride[3] != 1:
+            raise ValueError("head_dim must be contiguous")
+        size = k.element_size()
+        if any(s * size % 16 for s in stride[:3]) or k.data_ptr() % 16 or v.data_ptr() % 16:
+            raise ValueError("k, v and their strides must be multiples of 16 bytes")
+        # distinct rows must not overlap: each axis steps over all of the smaller ones
+        steps = sorted((s, n) for s, n in zip(stride[:3], k.shape[:3]) if n > 1)
+        extent = dim
+        for s, n in steps:
+            if s < extent:
+                raise ValueError("rows of k overlap (strides %s)" % (tuple(k.stride()),))
+            extent = s * (n - 1) + extent
+        self._span = extent * size
+        if kind == BD_E4M3:
+            for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+                _plain(name, t, torch.uint8, (pages, heads, page))
+                if t.data_ptr() % 8:
+                    raise ValueError("%s must be 8-byte aligned" % name)
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("a bf16 cache has no scales")
+        _same_gpu(k.device, (("v", v), ("k_scales", k_scales), ("v_scales", v_scales)))
+        if abs(k.data_ptr() - v.data_ptr()) < self._span and not self._interleaved(k, v, stride, size):
+            raise ValueError("k and v overlap")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.num_pages, self.num_heads, self.page_size, self.head_dim = pages, heads, page, dim
+        self.device = k.device
+        self._desc = _KV(k.data_ptr(), v.data_ptr(), _at(k_scales), _at(v_scales), kind, heads, dim, page, pages,
+                         *stride[:3])
+        self._ref = ctypes.addressof(self._desc)
+
+    @staticmethod
+    def _interleaved(k, v, stride, size):
+        """Whether v's rows lie in the gaps of k's: both are slices of one buffer, along an axis whose step leaves
+        room for the other's block."""
+        gap = abs(k.data_ptr() - v.data_ptr()) // size
+        inner = [(s, n) for s, n in zip(stride[:3], k.shape[:3]) if n > 1 and s <= gap]
+        outer = [s for s, n in zip(stride[:3], k.shape[:3]) if n > 1 and s > gap]
+        block = sum(s * (n - 1) for s, n in inner) + k.shape[3]
+        return block <= gap and all(gap + block <= s for s in outer)
+
+    @classmethod
+    def empty(cls, num_pages: int, num_heads: int, page_size: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
+              device="cuda"):
+        """A cache of its own memory, contents undefined."""
+        shape = (num_pages, num_heads, page_size, head_dim)
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.float8_e4m3fn:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
+
+
+def _rows(name, t, kv_heads, dim):
+    """(type, strides) of [n, heads, dim] rows with any token and head stride."""
+    kind = _typed(name, t, _IN)
+    if t.dim() != 3 or (kv_heads is not None and t.shape[1] != kv_heads) or t.shape[2] != dim:
+        raise ValueError("%s must be [n, %s, %d] (got %s)" % (name, kv_heads or "num_q_heads", dim, tuple(t.shape)))
+    a, b, c = t.stride()
+    if t.shape[0] <= 1:
+        a = 0
+    if t.shape[1] <= 1:
+        b = 0
+    if c != 1:
+        raise ValueError("%s's rows must be contiguous" % name)
+    size = t.element_size()
+    if a * size % 16 or b * size % 16 or t.data_ptr() % 16:
+        raise ValueError("%s and its strides must be multiples of 16 bytes" % name)
+    return kind, _Pair(a, b)
+
+
+def _cache(kv):
+    if not isinstance(kv, bd_kv_cache):
+        raise TypeError("kv must be a bd_kv_cache")
+    return kv
+
+
+def bd_kv_write(kv: bd_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
+    """Writes the rows k, v [T, num_heads, head_dim] (bf16 or fp32, any token and head strides) of T tokens into the
+    cache's slots (int32 [T]; slot = page · page_size + place).  Slots below 0 or past the cache's end are skipped; of
+    several tokens with one slot the last stays."""
+    lib = _library()
+    _cache(kv)
+    kind, ks = _rows("k", k, kv.num_heads, kv.head_dim)
+    v_kind, vs = _rows("v", v, kv.num_heads, kv.head_dim)
+    if v_kind != kind or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have one dtype and one number of tokens")
+    T = k.shape[0]
+    _plain("slots", slots, torch.int32, (T,))
+    _same_gpu(kv.device, (("k", k), ("v", v), ("slots", slots)))
+    with _on(kv.device):
+        st = lib.bd_kv_write(kv._ref, k.data_ptr(), ks, v.data_ptr(), vs, kind, slots.data_ptr(), T,
+                             torch.cuda.current_stream(kv.device).cuda_stream)
+        _check(lib, "bd_kv_write", st)
+
+
+def bd_kv_read(kv: bd_kv_cache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
+    """The rows of T slots (int32 [T]) as bf16 (k, v), each [T, num_heads, head_dim], exactly as held.  Slots below 0
+    give zeros, slots past the cache's end NaN."""
+    lib = _library()
+    _cache(kv)
+    _tensor("slots", slots)
+    shape = (slots.numel(), kv.num_heads, kv.head_dim)
+    _plain("slots", slots, torch.int32, shape[:1])
+    if out is not None:
+        for name, t in zip(("out[0]", "out[1]"), out):
+            _plain(name, t, torch.bfloat16, shape)
+        if slots.numel() and _overlap(*out):
+            raise ValueError("out[0] overlaps out[1]")
+        _same_gpu(kv.device, (("slots", slots), ("out[0]", out[0]), ("out[1]", out[1])))
+    else:
+        _same_gpu(kv.device, (("slots", slots),))
+    with _on(kv.device):
+        k, v = out if out is not None else (torch.empty(shape, dtype=torch.bfloat16, device=kv.device)
+                                            for _ in range(2))
+        st = lib.bd_kv_read(kv._ref, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
+                            torch.cuda.current_stream(kv.device).cuda_stream)
+        _check(lib, "bd_kv_read", st)
+    return k, v
+
+
+def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, lengths: torch.Tensor,
+              scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None):
+    """softmax(scale · q kᵀ) v of one new token per sequence over the cache; bf16 [B, num_q_heads, head_dim].
+
+    q [B, num_q_heads, head_dim] is bf16 or fp32 (any token and head strides); num_q_heads is a multiple of the cache's
+    heads.  page_table int32 [B, max_pages] (rows may be strided) and lengths int32 [B] say which tokens: lengths
+    counts the new one, whose row is in the cache by then.  A length of 0 gives zeros.  scale defaults to
+    head_dim^-0.5.  lse, if given, is an fp32 [B, num_q_heads] tensor that receives the log of the softmax's sum."""
+    lib = _library()
+    _cache(kv)
+    kind, qs = _rows("q", q, None, kv.head_dim)
+    B, heads = q.shape[0], q.shape[1]
+    if heads < 1 or heads > 65535 or heads % kv.num_heads:
+        raise ValueError("q's heads must be a multiple of the cache's %d, at most 65535 (got %d)" % (kv.num_heads, heads))
+    _tensor("page_table", page_table)
+    if page_table.dtype != torch.int32:
+        raise TypeError("page_table must be torch.int32 (got %s)" % page_table.dtype)
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1:
+        raise ValueError("page_table must be [%d, max_pages] (got %s)" % (B, tuple(page_table.shape)))
+    most = page_table.shape[1]
+    if most > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table's rows must be contiguous")
+    if most * kv.page_size > 1 << 24:
+        raise ValueError("page_table holds more than 2^24 tokens per sequence")
+    _plain("lengths", lengths, torch.int32, (B,))
+    scale = kv.head_dim ** -0.5 if scale is None else float(scale)
+    if not math.isfinite(scale):
+        raise ValueError("scale must be finite (got %r)" % scale)
+    if out is not None:
+        _plain("out", out, torch.bfloat16, (B, heads, kv.head_dim))
+    if lse is not None:
+        _plain("lse", lse, torch.float32, (B, heads))
+    _same_gpu(kv.device, (("q", q), ("page_table", page_table), ("lengths", lengths), ("out", out), ("lse", lse)))
+    nbytes = lib.bd_attend_workspace_bytes(B, heads, kv.num_heads, kv.head_dim, kv.page_size, most)
+    with _on(kv.device):
+        if out is None:
+            out = torch.empty((B, heads, kv.head_dim), dtype=torch.bfloat16, device=kv.device)
+        ws = _workspace(nbytes, kv.device)
+        st = lib.bd_attend(kv._ref, q.data_ptr(), kind, qs, heads, page_table.data_ptr(),
+                           page_table.stride(0) if B > 1 else 0, most, lengths.data_ptr(), B, scale, out.data_ptr(),
+                           _at(lse), _at(ws), nbytes, torch.cuda.current_stream(kv.device).cuda_stream)
+        _check(lib, "bd_attend", st)
+    return out
