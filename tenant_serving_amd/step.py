@@ -14,8 +14,8 @@ the remaining linears.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -26,6 +26,11 @@ BD_BF16, BD_FP32, BD_E4M3 = 0, 1, 2
 _IN = {torch.bfloat16: BD_BF16, torch.float32: BD_FP32}
 _HELD = {torch.bfloat16: BD_BF16, torch.float8_e4m3fn: BD_E4M3}
 _declared = None
+# the current stream's handle and device as plain numbers: a call of a few microseconds on the GPU has no room for the
+# objects around them (torch.cuda.current_stream takes 1.9 us, this 0.1)
+_stream_of = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+              or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class _KV(ctypes.Structure):
@@ -91,13 +96,6 @@ def _same_gpu(device, named):
             raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
 
 
-def _on(device):
-    """Makes the tensors' device the current one for the call, where it is not."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
 def _overlap(a, b):
     """Whether the memory of two contiguous tensors overlaps."""
     return (a.data_ptr() < b.data_ptr() + b.numel() * b.element_size()
@@ -108,10 +106,10 @@ def _at(t):
     return t.data_ptr() if t is not None else None
 
 
-def _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales):
-    lib = _library()
-    x_type = _typed("x", x, _IN)
-    gain_type = _typed("gain", gain, _IN)
+def _refuse_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales):
+    """Every check of a norm's arguments, in full; raises or returns."""
+    _typed("x", x, _IN)
+    _typed("gain", gain, _IN)
     if x.dim() < 1 or not x.is_contiguous():
         raise ValueError("x must be contiguous [..., d]")
     d = x.shape[-1]
@@ -121,51 +119,85 @@ def _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, 
     if d < 8 or d % 8 or d > 65536 or num_gains < 1:
         raise ValueError("d must be a multiple of 8, 8..65536, and there must be a gain (got d=%d, %d gains)"
                          % (d, num_gains))
-    eps = float(eps)
     if not eps >= 0.0:
         raise ValueError("eps must be >= 0 (got %r)" % eps)
     lead = x.shape[:-1]
-    M = math.prod(lead)
     if variant_ids is not None:
         _plain("variant_ids", variant_ids, torch.int32, lead)
-    res_type = BD_BF16
     if residual is not None:
-        res_type = _typed("residual", residual, _IN)
+        _typed("residual", residual, _IN)
         _plain("residual", residual, residual.dtype, x.shape)
         if residual_out is not None and residual_out is not residual:
             _plain("residual_out", residual_out, residual.dtype, x.shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    held = torch.bfloat16 if out_type == BD_BF16 else torch.float8_e4m3fn
     if out is not None:
-        _plain("out", out, held, x.shape)
+        _plain("out", out, torch.bfloat16 if out_type == BD_BF16 else torch.float8_e4m3fn, x.shape)
     if scales is not None:
         _plain("scales", scales, torch.uint8, (*lead, (d + 31) // 32))
-    _same_gpu(x.device, (("gain", gain), ("residual", residual), ("variant_ids", variant_ids),
-                         ("residual_out", residual_out), ("out", out), ("scales", scales)))
-    written = [("out", out), ("scales", scales)]
-    if residual_out is not None and residual is not None and residual_out.data_ptr() != residual.data_ptr():
-        written.append(("residual_out", residual_out))
-    read = [("x", x), ("gain", gain), ("residual", residual), ("variant_ids", variant_ids),
-            ("residual_out", residual_out)]
-    for name, t in written:
-        for other, o in read + written:
-            if t is not None and o is not None and other != name and t.numel() and o.numel() and _overlap(t, o):
+    every = [("x", x), ("gain", gain), ("residual", residual), ("variant_ids", variant_ids),
+             ("residual_out", residual_out), ("out", out), ("scales", scales)]
+    _same_gpu(x.device, every)
+    # no output may meet anything else, but for a residual updated in place
+    every = [(name, t) for name, t in every if t is not None and t.numel()]
+    for name, t in every[::-1]:
+        if name not in ("residual_out", "out", "scales"):
+            continue
+        for other, o in every:
+            if other == name or (name == "residual_out" and other == "residual" and o.data_ptr() == t.data_ptr()):
+                continue
+            if other == "residual" and residual_out is not None and o.data_ptr() == residual_out.data_ptr():
+                continue  # seen as residual_out
+            if _overlap(t, o):
                 raise ValueError("%s overlaps %s" % (name, other))
-    if residual_out is not None and residual_out.data_ptr() == residual.data_ptr():
-        for other, o in (("x", x), ("gain", gain)):
-            if o.numel() and residual_out.numel() and _overlap(residual_out, o):
-                raise ValueError("residual_out overlaps %s" % other)
-    with _on(x.device):
-        if out is None:
-            out = torch.empty_like(x, dtype=held)
-        if out_type == BD_E4M3 and scales is None:
-            scales = torch.empty((*lead, (d + 31) // 32), dtype=torch.uint8, device=x.device)
-        if residual is not None and residual_out is None:
+
+
+def _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales):
+    eps = float(eps)
+    # the ordinary call, seen through in a few comparisons; any other takes the checks one by one
+    try:
+        shape = x.shape
+        d, dev = shape[-1], x.get_device()
+        lead = shape[:-1]
+        ok = (out is None and scales is None and residual_out is None and dev >= 0 and 8 <= d <= 65536 and d % 8 == 0
+              and eps >= 0.0 and x.is_contiguous() and gain.is_contiguous() and gain.get_device() == dev
+              and gain.dim() == 2 and gain.shape[0] >= 1 and gain.shape[1] == d
+              and (residual is None or (residual.shape == shape and residual.is_contiguous()
+                                        and residual.get_device() == dev and residual.dtype in _IN))
+              and (variant_ids is None or (variant_ids.shape == lead and variant_ids.dtype == torch.int32
+                                           and variant_ids.is_contiguous() and variant_ids.get_device() == dev))
+              and x.dtype in _IN and gain.dtype in _IN)
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        _refuse_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales)
+    lib = _declared or _library()
+    x_type = _IN[x.dtype]
+    res_type = BD_BF16
+    if residual is not None:
+        res_type = _IN[residual.dtype]
+        if residual_out is None:
             residual_out = torch.empty_like(residual)
-        st = lib.bd_rms_norm(x.data_ptr(), x_type, _at(residual), _at(residual_out), res_type, gain.data_ptr(),
-                             gain_type, num_gains, _at(variant_ids), eps, out.data_ptr(), out_type, _at(scales), M,
-                             d, torch.cuda.current_stream(x.device).cuda_stream)
+    if out is None:
+        if out_type != BD_BF16:
+            out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        elif x_type == BD_BF16:
+            out = torch.empty_like(x)
+        elif residual is not None and res_type == BD_BF16:
+            out = torch.empty_like(residual)
+        else:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    if out_type != BD_BF16 and scales is None:
+        scales = torch.empty((*lead, (d + 31) // 32), dtype=torch.uint8, device=x.device)
+    st = lib.bd_rms_norm(x.data_ptr(), x_type, residual.data_ptr() if residual is not None else None,
+                         residual_out.data_ptr() if residual is not None else None, res_type, gain.data_ptr(),
+                         _IN[gain.dtype], gain.shape[0] if gain.dim() == 2 else 1,
+                         variant_ids.data_ptr() if variant_ids is not None else None, eps, out.data_ptr(), out_type,
+                         scales.data_ptr() if scales is not None else None, math.prod(lead), d, _stream_of(dev))
+    if st:
         _check(lib, "bd_rms_norm", st)
     return out, scales, residual_out
 
@@ -242,7 +274,7 @@ class bd_kv_cache:
             raise ValueError("k and v overlap")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.num_pages, self.num_heads, self.page_size, self.head_dim = pages, heads, page, dim
-        self.device = k.device
+        self.device, self._dev = k.device, k.get_device()
         self._desc = _KV(k.data_ptr(), v.data_ptr(), _at(k_scales), _at(v_scales), kind, heads, dim, page, pages,
                          *stride[:3])
         self._ref = ctypes.addressof(self._desc)
@@ -270,6 +302,16 @@ class bd_kv_cache:
 
 def _rows(name, t, kv_heads, dim):
     """(type, strides) of [n, heads, dim] rows with any token and head stride."""
+    try:
+        n, heads, last = t.shape
+        a, b, c = t.stride()
+        kind = _IN[t.dtype]
+        if last == dim and (heads == kv_heads or kv_heads is None) and c == 1 and n > 1 and heads > 1:
+            unit = 7 if kind == BD_BF16 else 3   # elements of 16 bytes, less one
+            if not (a | b) & unit and not t.data_ptr() & 15:
+                return kind, _Pair(a, b)
+    except (AttributeError, KeyError, ValueError):
+        pass
     kind = _typed(name, t, _IN)
     if t.dim() != 3 or (kv_heads is not None and t.shape[1] != kv_heads) or t.shape[2] != dim:
         raise ValueError("%s must be [n, %s, %d] (got %s)" % (name, kv_heads or "num_q_heads", dim, tuple(t.shape)))
@@ -289,51 +331,86 @@ def _rows(name, t, kv_heads, dim):
 def _cache(kv):
     if not isinstance(kv, bd_kv_cache):
         raise TypeError("kv must be a bd_kv_cache")
-    return kv
+
+
+def _index(name, t, n, dev):
+    """Whether t is an int32 [n] index on the device, as it nearly always is."""
+    return (type(t) is torch.Tensor and t.dtype == torch.int32 and t.shape == (n,) and t.is_contiguous()
+            and t.get_device() == dev)
 
 
 def bd_kv_write(kv: bd_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
     """Writes the rows k, v [T, num_heads, head_dim] (bf16 or fp32, any token and head strides) of T tokens into the
     cache's slots (int32 [T]; slot = page · page_size + place).  Slots below 0 or past the cache's end are skipped; of
     several tokens with one slot the last stays."""
-    lib = _library()
     _cache(kv)
     kind, ks = _rows("k", k, kv.num_heads, kv.head_dim)
     v_kind, vs = _rows("v", v, kv.num_heads, kv.head_dim)
-    if v_kind != kind or v.shape[0] != k.shape[0]:
+    T, dev = k.shape[0], kv._dev
+    if v_kind != kind or v.shape[0] != T:
         raise ValueError("k and v must have one dtype and one number of tokens")
-    T = k.shape[0]
-    _plain("slots", slots, torch.int32, (T,))
-    _same_gpu(kv.device, (("k", k), ("v", v), ("slots", slots)))
-    with _on(kv.device):
-        st = lib.bd_kv_write(kv._ref, k.data_ptr(), ks, v.data_ptr(), vs, kind, slots.data_ptr(), T,
-                             torch.cuda.current_stream(kv.device).cuda_stream)
+    if not (_index("slots", slots, T, dev) and k.get_device() == dev and v.get_device() == dev):
+        _plain("slots", slots, torch.int32, (T,))
+        _same_gpu(kv.device, (("k", k), ("v", v), ("slots", slots)))
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return bd_kv_write(kv, k, v, slots)
+    lib = _declared or _library()
+    st = lib.bd_kv_write(kv._ref, k.data_ptr(), ks, v.data_ptr(), vs, kind, slots.data_ptr(), T, _stream_of(dev))
+    if st:
         _check(lib, "bd_kv_write", st)
 
 
 def bd_kv_read(kv: bd_kv_cache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
     """The rows of T slots (int32 [T]) as bf16 (k, v), each [T, num_heads, head_dim], exactly as held.  Slots below 0
     give zeros, slots past the cache's end NaN."""
-    lib = _library()
     _cache(kv)
     _tensor("slots", slots)
-    shape = (slots.numel(), kv.num_heads, kv.head_dim)
-    _plain("slots", slots, torch.int32, shape[:1])
-    if out is not None:
-        for name, t in zip(("out[0]", "out[1]"), out):
+    dev, n = kv._dev, slots.numel()
+    shape = (n, kv.num_heads, kv.head_dim)
+    if out is not None or not _index("slots", slots, n, dev):
+        _plain("slots", slots, torch.int32, shape[:1])
+        given = [] if out is None else list(zip(("out[0]", "out[1]"), out, strict=True))
+        for name, t in given:
             _plain(name, t, torch.bfloat16, shape)
-        if slots.numel() and _overlap(*out):
+        if given and n and _overlap(*out):
             raise ValueError("out[0] overlaps out[1]")
-        _same_gpu(kv.device, (("slots", slots), ("out[0]", out[0]), ("out[1]", out[1])))
+        _same_gpu(kv.device, [("slots", slots)] + given)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return bd_kv_read(kv, slots, out)
+    lib = _declared or _library()
+    if out is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=kv.device)
+        v = torch.empty_like(k)
     else:
-        _same_gpu(kv.device, (("slots", slots),))
-    with _on(kv.device):
-        k, v = out if out is not None else (torch.empty(shape, dtype=torch.bfloat16, device=kv.device)
-                                            for _ in range(2))
-        st = lib.bd_kv_read(kv._ref, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
-                            torch.cuda.current_stream(kv.device).cuda_stream)
+        k, v = out
+    st = lib.bd_kv_read(kv._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _stream_of(dev))
+    if st:
         _check(lib, "bd_kv_read", st)
     return k, v
+
+
+def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
+    """The checks of an attention's tensors, in full; raises or returns."""
+    B = q.shape[0]
+    if heads < 1 or heads > 65535 or heads % kv.num_heads:
+        raise ValueError("q's heads must be a multiple of the cache's %d, at most 65535 (got %d)" % (kv.num_heads, heads))
+    _tensor("page_table", page_table)
+    if page_table.dtype != torch.int32:
+        raise TypeError("page_table must be torch.int32 (got %s)" % page_table.dtype)
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1:
+        raise ValueError("page_table must be [%d, max_pages] (got %s)" % (B, tuple(page_table.shape)))
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table's rows must be contiguous")
+    if page_table.shape[1] * kv.page_size > 1 << 24:
+        raise ValueError("page_table holds more than 2^24 tokens per sequence")
+    _plain("lengths", lengths, torch.int32, (B,))
+    if out is not None:
+        _plain("out", out, torch.bfloat16, (B, heads, kv.head_dim))
+    if lse is not None:
+        _plain("lse", lse, torch.float32, (B, heads))
+    _same_gpu(kv.device, (("q", q), ("page_table", page_table), ("lengths", lengths), ("out", out), ("lse", lse)))
 
 
 def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -344,38 +421,38 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     heads.  page_table int32 [B, max_pages] (rows may be strided) and lengths int32 [B] say which tokens: lengths
     counts the new one, whose row is in the cache by then.  A length of 0 gives zeros.  scale defaults to
     head_dim^-0.5.  lse, if given, is an fp32 [B, num_q_heads] tensor that receives the log of the softmax's sum."""
-    lib = _library()
     _cache(kv)
     kind, qs = _rows("q", q, None, kv.head_dim)
-    B, heads = q.shape[0], q.shape[1]
-    if heads < 1 or heads > 65535 or heads % kv.num_heads:
-        raise ValueError("q's heads must be a multiple of the cache's %d, at most 65535 (got %d)" % (kv.num_heads, heads))
-    _tensor("page_table", page_table)
-    if page_table.dtype != torch.int32:
-        raise TypeError("page_table must be torch.int32 (got %s)" % page_table.dtype)
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.shape[1] < 1:
-        raise ValueError("page_table must be [%d, max_pages] (got %s)" % (B, tuple(page_table.shape)))
-    most = page_table.shape[1]
-    if most > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table's rows must be contiguous")
-    if most * kv.page_size > 1 << 24:
-        raise ValueError("page_table holds more than 2^24 tokens per sequence")
-    _plain("lengths", lengths, torch.int32, (B,))
+    B, heads, _ = q.shape
+    dev = kv._dev
     scale = kv.head_dim ** -0.5 if scale is None else float(scale)
     if not math.isfinite(scale):
         raise ValueError("scale must be finite (got %r)" % scale)
-    if out is not None:
-        _plain("out", out, torch.bfloat16, (B, heads, kv.head_dim))
-    if lse is not None:
-        _plain("lse", lse, torch.float32, (B, heads))
-    _same_gpu(kv.device, (("q", q), ("page_table", page_table), ("lengths", lengths), ("out", out), ("lse", lse)))
-    nbytes = lib.bd_attend_workspace_bytes(B, heads, kv.num_heads, kv.head_dim, kv.page_size, most)
-    with _on(kv.device):
-        if out is None:
-            out = torch.empty((B, heads, kv.head_dim), dtype=torch.bfloat16, device=kv.device)
-        ws = _workspace(nbytes, kv.device)
-        st = lib.bd_attend(kv._ref, q.data_ptr(), kind, qs, heads, page_table.data_ptr(),
-                           page_table.stride(0) if B > 1 else 0, most, lengths.data_ptr(), B, scale, out.data_ptr(),
-                           _at(lse), _at(ws), nbytes, torch.cuda.current_stream(kv.device).cuda_stream)
+    if not (out is None and lse is None and type(page_table) is torch.Tensor and page_table.dim() == 2
+            and page_table.dtype == torch.int32 and page_table.shape[0] == B and page_table.is_contiguous()
+            and 1 <= page_table.shape[1] <= (1 << 24) // kv.page_size and page_table.get_device() == dev
+            and _index("lengths", lengths, B, dev) and q.get_device() == dev and 1 <= heads <= 65535
+            and heads % kv.num_heads == 0):
+        _refuse_attend(q, kv, page_table, lengths, out, lse, heads)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return bd_attend(q, kv, page_table, lengths, scale, out, lse)
+    lib = _declared or _library()
+    pages = page_table.shape[1]
+    nbytes = _attend_bytes(B, heads, kv.num_heads, kv.head_dim, kv.page_size, pages)
+    if out is None:
+        out = torch.empty((B, heads, kv.head_dim), dtype=torch.bfloat16, device=kv.device)
+    ws = _workspace(nbytes, kv.device)
+    st = lib.bd_attend(kv._ref, q.data_ptr(), kind, qs, heads, page_table.data_ptr(),
+                       page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, out.data_ptr(),
+                       lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None, nbytes,
+                       _stream_of(dev))
+    if st:
         _check(lib, "bd_attend", st)
     return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _attend_bytes(*sizes):
+    """The library's answer for these sizes: a host function of nothing else."""
+    return _library().bd_attend_workspace_bytes(*sizes)

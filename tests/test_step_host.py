@@ -171,7 +171,7 @@ def _pretend():
     """What the calls' checks read of a bd_kv_cache, on the host."""
     kv = object.__new__(bd.bd_kv_cache)
     kv.num_pages, kv.num_heads, kv.page_size, kv.head_dim = 6, 2, 16, 64
-    kv.device = torch.device("cpu")
+    kv.device, kv._dev = torch.device("cpu"), 0
     return kv
 
 
