@@ -49,6 +49,7 @@ struct Shape {
     int32_t group, tiles;                       // query heads per kv head, and tiles of 16 of them
     int32_t rows;                               // rows of units per sequence: heads * tiles
     int32_t capacity, groups;                   // tokens a table row holds; workgroups launched
+    int32_t crosses, by_row;                    // entries of the workspace's table
 };
 
 struct Args {
@@ -86,13 +87,6 @@ struct Line {
         first = inc - sum;
         total = __shfl(inc, 63, 64);
     }
-    // The first unit of sequence b.
-    __device__ __forceinline__ int start_of(const Args& p, int b) const {
-        const int l = b / n;
-        int u = uni(__shfl(first, l, 64));
-        for (int i = l * n; i < b; ++i) u += units_of(p.a.lengths[i], p.s.capacity) * p.s.rows;
-        return u;
-    }
     // The sequence that holds unit u, and its first unit.
     __device__ __forceinline__ int holder_of(const Args& p, int u, int* start) const {
         const int lane = threadIdx.x & 63;
@@ -127,11 +121,22 @@ struct Cut {
     }
 };
 
-// Partial results in the workspace: each workgroup has two places (the first
-// row it works on and the last one), each of 16 heads' (maximum, sum) and
-// unnormalised outputs.
-__device__ __forceinline__ int64_t place(int w, int which, int dim) {
-    return ((int64_t)w * 2 + which) * (16 * (dim + 2));
+// The workspace: a table of Cross, then each workgroup's partial results, two
+// places (the first row it works on and the last one) of 16 heads' (maximum,
+// sum) and unnormalised outputs.
+//
+// Cross: a row of units that starts in one workgroup and goes on in the next
+// ones.  The table has an entry per row of the batch where these are fewer
+// than the workgroups, else one per workgroup (in which at most one such row
+// starts); each is written in every call.
+struct Cross {
+    int32_t at;     // b * rows + row
+    int32_t first;  // the workgroup it starts in, times 2, plus its place there; -1: all of it is in one workgroup
+    int32_t last;   // the workgroup it ends in
+    int32_t pad;
+};
+__device__ __forceinline__ float* place(const Args& p, int w, int which) {
+    return p.a.part + (int64_t)p.s.crosses * 4 + ((int64_t)w * 2 + which) * (16 * (p.s.dim + 2));
 }
 
 // Page lookups: token group g8 (8 tokens, which no page boundary cuts) of a
@@ -159,18 +164,21 @@ template <int N>
 struct Dwords {
     uint32_t d[N];
 };
+// The cache is read once: streaming loads (against plain ones, 64 sequences of
+// 8192 tokens in e4m3 187 -> 173 us, 4 of 131072 in bf16 365 -> 334).
 template <int N>
 __device__ __forceinline__ Dwords<N> load_dwords(const void* p) {
     Dwords<N> r;
     if constexpr (N == 1) {
-        r.d[0] = *static_cast<const uint32_t*>(p);
+        r.d[0] = *static_cast<const uint32_t*>(p);  // rows of half a cache line, whose other half comes next
     } else if constexpr (N == 2) {
-        const uint2 v = *static_cast<const uint2*>(p);
+        typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+        const u32x2_t v = __builtin_nontemporal_load(static_cast<const u32x2_t*>(p));
         r.d[0] = v.x, r.d[1] = v.y;
     } else {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
-            const uint4 v = static_cast<const uint4*>(p)[i];
+            const uint4 v = load_stream16(static_cast<const uint4*>(p) + i);
             r.d[4 * i] = v.x, r.d[4 * i + 1] = v.y, r.d[4 * i + 2] = v.z, r.d[4 * i + 3] = v.w;
         }
     }
@@ -185,7 +193,7 @@ __device__ __forceinline__ void clear(Dwords<N>& r) {
 // kDC: head_dim rounded up to 64, 128 or 256.  kFull: head_dim is kDC.
 // kSplitQ: fp32 queries as two bf16 terms.
 template <int kDC, bool kFull, bool kE4m3, bool kSplitQ>
-__global__ __launch_bounds__(kWaves * 64) void attend_kernel(const Args p) {
+__global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel(const Args p) {
     constexpr int NS = kDC / 32;              // k-steps of a score product
     constexpr int DV = kDC / 16;              // value columns of a lane
     constexpr int KL = kE4m3 ? NS / 2 : NS;   // 16-byte loads of a key row per lane
@@ -200,6 +208,9 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(const Args p) {
     line.scan(p);
     const Cut cut(line.total, p.s.groups);
     const int w = blockIdx.x;
+    Cross* crosses = reinterpret_cast<Cross*>(p.a.part);
+    const bool by_row = p.s.by_row;
+    if (!by_row && crosses && threadIdx.x == 0) crosses[w].first = -1;
     if (w >= cut.W) return;
     int u = cut.start(w);
     const int end = cut.start(w + 1);
@@ -251,26 +262,31 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(const Args p) {
 
         const int32_t* table = p.a.table + b * p.a.table_stride;
         const int last8 = tokens > 0 ? (tokens - 1) >> 3 : 0;
-    again:
-#pragma unroll
-        for (int j = 0; j < DV; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        m = kNegInf, mm = 0.0f, l = 0.0f;
-#pragma nounroll
-        for (int t = unit * kUnit + wave * kTile; t < stop; t += kUnit) {
-            // this lane's token groups: of its key rows, of its value rows
-            int gk = (t >> 3) + (i16 >> 2), gv = (t >> 3) + g;
-            gk = gk < last8 ? gk : last8;
-            gv = gv < last8 ? gv : last8;
-            const int ik = page_index(p.s, gk), iv = page_index(p.s, gv);
-            const Where wk = locate(p, gk, ik, table[ik], head);
-            const Where wv = locate(p, gv, iv, table[iv], head);
-            bad |= wk.bad | wv.bad;
+        const int t0 = unit * kUnit + wave * kTile;
 
-            Dwords<4> kk[2][KL];
-            float ks[2];
+        // A tile's loads, in flight while the tile before it is worked on:
+        // the page numbers a tile earlier, the keys as soon as the scores are
+        // done with the registers, the values after the sums.
+        Dwords<4> kk[2][KL];
+        Dwords<VD> vv[8];
+        float ks[2];
+        uint2 vs;
+        int pk, pv;  // page numbers of the lane's key rows and value rows
+        const auto group_of = [&](int t, int add) {
+            const int g8 = (t >> 3) + add;
+            return g8 < last8 ? g8 : last8;
+        };
+        const auto load_pages = [&](int t) {
+            pk = table[page_index(p.s, group_of(t, i16 >> 2))];
+            pv = table[page_index(p.s, group_of(t, g))];
+        };
+        const auto load_keys = [&](int t) {
+            const int g8 = group_of(t, i16 >> 2);
+            const Where w = locate(p, g8, page_index(p.s, g8), pk, head);
+            bad |= w.bad;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t at = wk.at + ((i16 & 3) + 4 * h) * p.a.kv.token_stride;
+                const int64_t at = w.at + ((i16 & 3) + 4 * h) * p.a.kv.token_stride;
 #pragma unroll
                 for (int s = 0; s < KL; ++s) {
                     const int d = kE4m3 ? s * 64 + g * 16 : s * 32 + g * 8;
@@ -278,19 +294,36 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(const Args p) {
                     if (kFull || d < p.s.dim)
                         kk[h][s] = load_dwords<4>(static_cast<const char*>(p.a.kv.k) + (at + d) * (kE4m3 ? 1 : 2));
                 }
-                if (kE4m3) ks[h] = scale_of(p.a.kv.k_scales[wk.sc + (i16 & 3) + 4 * h]);
+                if (kE4m3) ks[h] = scale_of(p.a.kv.k_scales[w.sc + (i16 & 3) + 4 * h]);
             }
-            Dwords<VD> vv[8];
-            uint2 vs;
+        };
+        const auto load_values = [&](int t) {
+            const int g8 = group_of(t, g);
+            const Where w = locate(p, g8, page_index(p.s, g8), pv, head);
+            bad |= w.bad;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 clear(vv[j]);
                 if (kFull || i16 * DV < p.s.dim)
                     vv[j] = load_dwords<VD>(static_cast<const char*>(p.a.kv.v) +
-                                            (wv.at + j * p.a.kv.token_stride + i16 * DV) * (kE4m3 ? 1 : 2));
+                                            (w.at + j * p.a.kv.token_stride + i16 * DV) * (kE4m3 ? 1 : 2));
             }
-            if (kE4m3) vs = *reinterpret_cast<const uint2*>(p.a.kv.v_scales + wv.sc);
+            if (kE4m3) vs = *reinterpret_cast<const uint2*>(p.a.kv.v_scales + w.sc);
+        };
 
+    again:
+#pragma unroll
+        for (int j = 0; j < DV; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        m = kNegInf, mm = 0.0f, l = 0.0f;
+        if (t0 < stop) {
+            load_pages(t0);
+            load_keys(t0);
+            load_values(t0);
+            load_pages(t0 + kUnit);  // past the end: the last group's page
+        }
+#pragma nounroll
+        for (int t = t0; t < stop; t += kUnit) {
+            const bool more = t + kUnit < stop;
             // scores of tokens t + 8 g + j, head i16
             float sc[8];
 #pragma unroll
@@ -313,6 +346,7 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(const Args p) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sc[4 * h + r] = x[r] * c;
             }
+            if (more) load_keys(t + kUnit);
             const bool tail = t + kTile > tokens;
             if (tail) {
 #pragma unroll
@@ -386,6 +420,10 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(const Args p) {
                 acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, as_bf16x8(pl), acc[j], 0, 0, 0);
                 acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, as_bf16x8(ph), acc[j], 0, 0, 0);
             }
+            if (more) {
+                load_values(t + kUnit);
+                load_pages(t + 2 * kUnit);
+            }
         }
 
         // A second term breaks on infinities: it is of either sign or zero,
@@ -449,7 +487,11 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(const Args p) {
 
         const bool whole = n == un;
         const int d4 = p.s.dim / 4;
-        float* part = whole ? nullptr : p.a.part + place(w, first_row ? 0 : 1, p.s.dim);
+        float* part = whole ? nullptr : place(p, w, first_row ? 0 : 1);
+        if (unit == 0 && crosses && threadIdx.x == 0 && (by_row || !whole)) {
+            const int at = b * p.s.rows + row;
+            crosses[by_row ? at : w] = Cross{at, whole ? -1 : w * 2 + (first_row ? 0 : 1), cut.group_of(u + un - 1), 0};
+        }
         for (int i = threadIdx.x; i < nq * d4; i += kWaves * 64) {
             const int q = i / d4, d = (i - q * d4) * 4;
             float M = sm[0][q];
@@ -488,61 +530,68 @@ __global__ __launch_bounds__(kWaves * 64) void attend_kernel(const Args p) {
     }
 }
 
+// Adds a partial result (maximum m, sum l, unnormalised output x) to a running
+// one.  A part whose scores are all -infinity has sum and output 0 (or NaN).
+__device__ __forceinline__ void add_part(float& M, float& L, float4& o, float m, float l, float4 x) {
+    const float to = fmaxf(M, m);
+    const float f = M == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(M - to);
+    const float g = m == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+    M = to;
+    L = L * f + l * g;
+    o.x = o.x * f + x.x * g, o.y = o.y * f + x.y * g, o.z = o.z * f + x.z * g, o.w = o.w * f + x.w * g;
+}
+
 // Rows of units that several workgroups worked on: out = sum of their partial
-// outputs over the sum of their sums, each scaled to the common maximum.  One
-// workgroup per (row, query head of the row).
+// outputs over the sum of their sums, each scaled to the common maximum.  The
+// heads of a row are shared out over grid y.
 __global__ __launch_bounds__(256) void join_kernel(const Args p) {
     __shared__ float4 red[256];
-    Line line;
-    line.scan(p);
-    const Cut cut(line.total, p.s.groups);
-    const int b = blockIdx.x / p.s.rows, row = blockIdx.x - b * p.s.rows;
+    __shared__ float redm[256], redl[256];
+    const Cross cross = reinterpret_cast<const Cross*>(p.a.part)[blockIdx.x];
+    if (cross.first < 0) return;
+    const int w0 = cross.first >> 1, w1 = cross.last, which0 = cross.first & 1;
+    const int b = cross.at / p.s.rows, row = cross.at - b * p.s.rows;
     const int head = row / p.s.tiles, q0 = (row - head * p.s.tiles) * 16;
-    const int q = blockIdx.y;
-    if (q >= p.s.group - q0) return;
-    const int un = units_of(uni(p.a.lengths[b]), p.s.capacity);
-    const int u0 = line.start_of(p, b) + row * un;
-    const int w0 = cut.group_of(u0), w1 = cut.group_of(u0 + un - 1);
-    if (w0 == w1) return;  // written by its one workgroup
-    const int which0 = cut.start(w0) >= u0 ? 0 : 1;
-
-    float M = kNegInf;
-    for (int w = w0 + (int)(threadIdx.x & 63); w <= w1; w += 64)
-        M = fmaxf(M, p.a.part[place(w, w == w0 ? which0 : 0, p.s.dim) + 2 * q]);
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-
-    const int lanes = p.s.dim / 4;          // lanes of one partial result, 4 values each
-    const int sets = 256 / lanes;           // partial results at a time
-    const int set = threadIdx.x / lanes, d = (threadIdx.x - set * lanes) * 4;
-    float4 o = make_float4(0, 0, 0, 0);
-    float L = 0.0f;
-    if (set < sets) {
+    const int nq = p.s.group - q0 < 16 ? p.s.group - q0 : 16;
+    // this workgroup's heads, and its work: 4 values of one head per item
+    const int qa = nq * (int)blockIdx.y / (int)gridDim.y, qe = nq * ((int)blockIdx.y + 1) / (int)gridDim.y;
+    const int lanes = p.s.dim / 4, items = (qe - qa) * lanes;
+    // lanes beyond the items take every sets-th partial result
+    const int sets = items >= 256 ? 1 : items > 0 ? 256 / items : 1;
+    const int set = (int)threadIdx.x / (items < 256 && items > 0 ? items : 256);
+    for (int i0 = 0; i0 < items; i0 += 256) {
+        const int i = sets > 1 ? (int)threadIdx.x - set * items : i0 + (int)threadIdx.x;
+        const int q = qa + i / lanes, d = i % lanes * 4;
+        float4 o = make_float4(0, 0, 0, 0);
+        float M = kNegInf, L = 0.0f;
+        if (i < items && set < sets) {
 #pragma unroll 4
-        for (int w = w0 + set; w <= w1; w += sets) {
-            const float* part = p.a.part + place(w, w == w0 ? which0 : 0, p.s.dim);
-            const float m = part[2 * q], l = part[2 * q + 1];
-            const float4 x = *reinterpret_cast<const float4*>(part + 32 + q * p.s.dim + d);
-            const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - M);
-            L += m == kNegInf ? l : l * f;
-            o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
+            for (int w = w0 + set; w <= w1; w += sets) {
+                const float* part = place(p, w, w == w0 ? which0 : 0);
+                const float2 ml = *reinterpret_cast<const float2*>(part + 2 * q);
+                const float4 x = *reinterpret_cast<const float4*>(part + 32 + q * p.s.dim + d);
+                add_part(M, L, o, ml.x, ml.y, x);
+            }
+        }
+        if (sets > 1) {
+            redm[threadIdx.x] = M;
+            redl[threadIdx.x] = L;
+            red[threadIdx.x] = o;
+            __syncthreads();
+            if (set == 0)
+                for (int k = 1; k < sets; ++k) {
+                    const int at = k * items + (int)threadIdx.x;
+                    add_part(M, L, o, redm[at], redl[at], red[at]);
+                }
+        }
+        if (set == 0 && i < items) {
+            const float inv = 1.0f / L;
+            const int64_t at = (int64_t)b * p.a.Hq + head * p.s.group + q0 + q;
+            *reinterpret_cast<uint2*>(p.a.out + at * p.s.dim + d) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (p.a.lse && d == 0) p.a.lse[at] = (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
         }
     }
-    __shared__ float redl[256];
-    red[threadIdx.x] = o;
-    redl[threadIdx.x] = L;
-    __syncthreads();
-    if (set != 0) return;
-    for (int i = 1; i < sets; ++i) {
-        const float4 x = red[i * lanes + threadIdx.x];
-        o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
-        L += redl[i * lanes + threadIdx.x];
-    }
-    const float inv = 1.0f / L;
-    const int64_t at = (int64_t)b * p.a.Hq + head * p.s.group + q0 + q;
-    *reinterpret_cast<uint2*>(p.a.out + at * p.s.dim + d) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (p.a.lse && d == 0) p.a.lse[at] = (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
 }
 
 Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages) {
@@ -563,6 +612,8 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     // a capacity of one unit splits nothing: a workgroup per row of units
     const int64_t most = per_row == 1 ? int64_t(1) << 20 : kGroups;
     s.groups = (int32_t)(units < most ? units : most);
+    s.by_row = B * s.rows <= s.groups;
+    s.crosses = s.by_row ? (int32_t)(B * s.rows) : s.groups;
     return s;
 }
 
@@ -586,7 +637,8 @@ void go(const Args& p, bool q_fp32, hipStream_t s) {
 
 size_t attend_workspace_bytes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages) {
     if (page_size * max_pages <= kUnit) return 0;
-    return (size_t)shape_of(B, Hq, H, D, page_size, max_pages).groups * 2 * 16 * (D + 2) * sizeof(float);
+    const Shape s = shape_of(B, Hq, H, D, page_size, max_pages);
+    return (size_t)s.crosses * sizeof(Cross) + (size_t)s.groups * 2 * 16 * (D + 2) * sizeof(float);
 }
 
 hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
@@ -611,8 +663,11 @@ hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.s.capacity <= kUnit) return e;
-    const unsigned nq = (unsigned)(p.s.group < 16 ? p.s.group : 16);
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)(a.B * p.s.rows), nq), dim3(256), 0, stream, p);
+    // about two workgroups per CU: a row's heads on as many as that leaves
+    const int nq = p.s.group < 16 ? p.s.group : 16;
+    const int per = kGroups / p.s.crosses < 1 ? 1 : kGroups / p.s.crosses;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)p.s.crosses, (unsigned)(nq < per ? nq : per)), dim3(256), 0, stream,
+                       p);
     return hipGetLastError();
 }
 
