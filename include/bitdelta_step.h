@@ -86,8 +86,8 @@ bd_status bd_rms_norm(const void* x, int32_t x_type, const void* residual, void*
  *   page_size  a multiple of 8, 8 .. 4096.
  *   num_heads  1 .. 65535.
  *   head_dim   a multiple of 16, 16 .. 256.
- *   strides    in elements, >= 0, multiples of 16 bytes; distinct rows must
- *              not overlap.  k, v: 16-byte aligned.
+ *   strides    in elements, >= 0, multiples of 16 bytes and below 2^36 bytes;
+ *              distinct rows must not overlap.  k, v: 16-byte aligned.
  * The struct is read during the call only.
  * ------------------------------------------------------------------------- */
 typedef struct bd_kv {

@@ -29,7 +29,8 @@
 // query heads), four waves with a tile each.  The units of the whole batch
 // lie in one line, which the workgroups share out evenly, whatever the
 // lengths: every workgroup works the line up from the device's lengths by
-// itself.  A row of units that ends up in several workgroups leaves fp32
+// itself.  The loads of a tile are in flight while the one before it is worked
+// on, across the ends of rows too.  A row of units that ends up in several workgroups leaves fp32
 // partial results (sum, maximum, unnormalised output) in the workspace, and
 // join_kernel adds them in workgroup order.
 #include "step_internal.h"
@@ -40,7 +41,18 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 32;                  // tokens of a wave
 constexpr int kUnit = kWaves * kTile;      // tokens of a unit
-constexpr int kGroups = 512;               // workgroups at most: two per CU
+// Workgroups at most: what 256 CUs hold of them by their registers and LDS, so
+// that all start at once.  Three per CU at head_dim 64 (against two, 31
+// sequences of 4000 tokens, 32 heads, e4m3: 135 -> 117 us), two at 128 (with
+// 768 of them for 512 places, 64 of 8192 tokens in e4m3 173 -> 230 us), one at
+// 256.
+constexpr int kCUs = 256;
+constexpr int per_cu(int dim) { return dim <= 64 ? 3 : dim <= 128 ? 2 : 1; }
+// What a row costs beside its units, in units.  Without it the workgroups that
+// get many short rows come last: 64 sequences of up to 16381 tokens in e4m3
+// 187 -> 178 us, 31 of up to 1013 with 32 key-value heads 27.7 -> 22.7 (16 of
+// up to 4099 in bf16 28.9 -> 30.0).
+constexpr int kRowCost = 2;
 constexpr float kLazy = 10.0f;             // log2: how far a score may pass the running maximum
 constexpr float kNegInf = -__builtin_inff();
 
@@ -55,7 +67,11 @@ struct Shape {
 struct Args {
     AttendArgs a;
     Shape s;
-    float c;  // scale * log2(e)
+    uint32_t pages;                         // of the cache
+    uint32_t page16, head16, token16;       // its strides in units of 16 bytes
+    uint32_t page_scales;                   // scale bytes of a page
+    float c;                                // |scale| log2(e)
+    uint32_t flip;                          // the queries' sign bits where scale is negative
 };
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -66,17 +82,18 @@ __device__ __forceinline__ int units_of(int len, int capacity) {
     return len <= kUnit || len > capacity ? 1 : (len + kUnit - 1) / kUnit;
 }
 
-// The batch's line of units, worked out by each wave: lane l sums the
-// sequences [l n, l n + n).
+// The batch's line of places, worked out by each wave: a row has kRowCost of
+// them for its start and end (queries, sums over the waves, outputs) and one
+// for each of its units.  Lane l sums the sequences [l n, l n + n).
 struct Line {
-    int n, first, total;  // per lane: sequences, units before its own; units of the batch
+    int n, first, total;  // per lane: sequences, places before its own; places of the batch
     __device__ __forceinline__ void scan(const Args& p) {
         const int lane = threadIdx.x & 63;
         n = (p.a.B + 63) / 64;
         int sum = 0;
         const int b0 = lane * n;
         for (int i = 0; i < n; ++i)
-            if (b0 + i < p.a.B) sum += units_of(p.a.lengths[b0 + i], p.s.capacity);
+            if (b0 + i < p.a.B) sum += kRowCost + units_of(p.a.lengths[b0 + i], p.s.capacity);
         sum *= p.s.rows;
         int inc = sum;
 #pragma unroll
@@ -85,9 +102,9 @@ struct Line {
             if (lane >= off) inc += o;
         }
         first = inc - sum;
-        total = __shfl(inc, 63, 64);
+        total = uni(__shfl(inc, 63, 64));
     }
-    // The sequence that holds unit u, and its first unit.
+    // The sequence that holds place u, and its first place.
     __device__ __forceinline__ int holder_of(const Args& p, int u, int* start) const {
         const int lane = threadIdx.x & 63;
         // the last lane that has sequences and starts at or before u
@@ -96,7 +113,7 @@ struct Line {
         int s = uni(__shfl(first, l, 64));
         int b = l * n;
         for (;;) {
-            const int len = units_of(p.a.lengths[b], p.s.capacity) * p.s.rows;
+            const int len = (kRowCost + units_of(p.a.lengths[b], p.s.capacity)) * p.s.rows;
             if (u < s + len || b + 1 >= p.a.B) break;
             s += len;
             ++b;
@@ -106,7 +123,9 @@ struct Line {
     }
 };
 
-// Workgroup w of W takes the units [start(w), start(w + 1)).
+// Workgroup w of W takes the places [start(w), start(w + 1)).  A row's units
+// before place u are those of its places before u, less kRowCost: what is cut
+// within a row's cost starts with the row's first unit.
 struct Cut {
     int W, q, r;
     __device__ __forceinline__ Cut(int total, int groups) {
@@ -130,7 +149,7 @@ struct Cut {
 // than the workgroups, else one per workgroup (in which at most one such row
 // starts); each is written in every call.
 struct Cross {
-    int32_t at;     // b * rows + row
+    int32_t id;     // b * rows + row
     int32_t first;  // the workgroup it starts in, times 2, plus its place there; -1: all of it is in one workgroup
     int32_t last;   // the workgroup it ends in
     int32_t pad;
@@ -140,23 +159,26 @@ __device__ __forceinline__ float* place(const Args& p, int w, int which) {
 }
 
 // Page lookups: token group g8 (8 tokens, which no page boundary cuts) of a
-// sequence lies in page table[g8 / pg8].
+// sequence lies in page table[g8 / pg8], at group g8 % pg8 of it.
+struct Group {
+    int page, in_page;
+};
+__device__ __forceinline__ Group look_up(const Shape& s, const int32_t* table, int g8) {
+    // exact: g8 < 2^21, pg8 <= 2^9
+    const uint32_t idx = __umulhi((uint32_t)g8, (uint32_t)s.magic) + (s.pg8 == 1 ? g8 : 0);
+    return Group{table[idx], g8 - (int)__umul24(idx, (uint32_t)s.pg8)};
+}
 struct Where {
-    int64_t at;  // element of the group's first token in the cache's arrays
-    int64_t sc;  // its scale byte
+    uint64_t at;  // byte of the group's first token in the cache's arrays
+    uint64_t sc;  // its scale byte
     bool bad;
 };
-__device__ __forceinline__ int page_index(const Shape& s, int g8) {
-    // exact: g8 < 2^21, pg8 <= 2^9
-    return (int)__umulhi((uint32_t)g8, (uint32_t)s.magic) + (s.pg8 == 1 ? g8 : 0);
-}
-__device__ __forceinline__ Where locate(const Args& p, int g8, int idx, int page, int head) {
+__device__ __forceinline__ Where locate(const Args& p, Group x, int head) {
     Where w;
-    w.bad = page < 0 || page >= p.a.kv.num_pages;
-    page = w.bad ? 0 : page;
-    const int at = (g8 - idx * p.s.pg8) * 8;
-    w.at = page * p.a.kv.page_stride + head * p.a.kv.head_stride + at * p.a.kv.token_stride;
-    w.sc = ((int64_t)page * p.s.heads + head) * p.s.page_size + at;
+    w.bad = (uint32_t)x.page >= p.pages;
+    const uint32_t page = w.bad ? 0u : (uint32_t)x.page, at = (uint32_t)x.in_page * 8;
+    w.at = ((uint64_t)page * p.page16 + ((uint64_t)at * p.token16 + (uint64_t)(uint32_t)head * p.head16)) * 16;
+    w.sc = (uint64_t)page * p.page_scales + ((uint32_t)head * (uint32_t)p.s.page_size + at);
     return w;
 }
 
@@ -190,17 +212,21 @@ __device__ __forceinline__ void clear(Dwords<N>& r) {
     for (int i = 0; i < N; ++i) r.d[i] = 0;
 }
 
+__device__ __forceinline__ void flip(uint4& v, uint32_t mask) { v.x ^= mask, v.y ^= mask, v.z ^= mask, v.w ^= mask; }
+
 // kDC: head_dim rounded up to 64, 128 or 256.  kFull: head_dim is kDC.
 // kSplitQ: fp32 queries as two bf16 terms.
 template <int kDC, bool kFull, bool kE4m3, bool kSplitQ>
-__global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel(const Args p) {
+__global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const Args p) {
     constexpr int NS = kDC / 32;              // k-steps of a score product
     constexpr int DV = kDC / 16;              // value columns of a lane
     constexpr int KL = kE4m3 ? NS / 2 : NS;   // 16-byte loads of a key row per lane
     constexpr int VD = kE4m3 ? DV / 4 : DV / 2;  // dwords of a value row per lane
+    constexpr int kSize = kE4m3 ? 1 : 2;      // bytes of a held value
     constexpr int kPad = kDC + 4;
-    __shared__ float so[kWaves][16][kPad];
-    __shared__ float sm[kWaves][16], sl[kWaves][16];
+    // two of each, used in turn by the rows: one barrier a row
+    __shared__ float so[2][kWaves][16][kPad];
+    __shared__ float sm[2][kWaves][16], sl[2][kWaves][16];
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
@@ -212,115 +238,169 @@ __global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel
     const bool by_row = p.s.by_row;
     if (!by_row && crosses && threadIdx.x == 0) crosses[w].first = -1;
     if (w >= cut.W) return;
-    int u = cut.start(w);
+    const int u = cut.start(w);
     const int end = cut.start(w + 1);
-    int seq_start;
-    int b = line.holder_of(p, u, &seq_start);
-    int len = uni(p.a.lengths[b]);
-    int un = units_of(len, p.s.capacity);
-    int row = (u - seq_start) / un;
-    int unit = u - seq_start - row * un;
-    bool first_row = true;
+    int at;  // the current row's first place
+    const int b0 = line.holder_of(p, u, &at);
 
-    while (u < end) {
-        const int n = un - unit < end - u ? un - unit : end - u;
-        const int head = row / p.s.tiles;
-        const int q0 = (row - head * p.s.tiles) * 16;  // the tile's first query head of the group
-        const int nq = p.s.group - q0 < 16 ? p.s.group - q0 : 16;
-        const int hq0 = head * p.s.group + q0;
-        const bool too_long = len > p.s.capacity;
-        const int tokens = too_long || len < 0 ? 0 : len;
-        const int stop = tokens < (unit + n) * kUnit ? tokens : (unit + n) * kUnit;
+    // The part of a row of units that this workgroup works on.
+    struct Piece {
+        int b, row, unit, n, un;     // sequence, its row, first unit, units here, units of the row
+        int len, tokens, t0, stop;   // length as given and as used; this wave's first tile, its tokens' end
+        int head, q0, nq;            // key-value head; first query head of its group, and how many
+    };
+    const auto piece_at = [&](int b, int len, int row, int unit, int row_at) {
+        Piece x;
+        x.b = b, x.row = row, x.unit = unit, x.len = len;
+        x.un = units_of(len, p.s.capacity);
+        const int upto = end - row_at - kRowCost;  // of its units, as far as this workgroup goes
+        x.n = (upto < x.un ? upto : x.un) - unit;
+        x.tokens = len > p.s.capacity || len < 0 ? 0 : len;
+        x.t0 = unit * kUnit + wave * kTile;
+        x.stop = x.tokens < (unit + x.n) * kUnit ? x.tokens : (unit + x.n) * kUnit;
+        x.head = row / p.s.tiles;
+        x.q0 = (row - x.head * p.s.tiles) * 16;
+        x.nq = p.s.group - x.q0 < 16 ? p.s.group - x.q0 : 16;
+        return x;
+    };
+    const int len0 = uni(p.a.lengths[b0]);
+    const int span0 = kRowCost + units_of(len0, p.s.capacity), row0 = (u - at) / span0;
+    at += row0 * span0;
+    if (at + kRowCost >= end) return;  // no unit of its own
+    const int into = u - at - kRowCost;
+    Piece now = piece_at(b0, len0, row0, into > 0 ? into : 0, at);
+    bool first_piece = true;
 
-        // queries: B operand, column i16, k = the head's values in the order
-        // in which the key loads bring them
-        uint4 qh[NS], ql[NS];
+    // A tile's loads, in flight while the tile before it is worked on: the
+    // page numbers a tile earlier, the keys as soon as the scores are done
+    // with the registers, the values after the sums.  A row's first tile and
+    // its queries are loaded while the row before it is summed up.
+    Dwords<4> kk[2][KL];
+    Dwords<VD> vv[8];
+    float ks[2];
+    uint2 vs;
+    Raw8<kSplitQ> raw[NS];
+    bool bad = false;
+    const auto group_of = [&](const Piece& x, int t, int add) {
+        const int g8 = (t >> 3) + add, last = (x.tokens - 1) >> 3;
+        return g8 < last ? g8 : last;
+    };
+    // where the lane's key rows and value rows are
+    struct Groups {
+        Group k, v;
+    };
+    const auto load_pages = [&](const Piece& x, int t) {
+        const int32_t* table = p.a.table + x.b * p.a.table_stride;
+        return Groups{look_up(p.s, table, group_of(x, t, i16 >> 2)), look_up(p.s, table, group_of(x, t, g))};
+    };
+    const uint64_t token_bytes = (uint64_t)p.token16 * 16;
+    const auto load_keys = [&](const Piece& x, Group at_page) {
+        const Where wh = locate(p, at_page, x.head);
+        bad |= wh.bad;
+        // one address, stepped by uniform strides, so that no per-row address
+        // stays in registers
+        uint64_t at = opaque(wh.at + (uint64_t)(i16 & 3) * token_bytes + g * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int s = 0; s < KL; ++s) {
+                clear(kk[h][s]);
+                if (kFull || (s * 64 + g * 16) / kSize < p.s.dim)
+                    kk[h][s] = load_dwords<4>(static_cast<const char*>(p.a.kv.k) + at + s * 64);
+            }
+            at += 4 * token_bytes;
+            if (kE4m3) ks[h] = scale_of(p.a.kv.k_scales[wh.sc + (i16 & 3) + 4 * h]);
+        }
+    };
+    const auto load_values = [&](const Piece& x, Group at_page) {
+        const Where wh = locate(p, at_page, x.head);
+        bad |= wh.bad;
+        uint64_t at = opaque(wh.at + i16 * DV * kSize);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            clear(vv[j]);
+            if (kFull || i16 * DV < p.s.dim) vv[j] = load_dwords<VD>(static_cast<const char*>(p.a.kv.v) + at);
+            at += token_bytes;
+        }
+        if (kE4m3) vs = *reinterpret_cast<const uint2*>(p.a.kv.v_scales + wh.sc);
+    };
+    // queries: B operand, column i16, k = the head's values in the order in
+    // which the key loads bring them
+    const auto load_queries = [&](const Piece& x) {
+        const int64_t at = x.b * p.a.qs.token + (x.head * p.s.group + x.q0 + i16) * p.a.qs.head;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             const int d = kE4m3 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
-            float f[8];
-            Raw8<kSplitQ> raw;
-            raw.zero();
-            if (i16 < nq && (kFull || d < p.s.dim)) raw.load(p.a.q, b * p.a.qs.token + (hq0 + i16) * p.a.qs.head + d);
-            raw.widen(f);
-            qh[s] = narrow_bf16x8(f);
-            if (kSplitQ) {
-                float back[8];
+            raw[s].zero();
+            if (i16 < x.nq && (kFull || d < p.s.dim)) raw[s].load(p.a.q, at + d);
+        }
+    };
+
+    const auto drop = [&]() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < KL; ++s) clear(kk[h][s]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) clear(vv[j]);
+        ks[0] = ks[1] = 0.0f;
+        vs = make_uint2(0, 0);
+    };
+
+    Groups pages{};  // of the tile after the one in flight
+    drop();
+    load_queries(now);
+    if (now.t0 < now.stop) {
+        pages = load_pages(now, now.t0);
+        load_keys(now, pages.k);
+        load_values(now, pages.v);
+        pages = load_pages(now, now.t0 + kUnit);  // past the end: the last group's page
+    }
+
+    for (int turn = 0;; turn ^= 1) {
+        const int t0 = now.t0, stop = now.stop, nq = now.nq, tokens = now.tokens;
+        // what comes next, and its first page numbers
+        const int next_at = at + kRowCost + now.un;
+        const bool last = next_at + kRowCost >= end;
+        Piece next = now;
+        Groups next_pages{};
+        if (!last) {
+            const bool turn_over = now.row + 1 == p.s.rows;
+            const int nb = now.b + turn_over;
+            const int nlen = turn_over ? uni(p.a.lengths[nb]) : now.len;
+            next = piece_at(nb, nlen, turn_over ? 0 : now.row + 1, 0, next_at);
+            if (next.t0 < next.stop) next_pages = load_pages(next, next.t0);
+        }
+
+        uint4 qh[NS], ql[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            if constexpr (kSplitQ) {
+                float f[8], back[8];
+                raw[s].widen(f);
+                qh[s] = narrow_bf16x8(f);
                 widen_bf16x8(qh[s], back);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] -= back[j];
                 ql[s] = narrow_bf16x8(f);
+            } else {
+                qh[s] = raw[s].a;
             }
+            flip(qh[s], p.flip);
+            if constexpr (kSplitQ) flip(ql[s], p.flip);
+            raw[s].zero();  // not kept through the tiles
         }
 
         f32x4_t acc[DV];
         float m, mm, l;  // mm: m, or 0 while m is -infinity
-        bool bad = false;
         float c = p.c;
         int pass = 0;  // 1: again, see below
         bool lost = false;
-
-        const int32_t* table = p.a.table + b * p.a.table_stride;
-        const int last8 = tokens > 0 ? (tokens - 1) >> 3 : 0;
-        const int t0 = unit * kUnit + wave * kTile;
-
-        // A tile's loads, in flight while the tile before it is worked on:
-        // the page numbers a tile earlier, the keys as soon as the scores are
-        // done with the registers, the values after the sums.
-        Dwords<4> kk[2][KL];
-        Dwords<VD> vv[8];
-        float ks[2];
-        uint2 vs;
-        int pk, pv;  // page numbers of the lane's key rows and value rows
-        const auto group_of = [&](int t, int add) {
-            const int g8 = (t >> 3) + add;
-            return g8 < last8 ? g8 : last8;
-        };
-        const auto load_pages = [&](int t) {
-            pk = table[page_index(p.s, group_of(t, i16 >> 2))];
-            pv = table[page_index(p.s, group_of(t, g))];
-        };
-        const auto load_keys = [&](int t) {
-            const int g8 = group_of(t, i16 >> 2);
-            const Where w = locate(p, g8, page_index(p.s, g8), pk, head);
-            bad |= w.bad;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t at = w.at + ((i16 & 3) + 4 * h) * p.a.kv.token_stride;
-#pragma unroll
-                for (int s = 0; s < KL; ++s) {
-                    const int d = kE4m3 ? s * 64 + g * 16 : s * 32 + g * 8;
-                    clear(kk[h][s]);
-                    if (kFull || d < p.s.dim)
-                        kk[h][s] = load_dwords<4>(static_cast<const char*>(p.a.kv.k) + (at + d) * (kE4m3 ? 1 : 2));
-                }
-                if (kE4m3) ks[h] = scale_of(p.a.kv.k_scales[w.sc + (i16 & 3) + 4 * h]);
-            }
-        };
-        const auto load_values = [&](int t) {
-            const int g8 = group_of(t, g);
-            const Where w = locate(p, g8, page_index(p.s, g8), pv, head);
-            bad |= w.bad;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                clear(vv[j]);
-                if (kFull || i16 * DV < p.s.dim)
-                    vv[j] = load_dwords<VD>(static_cast<const char*>(p.a.kv.v) +
-                                            (w.at + j * p.a.kv.token_stride + i16 * DV) * (kE4m3 ? 1 : 2));
-            }
-            if (kE4m3) vs = *reinterpret_cast<const uint2*>(p.a.kv.v_scales + w.sc);
-        };
 
     again:
 #pragma unroll
         for (int j = 0; j < DV; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         m = kNegInf, mm = 0.0f, l = 0.0f;
-        if (t0 < stop) {
-            load_pages(t0);
-            load_keys(t0);
-            load_values(t0);
-            load_pages(t0 + kUnit);  // past the end: the last group's page
-        }
 #pragma nounroll
         for (int t = t0; t < stop; t += kUnit) {
             const bool more = t + kUnit < stop;
@@ -344,9 +424,9 @@ __global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel
                     x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kb), as_bf16x8(qh[s]), x, 0, 0, 0);
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sc[4 * h + r] = x[r] * c;
+                for (int r = 0; r < 4; ++r) sc[4 * h + r] = x[r];
             }
-            if (more) load_keys(t + kUnit);
+            if (more) load_keys(now, pages.k);
             const bool tail = t + kTile > tokens;
             if (tail) {
 #pragma unroll
@@ -366,6 +446,7 @@ __global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel
             float mx = sc[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) mx = fmaxf(mx, sc[j]);
+            mx *= c;
             if (__ballot(mx > m + kLazy)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
                 mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
@@ -381,7 +462,8 @@ __global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel
             float pr[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                pr[j] = __builtin_amdgcn_exp2f(sc[j] - mm);
+                pr[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j], c, -mm));
+                if (tail) pr[j] = t + 8 * g + j >= tokens ? 0.0f : pr[j];  // also where c is 0
                 l += pr[j];
             }
             const uint4 ph = narrow_bf16x8(pr);
@@ -421,8 +503,8 @@ __global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel
                 acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, as_bf16x8(ph), acc[j], 0, 0, 0);
             }
             if (more) {
-                load_values(t + kUnit);
-                load_pages(t + 2 * kUnit);
+                load_values(now, pages.v);
+                pages = load_pages(now, t + 2 * kUnit);
             }
         }
 
@@ -439,7 +521,7 @@ __global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel
                 for (int r = 0; r < 4; ++r) z = __builtin_fmaf(acc[j][r], 0.0f, z);
             if (__ballot(i16 < nq && (z != 0.0f || l != l))) {
                 lost = kSplitQ && __ballot(i16 < nq && l != l);
-                float* keep = &so[wave][0][0] + lane;
+                float* keep = &so[turn][wave][0][0] + lane;
 #pragma unroll
                 for (int j = 0; j < DV; ++j)
 #pragma unroll
@@ -450,10 +532,14 @@ __global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel
                     c *= 0.5f;
                 }
                 pass = 1;
+                pages = load_pages(now, t0);
+                load_keys(now, pages.k);
+                load_values(now, pages.v);
+                pages = load_pages(now, t0 + kUnit);
                 goto again;
             }
         } else {
-            const float* keep = &so[wave][0][0] + lane;
+            const float* keep = &so[turn][wave][0][0] + lane;
 #pragma unroll
             for (int j = 0; j < DV; ++j)
 #pragma unroll
@@ -463,70 +549,71 @@ __global__ __launch_bounds__(kWaves * 64, kDC == 256 ? 1 : 2) void attend_kernel
                 }
         }
 
+        const bool was_bad = __ballot(bad) != 0 || now.len > p.s.capacity;
+        bad = false;
+        if (!last) load_queries(next);
+        if (!last && next.t0 < next.stop) {
+            load_keys(next, next_pages.k);
+            load_values(next, next_pages.v);
+            pages = load_pages(next, next.t0 + kUnit);
+        } else {  // nothing is kept in these registers from here
+            drop();
+        }
+
         // the wave's result, then the workgroup's: heads i16, values
         // (4 g + r) DV + j of acc[j][r]
         l += __shfl_xor(l, 16, 64);
         l += __shfl_xor(l, 32, 64);
-        if (__ballot(bad) || too_long) l = __builtin_nanf("");
-        if (lane < 16) sm[wave][i16] = m, sl[wave][i16] = l;
-        __syncthreads();
-        float top = sm[0][i16];
-#pragma unroll
-        for (int v = 1; v < kWaves; ++v) top = fmaxf(top, sm[v][i16]);
-        const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+        if (was_bad) l = __builtin_nanf("");
+        if (lane < 16) sm[turn][wave][i16] = m, sl[turn][wave][i16] = l;
         if (i16 < nq) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int j = 0; j < DV; j += 4) {
-                    float4 o = make_float4(acc[j][r] * f, acc[j + 1][r] * f, acc[j + 2][r] * f, acc[j + 3][r] * f);
-                    *reinterpret_cast<float4*>(&so[wave][i16][(4 * g + r) * DV + j]) = o;
-                }
+                for (int j = 0; j < DV; j += 4)
+                    *reinterpret_cast<float4*>(&so[turn][wave][i16][(4 * g + r) * DV + j]) =
+                        make_float4(acc[j][r], acc[j + 1][r], acc[j + 2][r], acc[j + 3][r]);
         }
         __syncthreads();
 
-        const bool whole = n == un;
+        const bool whole = now.n == now.un;
+        const int which = first_piece ? 0 : 1;
         const int d4 = p.s.dim / 4;
-        float* part = whole ? nullptr : place(p, w, first_row ? 0 : 1);
-        if (unit == 0 && crosses && threadIdx.x == 0 && (by_row || !whole)) {
-            const int at = b * p.s.rows + row;
-            crosses[by_row ? at : w] = Cross{at, whole ? -1 : w * 2 + (first_row ? 0 : 1), cut.group_of(u + un - 1), 0};
+        float* part = whole ? nullptr : place(p, w, which);
+        if (now.unit == 0 && crosses && threadIdx.x == 0 && (by_row || !whole)) {
+            const int id = now.b * p.s.rows + now.row;
+            crosses[by_row ? id : w] = Cross{id, whole ? -1 : w * 2 + which, cut.group_of(next_at - 1), 0};
         }
         for (int i = threadIdx.x; i < nq * d4; i += kWaves * 64) {
             const int q = i / d4, d = (i - q * d4) * 4;
-            float M = sm[0][q];
-#pragma unroll
-            for (int v = 1; v < kWaves; ++v) M = fmaxf(M, sm[v][q]);
-            float L = 0.0f;
+            float M = kNegInf, L = 0.0f;
             float4 o = make_float4(0, 0, 0, 0);
 #pragma unroll
+            for (int v = 0; v < kWaves; ++v) M = fmaxf(M, sm[turn][v][q]);
+#pragma unroll
             for (int v = 0; v < kWaves; ++v) {
-                // a wave without tokens has sum 0 (or NaN where a page was bad)
-                L += sl[v][q] * (sm[v][q] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(sm[v][q] - M));
-                const float4 x = *reinterpret_cast<const float4*>(&so[v][q][d]);
-                o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+                // a wave without tokens has sum and output 0 (or a NaN sum where a page was bad)
+                const float f = sm[turn][v][q] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(sm[turn][v][q] - M);
+                const float4 x = *reinterpret_cast<const float4*>(&so[turn][v][q][d]);
+                L += sl[turn][v][q] * f;
+                o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
             }
             if (whole) {
-                const float inv = len <= 0 ? 0.0f : 1.0f / L;
-                const int64_t at = (int64_t)b * p.a.Hq + hq0 + q;
+                const float inv = now.len <= 0 ? 0.0f : 1.0f / L;
+                const int64_t at = (int64_t)now.b * p.a.Hq + now.head * p.s.group + now.q0 + q;
                 *reinterpret_cast<uint2*>(p.a.out + at * p.s.dim + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-                if (p.a.lse && d == 0) p.a.lse[at] = len <= 0 ? kNegInf : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+                if (p.a.lse && d == 0)
+                    p.a.lse[at] = now.len <= 0 ? kNegInf : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
             } else {
                 *reinterpret_cast<float4*>(part + 32 + q * p.s.dim + d) = o;
                 if (d == 0) part[2 * q] = M, part[2 * q + 1] = L;
             }
         }
-        first_row = false;
-        u += n;
-        unit = 0;
-        if (u < end && ++row == p.s.rows) {
-            row = 0;
-            ++b;
-            len = uni(p.a.lengths[b]);
-            un = units_of(len, p.s.capacity);
-        }
-        __syncthreads();
+        if (last) break;
+        at = next_at;
+        now = next;
+        first_piece = false;
     }
 }
 
@@ -550,7 +637,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
     const Cross cross = reinterpret_cast<const Cross*>(p.a.part)[blockIdx.x];
     if (cross.first < 0) return;
     const int w0 = cross.first >> 1, w1 = cross.last, which0 = cross.first & 1;
-    const int b = cross.at / p.s.rows, row = cross.at - b * p.s.rows;
+    const int b = cross.id / p.s.rows, row = cross.id - b * p.s.rows;
     const int head = row / p.s.tiles, q0 = (row - head * p.s.tiles) * 16;
     const int nq = p.s.group - q0 < 16 ? p.s.group - q0 : 16;
     // this workgroup's heads, and its work: 4 values of one head per item
@@ -608,9 +695,9 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     s.rows = s.heads * s.tiles;
     s.capacity = (int32_t)(page_size * max_pages);
     const int64_t per_row = s.capacity <= kUnit ? 1 : (s.capacity + kUnit - 1) / kUnit;
-    const int64_t units = B * s.rows * per_row;
+    const int64_t units = B * s.rows * (per_row == 1 ? 1 : per_row + kRowCost);
     // a capacity of one unit splits nothing: a workgroup per row of units
-    const int64_t most = per_row == 1 ? int64_t(1) << 20 : kGroups;
+    const int64_t most = per_row == 1 ? int64_t(1) << 20 : kCUs * per_cu((int)D);
     s.groups = (int32_t)(units < most ? units : most);
     s.by_row = B * s.rows <= s.groups;
     s.crosses = s.by_row ? (int32_t)(B * s.rows) : s.groups;
@@ -642,8 +729,11 @@ size_t attend_workspace_bytes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64
 }
 
 hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
+    const auto unit16 = [&](int64_t stride) { return (uint32_t)(stride * (a.kv.type == BD_E4M3 ? 1 : 2) / 16); };
     Args p{a, shape_of(a.B, a.Hq, a.kv.num_heads, a.kv.head_dim, a.kv.page_size, a.max_pages),
-           a.scale * 1.4426950408889634f};
+           (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride), unit16(a.kv.token_stride),
+           (uint32_t)(a.kv.num_heads * a.kv.page_size), __builtin_fabsf(a.scale) * 1.4426950408889634f,
+           a.scale < 0.0f ? 0x80008000u : 0u};
     const int D = a.kv.head_dim;
     if (D <= 64) {
         if (D == 64)
@@ -665,7 +755,7 @@ hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
     if (e != hipSuccess || p.s.capacity <= kUnit) return e;
     // about two workgroups per CU: a row's heads on as many as that leaves
     const int nq = p.s.group < 16 ? p.s.group : 16;
-    const int per = kGroups / p.s.crosses < 1 ? 1 : kGroups / p.s.crosses;
+    const int per = 2 * kCUs / p.s.crosses < 1 ? 1 : 2 * kCUs / p.s.crosses;
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)p.s.crosses, (unsigned)(nq < per ? nq : per)), dim3(256), 0, stream,
                        p);
     return hipGetLastError();

@@ -29,7 +29,7 @@ bd_status check_kv(const bd_kv* kv) {
         return BD_ERR_SHAPE;
     const int64_t unit = kv->type == BD_E4M3 ? 16 : 8;  // elements of 16 bytes
     for (const int64_t s : {kv->page_stride, kv->head_stride, kv->token_stride}) {
-        if (s < 0) return BD_ERR_SHAPE;
+        if (s < 0 || s / unit >= int64_t(1) << 32) return BD_ERR_SHAPE;
         if (s % unit != 0) return BD_ERR_ALIGN;
     }
     if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return BD_ERR_ALIGN;
@@ -53,7 +53,7 @@ bool attend_shape(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size
     if (max_pages < 1 || max_pages > bd::kAttendMaxTokens / page_size) return false;
     const int64_t rows = B * H * ((Hq / H + 15) / 16);  // of units of 128 tokens
     const int64_t units = (max_pages * page_size + 127) / 128;
-    return rows <= int64_t(1) << 23 && units * rows <= int64_t(1) << 30;
+    return rows <= int64_t(1) << 23 && (units + 4) * rows <= int64_t(1) << 30;
 }
 
 }  // namespace
