@@ -300,6 +300,30 @@ def test_kv_slots_out_of_range_and_named_twice(bd):
         c.check()
 
 
+@pytest.mark.parametrize("T,start", [(4096, 1), (4097, 2), (9001, 3), (70001, 1), (300001, 0)])
+def test_kv_write_many_with_repeats(bd, T, start):
+    """Long calls with many slots named again, near and far, from slot arrays at any 4-byte border."""
+    page, pages = 16, T // 24 + 3
+    kv = bd.bd_kv_cache.empty(pages, 1, page, 16, BF, DEV)
+    kv.k.zero_(), kv.v.zero_()
+    gen = gen_of(T)
+    slots = torch.randint(-2, pages * page + 2, (T + start,), generator=gen).to(torch.int32)
+    slots[start + 5:start + 40] = slots[start + 3]
+    k = torch.arange(T).float().view(T, 1, 1).expand(T, 1, 16)
+    # token numbers in two exact bf16 parts
+    hi, lo = (torch.div(k, 256, rounding_mode="floor") * 1.0).to(BF), (k % 256).to(BF)
+    bd.bd_kv_write(kv, hi.contiguous().to(DEV), lo.contiguous().to(DEV), slots.to(DEV)[start:])
+    want = np.full(pages * page, -1, np.int64)
+    own = slots[start:].numpy()
+    ok = (own >= 0) & (own < pages * page)
+    want[own[ok]] = np.arange(T)[ok]          # the last assignment stays
+    got_hi = kv.k.float().cpu().numpy()[:, 0].reshape(-1, 16)
+    got_lo = kv.v.float().cpu().numpy()[:, 0].reshape(-1, 16)
+    w_hi = torch.from_numpy(np.where(want < 0, 0, want // 256)).float().to(BF).float().numpy()
+    w_lo = np.where(want < 0, 0, want % 256)
+    assert (got_hi == w_hi[:, None]).all() and (got_lo == w_lo[:, None]).all()
+
+
 def test_kv_values(bd):
     """Ties, borders of the scale, signed zeros, subnormals, the largest numbers, NaN and infinities."""
     dim = 32
