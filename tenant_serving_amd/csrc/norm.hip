@@ -19,9 +19,17 @@ namespace {
 template <int NT>
 constexpr int kNormBlock = NT == 64 ? 256 : NT;
 
+// x and a bf16 residual are loaded streaming from this many bytes of them on,
+// as little of them can still be in the 256 MiB last-level cache then: 2048 x
+// 28672 of bf16 94 -> 82 us (5.7 TB/s), 8192 x 8192 with fp32 x 118 -> 106; below,
+// what the linear just wrote is found there (2048 x 8192 with fp32 x, 100 MB,
+// 29.6 against 30.8 us).  With an fp32 residual plain loads stay ahead (8192 x
+// 8192 to e4m3 135 against 141), without one they are level.
+constexpr int64_t kStreamBytes = int64_t(192) << 20;
+
 // kRes: 0 no residual, 1 bf16, 2 fp32.  NT lanes own a row (64: four rows to a
 // workgroup, one per wave), C chunks of 8 values each.
-template <bool kX32, int kRes, bool kE4m3, int NT, int C>
+template <bool kX32, int kRes, bool kE4m3, bool kStream, int NT, int C>
 __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, int64_t row0) {
     const int tid = NT == 64 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
     const int64_t row = row0 + (NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x);
@@ -40,8 +48,11 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
         xr[c].zero();
         rr[c].zero();
         if (e < a.d) {
-            xr[c].load(a.x, base + e);
-            if (kRes) rr[c].load(a.residual, base + e);
+            if (kStream)
+                xr[c].load_stream(a.x, base + e), rr[c].load_stream(a.residual, base + e);
+            else
+                xr[c].load(a.x, base + e);
+            if (kRes && !kStream) rr[c].load(a.residual, base + e);
         }
     }
     if (!a.gain_fp32) {
@@ -129,33 +140,40 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
     }
 }
 
-template <bool kX32, int kRes, bool kE4m3, int NT, int C>
+template <bool kX32, int kRes, bool kE4m3, bool kStream, int NT, int C>
 void go(const NormArgs& a, hipStream_t s) {
     constexpr int64_t most = int64_t(1) << 21;  // rows of one launch: its threads number below 2^32
     for (int64_t row0 = 0; row0 < a.M; row0 += most) {
         const int64_t n = a.M - row0 < most ? a.M - row0 : most;
         const unsigned grid = (unsigned)(NT == 64 ? (n + 3) / 4 : n);
-        hipLaunchKernelGGL((norm_kernel<kX32, kRes, kE4m3, NT, C>), dim3(grid), dim3(kNormBlock<NT>), 0, s, a, row0);
+        hipLaunchKernelGGL((norm_kernel<kX32, kRes, kE4m3, kStream, NT, C>), dim3(grid), dim3(kNormBlock<NT>), 0, s, a, row0);
     }
 }
 
-template <bool kX32, int kRes, bool kE4m3>
+template <bool kX32, int kRes, bool kE4m3, bool kStream>
 void pick(const NormArgs& a, hipStream_t s) {
-    if (a.d <= 512) return go<kX32, kRes, kE4m3, 64, 1>(a, s);
-    if (a.d <= 2048) return go<kX32, kRes, kE4m3, 256, 1>(a, s);
-    if (a.d <= 4096) return go<kX32, kRes, kE4m3, 256, 2>(a, s);
-    if (a.d <= 8192) return go<kX32, kRes, kE4m3, 256, 4>(a, s);
-    if (a.d <= 16384) return go<kX32, kRes, kE4m3, 1024, 2>(a, s);
-    if (a.d <= 32768) return go<kX32, kRes, kE4m3, 1024, 4>(a, s);
-    return go<kX32, kRes, kE4m3, 1024, 8>(a, s);
+    if (a.d <= 512) return go<kX32, kRes, kE4m3, kStream, 64, 1>(a, s);
+    if (a.d <= 2048) return go<kX32, kRes, kE4m3, kStream, 256, 1>(a, s);
+    if (a.d <= 4096) return go<kX32, kRes, kE4m3, kStream, 256, 2>(a, s);
+    if (a.d <= 8192) return go<kX32, kRes, kE4m3, kStream, 256, 4>(a, s);
+    if (a.d <= 16384) return go<kX32, kRes, kE4m3, kStream, 1024, 2>(a, s);
+    if (a.d <= 32768) return go<kX32, kRes, kE4m3, kStream, 1024, 4>(a, s);
+    return go<kX32, kRes, kE4m3, kStream, 1024, 8>(a, s);
 }
 
 template <bool kX32, int kRes>
 void pick_out(const NormArgs& a, bool e4m3, hipStream_t s) {
+    if constexpr (kRes == 1) {
+        if (a.M * a.d * (kX32 ? 6 : 4) >= kStreamBytes) {
+            if (e4m3)
+                return pick<kX32, kRes, true, true>(a, s);
+            return pick<kX32, kRes, false, true>(a, s);
+        }
+    }
     if (e4m3)
-        pick<kX32, kRes, true>(a, s);
+        pick<kX32, kRes, true, false>(a, s);
     else
-        pick<kX32, kRes, false>(a, s);
+        pick<kX32, kRes, false, false>(a, s);
 }
 
 template <bool kX32>

@@ -120,6 +120,9 @@ struct Raw8<false> {
     __device__ __forceinline__ void load(const void* p, int64_t i) {
         a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
     }
+    __device__ __forceinline__ void load_stream(const void* p, int64_t i) {
+        a = load_stream16(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+    }
     __device__ __forceinline__ void widen(float* f) const { widen_bf16x8(a, f); }
 };
 template <>
@@ -130,6 +133,11 @@ struct Raw8<true> {
         const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
         a = q[0];
         b = q[1];
+    }
+    __device__ __forceinline__ void load_stream(const void* p, int64_t i) {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        a = load_stream16(q);
+        b = load_stream16(q + 1);
     }
     __device__ __forceinline__ void widen(float* f) const {
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;

@@ -164,6 +164,25 @@ def test_norm_many_rows(bd):
         check_bf16(y[at:at + 1], want, 8)
 
 
+@pytest.mark.parametrize("x_t,d", [(BF, 28672), (F32, 8192), (BF, 512), (BF, 2056)])
+def test_norm_large(bd, x_t, d):
+    """Inputs beyond the last-level cache, which are loaded another way, against the same rows in a small call."""
+    M = (200 << 20) // (d * (6 if x_t == F32 else 4)) + 3
+    g = torch.Generator(device=DEV).manual_seed(d)
+    x = torch.randn((M, d), generator=g, device=DEV, dtype=x_t)
+    res = torch.randn((M, d), generator=g, device=DEV, dtype=BF)
+    gain = torch.randn((2, d), generator=g, device=DEV).to(BF)
+    ids = torch.arange(M, device=DEV, dtype=torch.int32) % 2
+    y, r = bd.bd_rms_norm(x, gain, residual=res, variant_ids=ids)
+    c, s, r2 = bd.bd_rms_norm_e4m3(x, gain, residual=res, variant_ids=ids)
+    for a in (0, M // 2, M - 16):
+        part = slice(a, a + 16)
+        y2, r3 = bd.bd_rms_norm(x[part], gain, residual=res[part], variant_ids=ids[part])
+        c2, s2, _ = bd.bd_rms_norm_e4m3(x[part], gain, residual=res[part], variant_ids=ids[part])
+        assert same_bits(y[part], y2) and same_bits(r[part], r3) and same_bits(r2[part], r3)
+        assert same_bits(c[part], c2) and same_bits(s[part], s2)
+
+
 # ----------------------------------------------------------------------------
 # the cache
 
