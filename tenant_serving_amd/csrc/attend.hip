@@ -44,10 +44,11 @@ constexpr int kUnit = kWaves * kTile;      // tokens of a unit
 // Workgroups at most: what 256 CUs hold of them by their registers and LDS, so
 // that all start at once.  Three per CU at head_dim 64 (against two, 31
 // sequences of 4000 tokens, 32 heads, e4m3: 135 -> 117 us), two at 128 (with
-// 768 of them for 512 places, 64 of 8192 tokens in e4m3 173 -> 230 us), one at
-// 256.
+// 768 of them for 512 places, 64 of 8192 tokens in e4m3 173 -> 230 us).  At 256
+// the registers of two spill but for e4m3 with bf16 queries (8 of 16384 tokens,
+// head_dim 192, 110 -> 81 us; in bf16, 8 of 8192, two would take 86 -> 107).
 constexpr int kCUs = 256;
-constexpr int per_cu(int dim) { return dim <= 64 ? 3 : dim <= 128 ? 2 : 1; }
+constexpr int per_cu(int dim, bool split_q, bool e4m3) { return dim <= 64 ? 3 : dim <= 128 || (e4m3 && !split_q) ? 2 : 1; }
 // What a row costs beside its units, in units.  Without it the workgroups that
 // get many short rows come last: 64 sequences of up to 16381 tokens in e4m3
 // 187 -> 178 us, 31 of up to 1013 with 32 key-value heads 27.7 -> 22.7 (16 of
@@ -217,16 +218,22 @@ __device__ __forceinline__ void flip(uint4& v, uint32_t mask) { v.x ^= mask, v.y
 // kDC: head_dim rounded up to 64, 128 or 256.  kFull: head_dim is kDC.
 // kSplitQ: fp32 queries as two bf16 terms.
 template <int kDC, bool kFull, bool kE4m3, bool kSplitQ>
-__global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const Args p) {
+__global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void attend_kernel(const Args p) {
     constexpr int NS = kDC / 32;              // k-steps of a score product
     constexpr int DV = kDC / 16;              // value columns of a lane
     constexpr int KL = kE4m3 ? NS / 2 : NS;   // 16-byte loads of a key row per lane
     constexpr int VD = kE4m3 ? DV / 4 : DV / 2;  // dwords of a value row per lane
     constexpr int kSize = kE4m3 ? 1 : 2;      // bytes of a held value
     constexpr int kPad = kDC + 4;
-    // two of each, used in turn by the rows: one barrier a row
-    __shared__ float so[2][kWaves][16][kPad];
-    __shared__ float sm[2][kWaves][16], sl[2][kWaves][16];
+    // Two of each, used in turn by the rows: one barrier a row.  At head_dim
+    // 256 with e4m3 and bf16 queries one, and the queries in LDS instead of
+    // registers, or a CU would hold one workgroup instead of two.
+    constexpr bool kTight = kDC == 256 && per_cu(kDC, kSplitQ, kE4m3) == 2;
+    constexpr int kTurns = kTight ? 1 : 2;
+    __shared__ float so[kTurns][kWaves][16][kPad];
+    __shared__ float sm[kTurns][kWaves][16], sl[kTurns][kWaves][16];
+    __shared__ uint4 sq[kTight ? (kSplitQ ? 2 : 1) : 1][kTight ? NS : 1][64];
+    constexpr int NR = kTight ? NS / kWaves : NS;  // k-steps whose queries a wave loads
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
@@ -279,7 +286,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
     Dwords<VD> vv[8];
     float ks[2];
     uint2 vs;
-    Raw8<kSplitQ> raw[NS];
+    Raw8<kSplitQ> raw[NR];
     bool bad = false;
     const auto group_of = [&](const Piece& x, int t, int add) {
         const int g8 = (t >> 3) + add, last = (x.tokens - 1) >> 3;
@@ -329,10 +336,11 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
     const auto load_queries = [&](const Piece& x) {
         const int64_t at = x.b * p.a.qs.token + (x.head * p.s.group + x.q0 + i16) * p.a.qs.head;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
+        for (int i = 0; i < NR; ++i) {
+            const int s = kTight ? i * kWaves + wave : i;
             const int d = kE4m3 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
-            raw[s].zero();
-            if (i16 < x.nq && (kFull || d < p.s.dim)) raw[s].load(p.a.q, at + d);
+            raw[i].zero();
+            if (i16 < x.nq && (kFull || d < p.s.dim)) raw[i].load(p.a.q, at + d);
         }
     };
 
@@ -357,7 +365,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
         pages = load_pages(now, now.t0 + kUnit);  // past the end: the last group's page
     }
 
-    for (int turn = 0;; turn ^= 1) {
+    for (int turn = 0;; turn ^= kTurns - 1) {
         const int t0 = now.t0, stop = now.stop, nq = now.nq, tokens = now.tokens;
         // what comes next, and its first page numbers
         const int next_at = at + kRowCost + now.un;
@@ -372,9 +380,9 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
             if (next.t0 < next.stop) next_pages = load_pages(next, next.t0);
         }
 
-        uint4 qh[NS], ql[NS];
+        uint4 qh[NR], ql[NR];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
+        for (int s = 0; s < NR; ++s) {
             if constexpr (kSplitQ) {
                 float f[8], back[8];
                 raw[s].widen(f);
@@ -389,7 +397,12 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
             flip(qh[s], p.flip);
             if constexpr (kSplitQ) flip(ql[s], p.flip);
             raw[s].zero();  // not kept through the tiles
+            if constexpr (kTight) {
+                sq[0][s * kWaves + wave][lane] = qh[s];
+                if constexpr (kSplitQ) sq[1][s * kWaves + wave][lane] = ql[s];
+            }
         }
+        if constexpr (kTight) __syncthreads();
 
         f32x4_t acc[DV];
         float m, mm, l;  // mm: m, or 0 while m is -infinity
@@ -420,8 +433,17 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
                         const Dwords<4>& r = kk[h][s];
                         kb = make_uint4(r.d[0], r.d[1], r.d[2], r.d[3]);
                     }
-                    if (kSplitQ) x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kb), as_bf16x8(ql[s]), x, 0, 0, 0);
-                    x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kb), as_bf16x8(qh[s]), x, 0, 0, 0);
+                    uint4 hi, lo;
+                    if constexpr (kTight) {
+                        hi = sq[0][s][lane];
+                        if constexpr (kSplitQ) lo = sq[lost ? 0 : 1][s][lane];
+                    } else {
+                        hi = qh[s];
+                        if constexpr (kSplitQ) lo = ql[s];
+                    }
+                    if constexpr (kSplitQ)
+                        x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kb), as_bf16x8(lo), x, 0, 0, 0);
+                    x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kb), as_bf16x8(hi), x, 0, 0, 0);
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sc[4 * h + r] = x[r];
@@ -475,32 +497,34 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
             if (pass) pl = ph;
 
             // value rows as bf16 pairs of columns, then pairs of tokens
-            uint32_t vb[8][DV / 2];
+            float vscale[8];
+            if constexpr (kE4m3) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if constexpr (kE4m3) {
-                    const uint32_t sw = j < 4 ? vs.x : vs.y;
-                    const float s = scale_of((sw >> (8 * (j & 3))) & 0xff);
-#pragma unroll
-                    for (int i = 0; i < VD; ++i) {
-                        vb[j][2 * i] = e4m3x2_to_bf16<false>(vv[j].d[i], s);
-                        vb[j][2 * i + 1] = e4m3x2_to_bf16<true>(vv[j].d[i], s);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < DV / 2; ++i) vb[j][i] = vv[j].d[i];
-                }
+                for (int j = 0; j < 8; ++j) vscale[j] = scale_of(((j < 4 ? vs.x : vs.y) >> (8 * (j & 3))) & 0xff);
             }
 #pragma unroll
-            for (int j = 0; j < DV; ++j) {
-                uint32_t va[4];
+            for (int i = 0; i < DV / 2; ++i) {
+                uint32_t vb[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    va[i] = __builtin_amdgcn_perm(vb[2 * i + 1][j / 2], vb[2 * i][j / 2],
-                                                  j & 1 ? 0x07060302u : 0x05040100u);
-                const bf16x8_t av = as_bf16x8(make_uint4(va[0], va[1], va[2], va[3]));
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, as_bf16x8(pl), acc[j], 0, 0, 0);
-                acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, as_bf16x8(ph), acc[j], 0, 0, 0);
+                for (int j = 0; j < 8; ++j) {
+                    if constexpr (kE4m3)
+                        vb[j] = i & 1 ? e4m3x2_to_bf16<true>(vv[j].d[i / 2], vscale[j])
+                                      : e4m3x2_to_bf16<false>(vv[j].d[i / 2], vscale[j]);
+                    else
+                        vb[j] = vv[j].d[i];
+                }
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    uint32_t va[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        va[k] = __builtin_amdgcn_perm(vb[2 * k + 1], vb[2 * k], o ? 0x07060302u : 0x05040100u);
+                    const bf16x8_t av = as_bf16x8(make_uint4(va[0], va[1], va[2], va[3]));
+                    f32x4_t& a = acc[2 * i + o];
+                    a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, as_bf16x8(pl), a, 0, 0, 0);
+                    a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, as_bf16x8(ph), a, 0, 0, 0);
+                }
+                if (kTight) __builtin_amdgcn_sched_barrier(0);  // or the pairs of all columns wait in registers
             }
             if (more) {
                 load_values(now, pages.v);
@@ -528,7 +552,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
                     for (int r = 0; r < 4; ++r) keep[(4 * j + r) * 64] = acc[j][r];
                 if (lost) {
 #pragma unroll
-                    for (int s = 0; s < NS; ++s) ql[s] = qh[s];
+                    for (int s = 0; s < NR; ++s) ql[s] = qh[s];
                     c *= 0.5f;
                 }
                 pass = 1;
@@ -611,6 +635,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC)) void attend_kernel(const 
             }
         }
         if (last) break;
+        if constexpr (kTight) __syncthreads();
         at = next_at;
         now = next;
         first_piece = false;
@@ -681,7 +706,8 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
     }
 }
 
-Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages) {
+Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages, bool q_fp32,
+               bool e4m3) {
     Shape s;
     s.heads = (int32_t)H;
     s.dim = (int32_t)D;
@@ -697,7 +723,7 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     const int64_t per_row = s.capacity <= kUnit ? 1 : (s.capacity + kUnit - 1) / kUnit;
     const int64_t units = B * s.rows * (per_row == 1 ? 1 : per_row + kRowCost);
     // a capacity of one unit splits nothing: a workgroup per row of units
-    const int64_t most = per_row == 1 ? int64_t(1) << 20 : kCUs * per_cu((int)D);
+    const int64_t most = per_row == 1 ? int64_t(1) << 20 : kCUs * per_cu((int)D, q_fp32, e4m3);
     s.groups = (int32_t)(units < most ? units : most);
     s.by_row = B * s.rows <= s.groups;
     s.crosses = s.by_row ? (int32_t)(B * s.rows) : s.groups;
@@ -724,13 +750,15 @@ void go(const Args& p, bool q_fp32, hipStream_t s) {
 
 size_t attend_workspace_bytes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages) {
     if (page_size * max_pages <= kUnit) return 0;
-    const Shape s = shape_of(B, Hq, H, D, page_size, max_pages);
+    // bf16 queries on e4m3: no fewer workgroups than any other call's
+    const Shape s = shape_of(B, Hq, H, D, page_size, max_pages, false, true);
     return (size_t)s.crosses * sizeof(Cross) + (size_t)s.groups * 2 * 16 * (D + 2) * sizeof(float);
 }
 
 hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
     const auto unit16 = [&](int64_t stride) { return (uint32_t)(stride * (a.kv.type == BD_E4M3 ? 1 : 2) / 16); };
-    Args p{a, shape_of(a.B, a.Hq, a.kv.num_heads, a.kv.head_dim, a.kv.page_size, a.max_pages),
+    Args p{a, shape_of(a.B, a.Hq, a.kv.num_heads, a.kv.head_dim, a.kv.page_size, a.max_pages, q_fp32,
+                     a.kv.type == BD_E4M3),
            (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride), unit16(a.kv.token_stride),
            (uint32_t)(a.kv.num_heads * a.kv.page_size), __builtin_fabsf(a.scale) * 1.4426950408889634f,
            a.scale < 0.0f ? 0x80008000u : 0u};

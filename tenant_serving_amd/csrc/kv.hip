@@ -335,8 +335,12 @@ void read_lanes(ReadArgs a, hipStream_t s) {
 
 hipError_t launch_kv_write(const bd_kv& kv, const void* k, Strides2 ks, const void* v, Strides2 vs, bool fp32,
                            const int32_t* slots, int64_t T, hipStream_t stream) {
-    const int64_t want = T <= kSmallWrite ? (T + kSmallGroups - 1) / kSmallGroups : (T + kGroups - 1) / kGroups;
+    int64_t want = T <= kSmallWrite ? (T + kSmallGroups - 1) / kSmallGroups : (T + kGroups - 1) / kGroups;
     const int64_t most = T <= kSmallWrite ? 64 : 256;  // what the kernels' tables hold
+    // 128 rows at least of the 64 that 1024 lanes take at once: few heads would
+    // leave the search for repeats to more workgroups than their rows are worth
+    const int64_t least = T <= kSmallWrite ? 1 : 64 / kv.num_heads;
+    if (want < least) want = least;
     const int32_t per = (int32_t)(want < most ? want : most);
     const WriteArgs a{kv, k, v, ks, vs, slots, Div((uint32_t)kv.page_size), Div((uint32_t)(2 * kv.num_heads)), (int32_t)T,
                       per, (int32_t)(kv.num_pages * kv.page_size)};
