@@ -71,7 +71,8 @@ struct Args {
     uint32_t pages;                         // of the cache
     uint32_t page16, head16, token16;       // its strides in units of 16 bytes
     uint32_t page_scales;                   // scale bytes of a page
-    float c;                                // |scale| log2(e)
+    float c;                                // |scale| log2(e), no smaller than the least normal number: times
+                                            // it, -infinity (a score behind the end) stays what it is
     uint32_t flip;                          // the queries' sign bits where scale is negative
 };
 
@@ -292,6 +293,12 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
         const int g8 = (t >> 3) + add, last = (x.tokens - 1) >> 3;
         return g8 < last ? g8 : last;
     };
+    // The one after x, in the same sequence or the next.
+    const auto piece_after = [&](const Piece& x, int row_at) {
+        const bool over = x.row + 1 == p.s.rows;
+        const int b = x.b + over;
+        return piece_at(b, over ? uni(p.a.lengths[b]) : x.len, over ? 0 : x.row + 1, 0, row_at);
+    };
     // where the lane's key rows and value rows are
     struct Groups {
         Group k, v;
@@ -370,13 +377,9 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
         // what comes next, and its first page numbers
         const int next_at = at + kRowCost + now.un;
         const bool last = next_at + kRowCost >= end;
-        Piece next = now;
         Groups next_pages{};
         if (!last) {
-            const bool turn_over = now.row + 1 == p.s.rows;
-            const int nb = now.b + turn_over;
-            const int nlen = turn_over ? uni(p.a.lengths[nb]) : now.len;
-            next = piece_at(nb, nlen, turn_over ? 0 : now.row + 1, 0, next_at);
+            const Piece next = piece_after(now, next_at);
             if (next.t0 < next.stop) next_pages = load_pages(next, next.t0);
         }
 
@@ -485,7 +488,6 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 pr[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j], c, -mm));
-                if (tail) pr[j] = t + 8 * g + j >= tokens ? 0.0f : pr[j];  // also where c is 0
                 l += pr[j];
             }
             const uint4 ph = narrow_bf16x8(pr);
@@ -573,6 +575,10 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
                 }
         }
 
+        // worked out again, so that it takes no registers through the tiles
+        Piece from = now;
+        asm("" : "+s"(from.row), "+s"(from.b));
+        const Piece next = last ? now : piece_after(from, next_at);
         const bool was_bad = __ballot(bad) != 0 || now.len > p.s.capacity;
         bad = false;
         if (!last) load_queries(next);
@@ -760,7 +766,7 @@ hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
     Args p{a, shape_of(a.B, a.Hq, a.kv.num_heads, a.kv.head_dim, a.kv.page_size, a.max_pages, q_fp32,
                      a.kv.type == BD_E4M3),
            (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride), unit16(a.kv.token_stride),
-           (uint32_t)(a.kv.num_heads * a.kv.page_size), __builtin_fabsf(a.scale) * 1.4426950408889634f,
+           (uint32_t)(a.kv.num_heads * a.kv.page_size), __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f),
            a.scale < 0.0f ? 0x80008000u : 0u};
     const int D = a.kv.head_dim;
     if (D <= 64) {
