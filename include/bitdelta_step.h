@@ -108,7 +108,7 @@ typedef struct bd_kv {
 /* Writes the keys and values of T tokens into their slots.
  *
  *   k, v     T tokens of num_heads rows of head_dim values, in_type BD_BF16
- *            or BD_FP32, 16-byte aligned: token t's row of head h starts at
+ *            or BD_FP32, 16-byte aligned, apart from the cache's memory: token t's row of head h starts at
  *            element t * k_strides[0] + h * k_strides[1] (v likewise).  The
  *            strides are HOST arrays of two, multiples of 16 bytes.
  *   slots    [T] int32.  A slot below 0 or past the last page: that token is
@@ -149,7 +149,7 @@ bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t*
  *               last token in its page does not matter, NaN included.
  *               A length over max_pages * page_size, or a looked-up page
  *               outside [0, num_pages), gives rows of NaN.
- *   scale       multiplies the scores; finite.
+ *   scale       multiplies the scores; of any sign, 2^60 at most.
  *   out         [B, num_q_heads, head_dim] bf16, 16-byte aligned.
  *   lse         [B, num_q_heads] fp32, the natural logarithm of
  *               sum_j exp(scale * q . k_j); NULL if not wanted.
@@ -161,7 +161,9 @@ bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t*
  *               Its contents on entry do not matter.
  * Scores, the running maximum and sum and the output sums are fp32; fp32
  * queries and the softmax weights enter the matrix products as two bf16
- * terms each, so no input or weight is cut to 8 bits.  The same inputs and
+ * terms each, so no input or weight is cut to 8 bits (but where a row of the
+ * sequence itself holds infinities: what they reach is summed with one term
+ * each, as a second one would make NaN of them).  The same inputs and
  * batch give bitwise the same outputs.  B == 0 is a no-op.
  * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _WORKSPACE, _HIP,
  * _DEVICE.

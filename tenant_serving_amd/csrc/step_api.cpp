@@ -9,6 +9,7 @@
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr float kMaxScale = 1152921504606846976.0f;  // 2^60: times log2(e) it stays far from infinity
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool in_type(int32_t t) { return t == BD_BF16 || t == BD_FP32; }
@@ -124,7 +125,7 @@ bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_
     if (st != BD_OK) return st;
     if (!q_strides || (B > 0 && (!q || !page_table || !lengths || !out))) return BD_ERR_NULL;
     if (!in_type(q_type)) return BD_ERR_MODE;
-    if (B < 0 || table_stride < 0 || !std::isfinite(scale) ||
+    if (B < 0 || table_stride < 0 || !(std::fabs(scale) <= kMaxScale) ||
         !attend_shape(B > 0 ? B : 1, num_q_heads, kv->num_heads, kv->head_dim, kv->page_size, max_pages))
         return BD_ERR_SHAPE;
     if ((st = check_strides(q_strides, q_type)) != BD_OK) return st;
@@ -136,7 +137,7 @@ bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return BD_ERR_WORKSPACE;
     if ((st = bd::check_current_device(nullptr)) != BD_OK) return st;
     const bd::AttendArgs a{*kv, q, {q_strides[0], q_strides[1]}, page_table, lengths, out, lse,
-                           static_cast<float*>(workspace), table_stride, (int32_t)max_pages, (int32_t)B,
+                           need > 0 ? static_cast<float*>(workspace) : nullptr, table_stride, (int32_t)max_pages, (int32_t)B,
                            num_q_heads, scale};
     return finish(bd::launch_attend(a, q_type == BD_FP32, static_cast<hipStream_t>(stream)));
 }

@@ -96,10 +96,15 @@ def _same_gpu(device, named):
             raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
 
 
+def _span(t):
+    """The addresses that a tensor reaches, gaps of its strides included."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
+
 def _overlap(a, b):
-    """Whether the memory of two contiguous tensors overlaps."""
-    return (a.data_ptr() < b.data_ptr() + b.numel() * b.element_size()
-            and b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
+    (a0, a1), (b0, b1) = _span(a), _span(b)
+    return a0 < b1 and b0 < a1
 
 
 def _at(t):
@@ -410,7 +415,13 @@ def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
         _plain("out", out, torch.bfloat16, (B, heads, kv.head_dim))
     if lse is not None:
         _plain("lse", lse, torch.float32, (B, heads))
-    _same_gpu(kv.device, (("q", q), ("page_table", page_table), ("lengths", lengths), ("out", out), ("lse", lse)))
+    every = (("q", q), ("page_table", page_table), ("lengths", lengths), ("out", out), ("lse", lse))
+    _same_gpu(kv.device, every)
+    every = [(name, t) for name, t in every if t is not None and t.numel()]
+    for name, t in every:
+        for other, o in every:
+            if name in ("out", "lse") and other != name and _overlap(t, o):
+                raise ValueError("%s overlaps %s" % (name, other))
 
 
 def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -426,8 +437,8 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     B, heads, _ = q.shape
     dev = kv._dev
     scale = kv.head_dim ** -0.5 if scale is None else float(scale)
-    if not math.isfinite(scale):
-        raise ValueError("scale must be finite (got %r)" % scale)
+    if not abs(scale) <= 2.0 ** 60:
+        raise ValueError("scale must be at most 2^60 (got %r)" % scale)
     if not (out is None and lse is None and type(page_table) is torch.Tensor and page_table.dim() == 2
             and page_table.dtype == torch.int32 and page_table.shape[0] == B and page_table.is_contiguous()
             and 1 <= page_table.shape[1] <= (1 << 24) // kv.page_size and page_table.get_device() == dev

@@ -565,6 +565,72 @@ def test_attend_forms(bd):
     check_attend(c, q[2:3], [140], slots[33:173], one, lse[2:3], 0.125)
 
 
+def test_attend_outputs_apart_from_inputs(bd):
+    lens = [33, 140]
+    c, q, table, lens_t, _ = attend_case(bd, lens, 2, 4, 64, 16, BF, BF)
+    args = (c.kv, table.to(DEV), lens_t.to(DEV))
+    gq = q.to(DEV)
+    with pytest.raises(ValueError, match="out overlaps q"):
+        bd.bd_attend(gq, *args, out=gq)
+    out = torch.empty_like(gq)
+    with pytest.raises(ValueError, match="overlaps"):
+        bd.bd_attend(gq, *args, out=out, lse=out.view(torch.float32).view(-1)[:16].view(2, 8))
+    wide = torch.zeros((2, 16, 64), dtype=BF, device=DEV)
+    with pytest.raises(ValueError, match="overlaps"):    # in the gaps of q's strides
+        bd.bd_attend(wide[:, :8], *args, out=wide.view(-1)[512:1536].view(2, 8, 64))
+
+
+def test_attend_through_the_c_abi(bd):
+    """The C call with a workspace of just the size asked for, used again by the next call, and with one that is not
+    needed: nothing is written around them."""
+    import ctypes
+    from tenant_serving_amd import step
+    lib = step._library()
+    for lens, page in (([100, 3], 16), ([1000, 129, 0], 16)):
+        c, q, table, lens_t, slots = attend_case(bd, lens, 2, 2, 64, page, E4, BF)
+        B, hq, D = q.shape
+        gq, gt, gl = q.to(DEV), table.to(DEV), lens_t.to(DEV)
+        need = lib.bd_attend_workspace_bytes(B, hq, 2, D, page, table.shape[1])
+        assert (need == 0) == (table.shape[1] * page <= 128)
+        mem = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device=DEV)
+        out = torch.empty((B, hq, D), dtype=BF, device=DEV)
+        lse = torch.empty((B, hq), dtype=F32, device=DEV)
+        qs = step._Pair(hq * D, D)
+        for _ in range(3):
+            st = lib.bd_attend(c.kv._ref, gq.data_ptr(), 0, qs, hq, gt.data_ptr(), table.shape[1], table.shape[1],
+                               gl.data_ptr(), B, D ** -0.5, out.data_ptr(), lse.data_ptr(), mem.data_ptr() + 4096,
+                               need, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+            assert st == 0
+            check_attend(c, q, lens, slots, out, lse, D ** -0.5)
+        assert (mem[:4096] == 0xA5).all() and (mem[4096 + need:] == 0xA5).all()
+
+
+def test_attend_fp32_queries_and_infinite_keys(bd):
+    """fp32 queries against keys with infinities: a score of -infinity drops out, whatever the queries' second term."""
+    lens = [70, 300]
+    c, q, table, lens_t, slots = attend_case(bd, lens, 1, 2, 32, 16, BF, F32)
+    k = torch.randn((370, 1, 32), generator=gen_of(3)).to(BF)
+    v = torch.randn((370, 1, 32), generator=gen_of(4)).to(BF)
+    q = q.abs() + 0.1
+    k[5, 0, 0] = -float("inf")
+    k[200, 0, 7] = -float("inf")
+    s = torch.tensor(slots, dtype=torch.int32)
+    c.expect(k, v, s)
+    bd.bd_kv_write(c.kv, k.to(DEV), v.to(DEV), s.to(DEV))
+    out, lse = run_attend(bd, c, q, table, lens_t)
+    # where a score broke, the wave's queries are one bf16 term: half a step, 2^-8, of each
+    at = 0
+    for b, n in enumerate(lens):
+        kr = np.stack([c.row64(0, x) for x in slots[at:at + n]])
+        vr = np.stack([c.row64(1, x) for x in slots[at:at + n]])
+        at += n
+        want, want_lse, S = ref.attend(ref.to64(q)[b], kr, vr, 32 ** -0.5)
+        ds = 2.0 ** -8 * S + 40 * U * S
+        tol = 2.0 ** -8 * np.abs(want) + 2 * np.abs(vr).max() * (np.expm1(2 * ds) + 2.0 ** -8 + (n + 64) * U)
+        assert np.all(np.abs(ref.to64(out)[b] - want) <= tol)
+        assert np.all(np.abs(ref.to64(lse)[b] - want_lse) <= ds + 1e-4)
+
+
 def test_offsets_past_32_bits(bd):
     """Rows at the far end of arrays of more than 4 GiB each."""
     heads, page, dim = 8, 16, 128

@@ -92,7 +92,7 @@ def test_attend_refusals(lib):
                          (dict(lengths=None), NULL), (dict(out=None), NULL), (dict(q_type=2), MODE),
                          (dict(B=-1), SHAPE), (dict(heads=0), SHAPE), (dict(heads=3), SHAPE), (dict(heads=65538), SHAPE),
                          (dict(pages=0), SHAPE), (dict(pages=(1 << 20) + 1), SHAPE), (dict(stride=-1), SHAPE),
-                         (dict(scale=float("inf")), SHAPE), (dict(scale=float("nan")), SHAPE),
+                         (dict(scale=float("inf")), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(scale=-2.0 ** 61), SHAPE),
                          (dict(qs=_pair(-8, 64)), SHAPE), (dict(qs=_pair(260, 64)), ALIGN), (dict(q=OFF), ALIGN),
                          (dict(out=OFF), ALIGN), (dict(table=OFF), ALIGN), (dict(lengths=OFF), ALIGN),
                          (dict(lse=OFF), ALIGN), (dict(ws=None), WORKSPACE), (dict(bytes=need - 4), WORKSPACE),
