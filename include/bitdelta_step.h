@@ -47,7 +47,7 @@ typedef enum bd_type {
  *
  *   h = x + residual  (fp32; without a residual h = x)
  *   residual_out = h rounded to residual_type, and h stands for that value
- *   y = h / sqrt(mean(h^2) + eps) * gain[variant]   (fp32 throughout)
+ *   y = h / sqrt(mean(h^2) + eps) * gain[variant]
  *
  *   x            [M, d], x_type BD_BF16 or BD_FP32 (the linears give either).
  *   residual     [M, d], residual_type BD_BF16 or BD_FP32; NULL for none.
@@ -63,8 +63,9 @@ typedef enum bd_type {
  *                the last one of the rest.  NULL for BD_BF16.
  * d: a multiple of 8, 8 .. 65536.  eps >= 0.  x, residual, residual_out,
  * gain, out: 16-byte aligned (out: 8 for BD_E4M3).  M == 0 is a no-op.
- * Sums in fp32, in a fixed order: the same inputs give bitwise the same
- * outputs.
+ * fp32 throughout for a bf16 result; for codes the sum, root and products are
+ * 64-bit and y is rounded once, to its code.  Fixed order: the same inputs give
+ * bitwise the same outputs.
  * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _HIP, _DEVICE.
  * ------------------------------------------------------------------------- */
 bd_status bd_rms_norm(const void* x, int32_t x_type, const void* residual, void* residual_out,

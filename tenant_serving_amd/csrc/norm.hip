@@ -10,11 +10,28 @@
 // wave, then the waves' sums in wave order.
 //
 // A group of 32 columns of the e4m3 result is four neighbouring lanes, whose
-// largest magnitude two lane exchanges give.
+// largest magnitude two lane exchanges give.  For this result the sums and
+// products are 64-bit: in 32 bits a few codes in a million fall on the other
+// side of their border, and the extra work hides behind the memory (8192 x 8192
+// with an fp32 residual 134.9 -> 136.3 us).
 #include "step_internal.h"
+
+#include <type_traits>
 
 namespace bd {
 namespace {
+
+// A double as the fp32 next to it whose last bit is odd, unless it is an fp32
+// itself: what is rounded to fewer bits from there (and a comparison with
+// numbers of fewer bits) comes out as from the double.
+__device__ __forceinline__ float to_odd(double y) {
+    const float f = (float)y;
+    const double off = y - (double)f;
+    const uint32_t b = __float_as_uint(f);
+    // towards y: one more in magnitude where f fell short of it
+    const uint32_t step = (off > 0.0) == (f > 0.0f) ? 1u : 0xffffffffu;
+    return __uint_as_float(off != 0.0 && off == off && !(b & 1) ? b + step : b);
+}
 
 template <int NT>
 constexpr int kNormBlock = NT == 64 ? 256 : NT;
@@ -35,6 +52,7 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
     const int64_t row = row0 + (NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x);
     if (NT == 64 && row >= a.M) return;  // a whole wave; this form has no barrier
     const int64_t base = row * a.d;
+    typedef typename std::conditional<kE4m3, double, float>::type Sum;
 
     Raw8<kX32> xr[C];
     Raw8<kRes == 2> rr[C];
@@ -65,7 +83,7 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
     }
 
     float h[C][8];
-    float sum = 0.0f;
+    Sum sum = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int e = (c * NT + tid) * 8;
@@ -86,18 +104,18 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[c][i], h[c][i], sum);
+        for (int i = 0; i < 8; ++i) sum = fma((Sum)h[c][i], (Sum)h[c][i], sum);
     }
     sum = wave_sum(sum);
     if (NT > 64) {
-        __shared__ float part[NT / 64];
+        __shared__ Sum part[NT / 64];
         if ((tid & 63) == 0) part[tid >> 6] = sum;
         __syncthreads();
-        sum = 0.0f;
+        sum = 0;
 #pragma unroll
         for (int w = 0; w < NT / 64; ++w) sum += part[w];
     }
-    const float rstd = known ? 1.0f / sqrtf(sum / (float)a.d + a.eps) : __builtin_nanf("");
+    const Sum rstd = known ? (Sum)1 / sqrt(sum / (Sum)a.d + (Sum)a.eps) : (Sum)__builtin_nanf("");
 
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -112,7 +130,12 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
             gb[c].widen(g);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[c][i] = h[c][i] * rstd * g[i];
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (kE4m3)
+                h[c][i] = to_odd((double)h[c][i] * rstd * (double)g[i]);
+            else
+                h[c][i] = h[c][i] * rstd * g[i];
+        }
         if (kE4m3) {
             uint32_t top = 0;
 #pragma unroll
