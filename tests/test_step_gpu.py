@@ -477,6 +477,33 @@ def test_attend_every_workgroup(bd):
     check_attend(c, q, lens, slots, out, lse, 0.25)
 
 
+@pytest.mark.parametrize("heads,dim,kind", [(8, 16, BF), (4, 64, E4), (2, 128, BF), (3, 208, E4)])
+def test_attend_more_rows_than_workgroups(bd, heads, dim, kind):
+    """More (sequence, head) rows than workgroups, short ones among long ones, so that rows of every length are cut."""
+    B = 800 // heads
+    lens = [(37 * i) % 150 for i in range(B)]
+    for i, n in ((3, 2000), (B // 2, 1300), (B - 2, 777)):
+        lens[i] = n
+    c, q, table, lens_t, slots = attend_case(bd, lens, heads, 2, dim, 16, kind, BF)
+    out, lse = run_attend(bd, c, q, table, lens_t)
+    check_attend(c, q, lens, slots, out, lse, dim ** -0.5,
+                 rows=(0, 1, 2, 3, 4, 5, B // 2 - 1, B // 2, B // 2 + 1, B - 3, B - 2, B - 1))
+
+
+def test_attend_many_sequences(bd):
+    """Thousands of sequences that share their pages: rows of the batch are what they are alone."""
+    lens = [0, 1, 30, 64, 130, 7, 128, 129]
+    c, q, table, lens_t, slots = attend_case(bd, lens, 1, 2, 32, 16, E4, BF)
+    B = 4099
+    pick = torch.arange(B) * 5 % len(lens)
+    out, lse = run_attend(bd, c, q[pick].contiguous(), table[pick].contiguous(), lens_t[pick].contiguous())
+    alone, alone_lse = run_attend(bd, c, q, table, lens_t)
+    check_attend(c, q, lens, slots, alone, alone_lse, 32 ** -0.5)
+    # a row may be cut elsewhere in another batch: two bf16 roundings and the sums' own
+    o, a = ref.to64(out), ref.to64(alone)[pick.numpy()]
+    assert np.all(np.abs(o - a) <= 2.0 ** -7 * np.abs(a) + 2.0 ** -14)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
 def test_attend_scales(bd, scale):
     for kind in (BF, E4):
@@ -725,6 +752,56 @@ def test_graph_of_a_step(bd):
             eager = step()
             for a, b in zip(first, eager):
                 assert same_bits(a, b), t
+
+
+def test_two_graphs_in_turn(bd):
+    """Two captured calls, replayed in turn with eager ones between them, each with a workspace of its own."""
+    cases = [attend_case(bd, lens, 2, 4, 64, 16, kind, BF, seed=s)
+             for lens, kind, s in (([900, 3, 257], E4, 1), ([2000, 150], BF, 2))]
+    args = [(q.to(DEV), c.kv, t.to(DEV), n.to(DEV)) for c, q, t, n, _ in cases]
+    want = [bd.bd_attend(*a) for a in args]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for a in args:
+            bd.bd_attend(*a)
+    torch.cuda.synchronize()
+    graphs, held = [], []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(bd.bd_attend(*a))
+        graphs.append(g)
+    for _ in range(6):
+        for h in held:
+            h.fill_(7.0)
+        graphs[0].replay()
+        graphs[1].replay()
+        again = bd.bd_attend(*args[0])
+        graphs[0].replay()
+        torch.cuda.synchronize()
+        assert same_bits(held[0], want[0]) and same_bits(held[1], want[1]) and same_bits(again, want[0])
+
+
+def test_tensors_of_another_device(bd, monkeypatch):
+    """Where the current device is not the tensors', the call makes theirs current (told here that it is not)."""
+    from tenant_serving_amd import step
+    real, left = step._current_device, []
+
+    def other_once():
+        return left.pop() if left else real()
+    monkeypatch.setattr(step, "_current_device", other_once)
+    x, res, gain, ids = on_gpu(*norm_inputs(4, 64, BF, BF, BF, 2))
+    c, q, table, lens, _ = attend_case(bd, [40, 9], 2, 2, 64, 16, BF, BF)
+    slots = torch.arange(4, dtype=torch.int32, device=DEV)
+    rows = torch.randn((4, 2, 64), generator=gen_of(1)).to(BF).to(DEV)
+    calls = [lambda: bd.bd_rms_norm(x, gain, residual=res, variant_ids=ids)[0],
+             lambda: bd.bd_rms_norm_e4m3(x, gain, variant_ids=ids)[0],
+             lambda: bd.bd_attend(q.to(DEV), c.kv, table.to(DEV), lens.to(DEV)),
+             lambda: (bd.bd_kv_write(c.kv, rows, rows, slots), bd.bd_kv_read(c.kv, slots)[1])[1]]
+    for call in calls:
+        want = call()
+        left.append(1)
+        assert same_bits(call(), want) and not left
 
 
 def test_a_layer_together(bd):
