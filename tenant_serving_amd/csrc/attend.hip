@@ -89,13 +89,18 @@ __device__ __forceinline__ int units_of(int len, int capacity) {
 // for each of its units.  Lane l sums the sequences [l n, l n + n).
 struct Line {
     int n, first, total;  // per lane: sequences, places before its own; places of the batch
+    int len;              // per lane: its last sequence's length
     __device__ __forceinline__ void scan(const Args& p) {
         const int lane = threadIdx.x & 63;
         n = (p.a.B + 63) / 64;
         int sum = 0;
         const int b0 = lane * n;
+        len = 0;
         for (int i = 0; i < n; ++i)
-            if (b0 + i < p.a.B) sum += kRowCost + units_of(p.a.lengths[b0 + i], p.s.capacity);
+            if (b0 + i < p.a.B) {
+                len = p.a.lengths[b0 + i];
+                sum += kRowCost + units_of(len, p.s.capacity);
+            }
         sum *= p.s.rows;
         int inc = sum;
 #pragma unroll
@@ -106,18 +111,24 @@ struct Line {
         first = inc - sum;
         total = uni(__shfl(inc, 63, 64));
     }
-    // The sequence that holds place u, and its first place.
-    __device__ __forceinline__ int holder_of(const Args& p, int u, int* start) const {
+    // The sequence that holds place u, its first place and its length.
+    __device__ __forceinline__ int holder_of(const Args& p, int u, int* start, int* length) const {
         const int lane = threadIdx.x & 63;
         // the last lane that has sequences and starts at or before u
         const uint64_t at = __ballot(lane * n < p.a.B && first <= u);
         const int l = 63 - __clzll(at);
         int s = uni(__shfl(first, l, 64));
+        if (n == 1) {
+            *start = s;
+            *length = uni(__shfl(len, l, 64));
+            return uni(l);
+        }
         int b = l * n;
         for (;;) {
-            const int len = (kRowCost + units_of(p.a.lengths[b], p.s.capacity)) * p.s.rows;
-            if (u < s + len || b + 1 >= p.a.B) break;
-            s += len;
+            *length = uni(p.a.lengths[b]);
+            const int span = (kRowCost + units_of(*length, p.s.capacity)) * p.s.rows;
+            if (u < s + span || b + 1 >= p.a.B) break;
+            s += span;
             ++b;
         }
         *start = uni(s);
@@ -238,9 +249,11 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
+    // where no row has more than one unit, the line needs no lengths
+    const bool single = p.s.capacity <= kUnit;
     Line line;
-    line.scan(p);
-    const Cut cut(line.total, p.s.groups);
+    if (!single) line.scan(p);
+    const Cut cut(single ? p.a.B * p.s.rows * (kRowCost + 1) : line.total, p.s.groups);
     const int w = blockIdx.x;
     Cross* crosses = reinterpret_cast<Cross*>(p.a.part);
     const bool by_row = p.s.by_row;
@@ -248,8 +261,14 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
     if (w >= cut.W) return;
     const int u = cut.start(w);
     const int end = cut.start(w + 1);
-    int at;  // the current row's first place
-    const int b0 = line.holder_of(p, u, &at);
+    int at, len0, b0;  // the current row's first place; the first sequence
+    if (single) {
+        b0 = u / (p.s.rows * (kRowCost + 1));
+        at = b0 * p.s.rows * (kRowCost + 1);
+        len0 = uni(p.a.lengths[b0]);
+    } else {
+        b0 = line.holder_of(p, u, &at, &len0);
+    }
 
     // The part of a row of units that this workgroup works on.
     struct Piece {
@@ -271,7 +290,6 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
         x.nq = p.s.group - x.q0 < 16 ? p.s.group - x.q0 : 16;
         return x;
     };
-    const int len0 = uni(p.a.lengths[b0]);
     const int span0 = kRowCost + units_of(len0, p.s.capacity), row0 = (u - at) / span0;
     at += row0 * span0;
     if (at + kRowCost >= end) return;  // no unit of its own

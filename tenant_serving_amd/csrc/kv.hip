@@ -10,10 +10,18 @@
 namespace bd {
 namespace {
 
-// Streaming stores: what is read back goes to the next kernel once.
+// Streaming stores, for what is read back (it goes to the next kernel once) and
+// for long writes, whose rows are read again a layer's worth of other data
+// later (16384 tokens from fp32 to e4m3 38.9 -> 35.8 us, 16169 of 8 rows of 80 in
+// bf16 26.5 -> 21.8).
 __device__ __forceinline__ void store_stream16(uint16_t* p, uint4 v) {
     const u32x4_t w = {v.x, v.y, v.z, v.w};
     __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
+}
+__device__ __forceinline__ void store_stream8(uint8_t* p, uint2 v) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    const u32x2_t w = {v.x, v.y};
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t*>(p));
 }
 
 constexpr int kThreads = 256;   // of the read
@@ -201,12 +209,20 @@ __global__ __launch_bounds__(kWide) void kv_write_kernel(const WriteArgs a) {
             if (in && keep) {
                 const uint2 w = make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3], inv),
                                            pack_e4m3x4(f[4], f[5], f[6], f[7], inv));
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + to) = w;
+                uint8_t* p = static_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + to;
+                if (kWide == 256)
+                    *reinterpret_cast<uint2*>(p) = w;
+                else
+                    store_stream8(p, w);
             }
             if (lane == 0 && keep)
                 (is_v ? a.kv.v_scales : a.kv.k_scales)[to_scale[i] + (int64_t)head * a.kv.page_size] = (uint8_t)byte;
         } else if (in && keep) {
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.kv.v : a.kv.k) + to) = narrow_bf16x8(f);
+            uint16_t* p = static_cast<uint16_t*>(is_v ? a.kv.v : a.kv.k) + to;
+            if (kWide == 256)
+                *reinterpret_cast<uint4*>(p) = narrow_bf16x8(f);
+            else
+                store_stream16(p, narrow_bf16x8(f));
         }
     }
 }

@@ -164,15 +164,30 @@ def _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, 
         shape = x.shape
         d, dev = shape[-1], x.get_device()
         lead = shape[:-1]
-        ok = (out is None and scales is None and residual_out is None and dev >= 0 and 8 <= d <= 65536 and d % 8 == 0
-              and eps >= 0.0 and x.is_contiguous() and gain.is_contiguous() and gain.get_device() == dev
-              and gain.dim() == 2 and gain.shape[0] >= 1 and gain.shape[1] == d
+        ok = (dev >= 0 and 8 <= d <= 65536 and d % 8 == 0 and eps >= 0.0 and x.is_contiguous()
+              and gain.is_contiguous() and gain.get_device() == dev and gain.dim() == 2 and gain.shape[0] >= 1
+              and gain.shape[1] == d
               and (residual is None or (residual.shape == shape and residual.is_contiguous()
                                         and residual.get_device() == dev and residual.dtype in _IN))
               and (variant_ids is None or (variant_ids.shape == lead and variant_ids.dtype == torch.int32
                                            and variant_ids.is_contiguous() and variant_ids.get_device() == dev))
-              and x.dtype in _IN and gain.dtype in _IN)
-    except (AttributeError, IndexError):
+              and x.dtype in _IN and gain.dtype in _IN and scales is None)
+        if ok and (out is not None or residual_out is not None):
+            # given outputs: of the right kind, and no two tensors meet (but for a residual updated in place)
+            used = [x, gain] if variant_ids is None else [x, gain, variant_ids]
+            if residual is not None:
+                used.append(residual)
+            if residual_out is not None and residual_out is not residual:
+                ok = (residual is not None and residual_out.shape == shape and residual_out.dtype == residual.dtype
+                      and residual_out.is_contiguous() and residual_out.get_device() == dev)
+                used.append(residual_out)
+            if out is not None:
+                ok = (ok and out.shape == shape and out.is_contiguous() and out.get_device() == dev
+                      and out.dtype == (torch.bfloat16 if out_type == BD_BF16 else torch.float8_e4m3fn))
+                used.append(out)
+            at = sorted([(t.data_ptr(), t.nbytes) for t in used])
+            ok = ok and all(p + n <= q for (p, n), (q, _) in zip(at, at[1:]))
+    except (AttributeError, IndexError, TypeError):
         ok = False
     if not ok:
         _refuse_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales)
@@ -396,6 +411,15 @@ def bd_kv_read(kv: bd_kv_cache, slots: torch.Tensor, out: tuple[torch.Tensor, to
     return k, v
 
 
+def _free(out, q, shape, dev):
+    """Whether out is a bf16 tensor of this shape that lies apart from contiguous queries."""
+    if not (type(out) is torch.Tensor and out.dtype == torch.bfloat16 and out.shape == shape and out.is_contiguous()
+            and out.get_device() == dev and q.is_contiguous()):
+        return False
+    a, b = out.data_ptr(), q.data_ptr()
+    return a + out.nbytes <= b or b + q.nbytes <= a
+
+
 def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
     """The checks of an attention's tensors, in full; raises or returns."""
     B = q.shape[0]
@@ -439,7 +463,7 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     scale = kv.head_dim ** -0.5 if scale is None else float(scale)
     if not abs(scale) <= 2.0 ** 60:
         raise ValueError("scale must be at most 2^60 (got %r)" % scale)
-    if not (out is None and lse is None and type(page_table) is torch.Tensor and page_table.dim() == 2
+    if not (lse is None and (out is None or _free(out, q, (B, heads, kv.head_dim), dev)) and type(page_table) is torch.Tensor and page_table.dim() == 2
             and page_table.dtype == torch.int32 and page_table.shape[0] == B and page_table.is_contiguous()
             and 1 <= page_table.shape[1] <= (1 << 24) // kv.page_size and page_table.get_device() == dev
             and _index("lengths", lengths, B, dev) and q.get_device() == dev and 1 <= heads <= 65535
