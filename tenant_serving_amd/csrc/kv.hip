@@ -30,13 +30,16 @@ constexpr int kThreads = 256;   // of the read
 // lane and plain stores: 192 -> 141 us (5.7 TB/s); one row 147, four 145, two
 // with plain stores 155.
 constexpr int kReadRows = 2;
-// The write: up to this many tokens by workgroups of 256 lanes (of 1..2
-// tokens), more by at most 1024 of 1024 lanes.  Fewer and larger workgroups
-// read the later slots fewer times, but start on the rows later: 16384 tokens
-// from fp32 to e4m3 with 512 / 1024 / 2048 of them 39.3 / 38.2 / 47.3 us, 65536
-// 169 / 155 / 150.
+// The write: up to kSmallWrite tokens by workgroups of 256 lanes (1..2 tokens
+// each), more by at most 1024 of 1024 lanes (up to 32 tokens each), in slices.
+// Fewer and larger workgroups read the later slots fewer times, but start on
+// the rows later: 16384 tokens from fp32 to e4m3 with 512 / 1024 / 2048 of them
+// 39.3 / 38.2 / 47.3 us; 65536 in slices of 16384 / 32768 / 65536 157 / 162 / 155,
+// from bf16 125 / 118 / 126, and a slice bounds what the search costs a token.
 constexpr int64_t kSmallWrite = 4096;
 constexpr int64_t kSmallGroups = 2048, kGroups = 1024;
+constexpr int64_t kSlice = 32768;
+static_assert(kSmallWrite <= 2 * kSmallGroups && kSlice <= 32 * kGroups, "tables of kv_write_kernel");
 
 // n / d for 0 <= n < 2^31 by a product: m = ceil(2^s / d) with s = 31 + ceil(log2 d)
 // is below 2^32 and too large by less than d / 2^s, which n cannot carry over.
@@ -92,7 +95,7 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x) {
 // them; the rest are compared.
 template <bool kX32, bool kE4m3, int kLanes, int kWide>
 __global__ __launch_bounds__(kWide) void kv_write_kernel(const WriteArgs a) {
-    constexpr int kMost = kWide == 256 ? 64 : 256;  // tokens of a workgroup
+    constexpr int kMost = kWide == 256 ? 2 : 32;  // tokens of a workgroup
     __shared__ int own[kMost], dead[kMost];
     __shared__ int64_t to_row[kMost], to_scale[kMost];
     __shared__ int range[2];
@@ -147,9 +150,9 @@ __global__ __launch_bounds__(kWide) void kv_write_kernel(const WriteArgs a) {
     __syncthreads();
     {
         const int lo = kWide == 256 ? range[0] : 0;
-        const uint32_t width = kWide == 256 ? (uint32_t)(range[1] - lo) : 0u;
+        const uint32_t width = kWide == 256 ? (uint32_t)range[1] - (uint32_t)lo : 0u;
         const auto maybe = [&](int s) -> bool {
-            if (kWide == 256) return lo >= 0 && (uint32_t)(s - lo) <= width;
+            if (kWide == 256) return lo >= 0 && (uint32_t)s - (uint32_t)lo <= width;
             const uint32_t h = hash(s);
             return (bits[h >> 5] >> (h & 31)) & 1;
         };
@@ -351,27 +354,38 @@ void read_lanes(ReadArgs a, hipStream_t s) {
 
 hipError_t launch_kv_write(const bd_kv& kv, const void* k, Strides2 ks, const void* v, Strides2 vs, bool fp32,
                            const int32_t* slots, int64_t T, hipStream_t stream) {
-    int64_t want = T <= kSmallWrite ? (T + kSmallGroups - 1) / kSmallGroups : (T + kGroups - 1) / kGroups;
-    const int64_t most = T <= kSmallWrite ? 64 : 256;  // what the kernels' tables hold
-    // 128 rows at least of the 64 that 1024 lanes take at once: few heads would
-    // leave the search for repeats to more workgroups than their rows are worth
-    const int64_t least = T <= kSmallWrite ? 1 : 64 / kv.num_heads;
-    if (want < least) want = least;
-    const int32_t per = (int32_t)(want < most ? want : most);
-    const WriteArgs a{kv, k, v, ks, vs, slots, Div((uint32_t)kv.page_size), Div((uint32_t)(2 * kv.num_heads)), (int32_t)T,
-                      per, (int32_t)(kv.num_pages * kv.page_size)};
-    if (kv.type == BD_E4M3) {
-        if (fp32)
-            write_lanes<true, true>(a, stream);
-        else
-            write_lanes<false, true>(a, stream);
-    } else {
-        if (fp32)
-            write_lanes<true, false>(a, stream);
-        else
-            write_lanes<false, false>(a, stream);
+    // Long calls in slices, one after another on the stream: a later slice's
+    // rows come over an earlier one's by themselves, and a workgroup's search
+    // stays within its slice.
+    for (int64_t t0 = 0; t0 < T; t0 += kSlice) {
+        const int64_t n = T - t0 < kSlice ? T - t0 : kSlice;
+        const bool small = n <= kSmallWrite;
+        int64_t per = small ? (n + kSmallGroups - 1) / kSmallGroups : (n + kGroups - 1) / kGroups;
+        // 64 rows at least, which 1024 lanes take at once at head_dim 128: few
+        // heads would leave the search to more workgroups than their rows are
+        // worth
+        const int64_t least = small ? 1 : 32 / kv.num_heads;
+        if (per < least) per = least;
+        const int64_t size = fp32 ? 4 : 2;
+        const WriteArgs a{kv, static_cast<const char*>(k) + t0 * ks.token * size,
+                          static_cast<const char*>(v) + t0 * vs.token * size, ks, vs, slots + t0,
+                          Div((uint32_t)kv.page_size), Div((uint32_t)(2 * kv.num_heads)), (int32_t)n, (int32_t)per,
+                          (int32_t)(kv.num_pages * kv.page_size)};
+        if (kv.type == BD_E4M3) {
+            if (fp32)
+                write_lanes<true, true>(a, stream);
+            else
+                write_lanes<false, true>(a, stream);
+        } else {
+            if (fp32)
+                write_lanes<true, false>(a, stream);
+            else
+                write_lanes<false, false>(a, stream);
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 hipError_t launch_kv_read(const bd_kv& kv, const int32_t* slots, int64_t T, uint16_t* k_out, uint16_t* v_out,
