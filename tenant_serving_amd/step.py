@@ -24,6 +24,7 @@ from .bitdelta import _check, _workspace, library
 
 BD_BF16, BD_FP32, BD_E4M3 = 0, 1, 2
 _IN = {torch.bfloat16: BD_BF16, torch.float32: BD_FP32}
+_INT = torch.int32
 _HELD = {torch.bfloat16: BD_BF16, torch.float8_e4m3fn: BD_E4M3}
 _declared = None
 # the current stream's handle and device as plain numbers: a call of a few microseconds on the GPU has no room for the
@@ -164,14 +165,15 @@ def _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, 
         shape = x.shape
         d, dev = shape[-1], x.get_device()
         lead = shape[:-1]
-        ok = (dev >= 0 and 8 <= d <= 65536 and d % 8 == 0 and eps >= 0.0 and x.is_contiguous()
-              and gain.is_contiguous() and gain.get_device() == dev and gain.dim() == 2 and gain.shape[0] >= 1
-              and gain.shape[1] == d
+        num_gains, gain_d = gain.shape
+        x_type, gain_type = _IN[x.dtype], _IN[gain.dtype]
+        res_type = _IN[residual.dtype] if residual is not None else BD_BF16
+        ok = (dev >= 0 and 8 <= d <= 65536 and d % 8 == 0 and eps >= 0.0 and gain_d == d and num_gains >= 1
+              and scales is None and x.is_contiguous() and gain.is_contiguous() and gain.get_device() == dev
               and (residual is None or (residual.shape == shape and residual.is_contiguous()
-                                        and residual.get_device() == dev and residual.dtype in _IN))
-              and (variant_ids is None or (variant_ids.shape == lead and variant_ids.dtype == torch.int32
-                                           and variant_ids.is_contiguous() and variant_ids.get_device() == dev))
-              and x.dtype in _IN and gain.dtype in _IN and scales is None)
+                                        and residual.get_device() == dev))
+              and (variant_ids is None or (variant_ids.shape == lead and variant_ids.dtype is _INT
+                                           and variant_ids.is_contiguous() and variant_ids.get_device() == dev)))
         if ok and (out is not None or residual_out is not None):
             # given outputs: of the right kind, and no two tensors meet (but for a residual updated in place)
             used = [x, gain] if variant_ids is None else [x, gain, variant_ids]
@@ -187,20 +189,19 @@ def _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, 
                 used.append(out)
             at = sorted([(t.data_ptr(), t.nbytes) for t in used])
             ok = ok and all(p + n <= q for (p, n), (q, _) in zip(at, at[1:]))
-    except (AttributeError, IndexError, TypeError):
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
         ok = False
     if not ok:
         _refuse_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales)
+        num_gains = gain.shape[0] if gain.dim() == 2 else 1
+        x_type, gain_type = _IN[x.dtype], _IN[gain.dtype]
+        res_type = _IN[residual.dtype] if residual is not None else BD_BF16
     if _current_device() != dev:
         with torch.cuda.device(dev):
             return _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales)
     lib = _declared or _library()
-    x_type = _IN[x.dtype]
-    res_type = BD_BF16
-    if residual is not None:
-        res_type = _IN[residual.dtype]
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
     if out is None:
         if out_type != BD_BF16:
             out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
@@ -214,9 +215,9 @@ def _rms_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, 
         scales = torch.empty((*lead, (d + 31) // 32), dtype=torch.uint8, device=x.device)
     st = lib.bd_rms_norm(x.data_ptr(), x_type, residual.data_ptr() if residual is not None else None,
                          residual_out.data_ptr() if residual is not None else None, res_type, gain.data_ptr(),
-                         _IN[gain.dtype], gain.shape[0] if gain.dim() == 2 else 1,
-                         variant_ids.data_ptr() if variant_ids is not None else None, eps, out.data_ptr(), out_type,
-                         scales.data_ptr() if scales is not None else None, math.prod(lead), d, _stream_of(dev))
+                         gain_type, num_gains, variant_ids.data_ptr() if variant_ids is not None else None, eps,
+                         out.data_ptr(), out_type, scales.data_ptr() if scales is not None else None, x.numel() // d,
+                         d, _stream_of(dev))
     if st:
         _check(lib, "bd_rms_norm", st)
     return out, scales, residual_out
@@ -355,7 +356,7 @@ def _cache(kv):
 
 def _index(name, t, n, dev):
     """Whether t is an int32 [n] index on the device, as it nearly always is."""
-    return (type(t) is torch.Tensor and t.dtype == torch.int32 and t.shape == (n,) and t.is_contiguous()
+    return (type(t) is torch.Tensor and t.dtype is _INT and t.shape == (n,) and t.is_contiguous()
             and t.get_device() == dev)
 
 
@@ -464,7 +465,7 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     if not abs(scale) <= 2.0 ** 60:
         raise ValueError("scale must be at most 2^60 (got %r)" % scale)
     if not (lse is None and (out is None or _free(out, q, (B, heads, kv.head_dim), dev)) and type(page_table) is torch.Tensor and page_table.dim() == 2
-            and page_table.dtype == torch.int32 and page_table.shape[0] == B and page_table.is_contiguous()
+            and page_table.dtype is _INT and page_table.shape[0] == B and page_table.is_contiguous()
             and 1 <= page_table.shape[1] <= (1 << 24) // kv.page_size and page_table.get_device() == dev
             and _index("lengths", lengths, B, dev) and q.get_device() == dev and 1 <= heads <= 65535
             and heads % kv.num_heads == 0):
@@ -476,7 +477,10 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     pages = page_table.shape[1]
     nbytes = _attend_bytes(B, heads, kv.num_heads, kv.head_dim, kv.page_size, pages)
     if out is None:
-        out = torch.empty((B, heads, kv.head_dim), dtype=torch.bfloat16, device=kv.device)
+        if kind == BD_BF16 and q.is_contiguous():
+            out = torch.empty_like(q)
+        else:
+            out = torch.empty((B, heads, kv.head_dim), dtype=torch.bfloat16, device=kv.device)
     ws = _workspace(nbytes, kv.device)
     st = lib.bd_attend(kv._ref, q.data_ptr(), kind, qs, heads, page_table.data_ptr(),
                        page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, out.data_ptr(),
