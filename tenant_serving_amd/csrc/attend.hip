@@ -48,7 +48,9 @@ constexpr int kUnit = kWaves * kTile;      // tokens of a unit
 // the registers of two spill but for e4m3 with bf16 queries (8 of 16384 tokens,
 // head_dim 192, 110 -> 81 us; in bf16, 8 of 8192, two would take 86 -> 107).
 constexpr int kCUs = 256;
-constexpr int per_cu(int dim, bool split_q, bool e4m3) { return dim <= 64 ? 3 : dim <= 128 || (e4m3 && !split_q) ? 2 : 1; }
+constexpr int per_cu(int dim, bool split_q, bool e4m3) {
+    return dim <= 64 ? 3 : dim <= 128 || (e4m3 && !split_q) ? 2 : 1;
+}
 // What a row costs beside its units, in units.  Without it the workgroups that
 // get many short rows come last: 64 sequences of up to 16381 tokens in e4m3
 // 187 -> 178 us, 31 of up to 1013 with 32 key-value heads 27.7 -> 22.7 (16 of
@@ -784,7 +786,8 @@ hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
     Args p{a, shape_of(a.B, a.Hq, a.kv.num_heads, a.kv.head_dim, a.kv.page_size, a.max_pages, q_fp32,
                      a.kv.type == BD_E4M3),
            (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride), unit16(a.kv.token_stride),
-           (uint32_t)(a.kv.num_heads * a.kv.page_size), __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f),
+           (uint32_t)(a.kv.num_heads * a.kv.page_size),
+           __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f),
            a.scale < 0.0f ? 0x80008000u : 0u};
     const int D = a.kv.head_dim;
     if (D <= 64) {

@@ -10,25 +10,27 @@
 namespace bd {
 namespace {
 
-// Streaming stores, for what is read back (it goes to the next kernel once) and
-// for long writes, whose rows are read again a layer's worth of other data
-// later (16384 tokens from fp32 to e4m3 38.9 -> 35.8 us, 16169 of 8 rows of 80 in
-// bf16 26.5 -> 21.8).
-__device__ __forceinline__ void store_stream16(uint16_t* p, uint4 v) {
+// What is read back is stored streaming where it is more than the 256 MiB
+// last-level cache would keep for the next kernel: 65536 tokens (268 MB) 80.7 ->
+// 73.5 us, with a kernel that reads it after 153.9 -> 145.5; at 32768 plain stores
+// win with that kernel (65.4 against 70.5; right behind the write of the same
+// tokens the two are within 3% from 4096 to 32768).  What is written to the cache, never:
+// a prefill reads it right after (16384 tokens from fp32 to e4m3 37.0 -> 35.1 us,
+// but their read-back 16.6 -> 20.9).
+constexpr int64_t kStreamBytes = int64_t(192) << 20;
+template <bool kStream>
+__device__ __forceinline__ void store16(uint16_t* p, uint4 v) {
     const u32x4_t w = {v.x, v.y, v.z, v.w};
-    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
-}
-__device__ __forceinline__ void store_stream8(uint8_t* p, uint2 v) {
-    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-    const u32x2_t w = {v.x, v.y};
-    __builtin_nontemporal_store(w, reinterpret_cast<u32x2_t*>(p));
+    if (kStream)
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(p));
+    else
+        *reinterpret_cast<u32x4_t*>(p) = w;
 }
 
 constexpr int kThreads = 256;   // of the read
 // Rows that a lane of the read holds at once, of keys and of values each.
 // 131071 tokens of 8 heads of 128 in e4m3, against one row of either array per
-// lane and plain stores: 192 -> 141 us (5.7 TB/s); one row 147, four 145, two
-// with plain stores 155.
+// lane and plain stores: 192 -> 142 us (5.7 TB/s); one row 147, four 145.
 constexpr int kReadRows = 2;
 // The write: up to kSmallWrite tokens by workgroups of 256 lanes (1..2 tokens
 // each), more by at most 1024 of 1024 lanes (up to 32 tokens each), in slices.
@@ -212,20 +214,12 @@ __global__ __launch_bounds__(kWide) void kv_write_kernel(const WriteArgs a) {
             if (in && keep) {
                 const uint2 w = make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3], inv),
                                            pack_e4m3x4(f[4], f[5], f[6], f[7], inv));
-                uint8_t* p = static_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + to;
-                if (kWide == 256)
-                    *reinterpret_cast<uint2*>(p) = w;
-                else
-                    store_stream8(p, w);
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + to) = w;
             }
             if (lane == 0 && keep)
                 (is_v ? a.kv.v_scales : a.kv.k_scales)[to_scale[i] + (int64_t)head * a.kv.page_size] = (uint8_t)byte;
         } else if (in && keep) {
-            uint16_t* p = static_cast<uint16_t*>(is_v ? a.kv.v : a.kv.k) + to;
-            if (kWide == 256)
-                *reinterpret_cast<uint4*>(p) = narrow_bf16x8(f);
-            else
-                store_stream16(p, narrow_bf16x8(f));
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.kv.v : a.kv.k) + to) = narrow_bf16x8(f);
         }
     }
 }
@@ -270,7 +264,7 @@ struct ReadArgs {
 
 // A lane reads its piece of kRows rows of keys and of as many rows of values
 // before it writes any of them.
-template <bool kE4m3, int kLanes>
+template <bool kE4m3, int kLanes, bool kStream>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(const ReadArgs a) {
     constexpr int kPer = kThreads / kLanes;  // rows at a time
     const int e = ((int)threadIdx.x % kLanes) * 8;
@@ -302,8 +296,8 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(const ReadArgs a) {
         if (r >= a.rows) break;
         const bool past = slot[i] >= a.capacity;
         const uint4 nan = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-        store_stream16(a.k_out + r * a.kv.head_dim + e, past ? nan : x[i][0].value());
-        store_stream16(a.v_out + r * a.kv.head_dim + e, past ? nan : x[i][1].value());
+        store16<kStream>(a.k_out + r * a.kv.head_dim + e, past ? nan : x[i][0].value());
+        store16<kStream>(a.v_out + r * a.kv.head_dim + e, past ? nan : x[i][1].value());
     }
 }
 
@@ -327,7 +321,7 @@ void write_lanes(const WriteArgs& a, hipStream_t s) {
         write_wide<kX32, kE4m3, 32>(a, s);
 }
 
-template <bool kE4m3>
+template <bool kE4m3, bool kStream>
 void read_lanes(ReadArgs a, hipStream_t s) {
     const int lanes = a.kv.head_dim / 8 <= 8 ? 8 : a.kv.head_dim / 8 <= 16 ? 16 : 32;
     const int64_t per = kThreads / lanes;
@@ -342,12 +336,20 @@ void read_lanes(ReadArgs a, hipStream_t s) {
         b.rows = n * a.kv.num_heads;
         const dim3 grid((unsigned)((b.rows + per * kReadRows - 1) / (per * kReadRows))), block(kThreads);
         if (lanes == 8)
-            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 8>), grid, block, 0, s, b);
+            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 8, kStream>), grid, block, 0, s, b);
         else if (lanes == 16)
-            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 16>), grid, block, 0, s, b);
+            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 16, kStream>), grid, block, 0, s, b);
         else
-            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 32>), grid, block, 0, s, b);
+            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 32, kStream>), grid, block, 0, s, b);
     }
+}
+
+template <bool kE4m3>
+void read_any(const ReadArgs& a, hipStream_t s) {
+    if (a.rows * a.kv.head_dim * 4 >= kStreamBytes)
+        read_lanes<kE4m3, true>(a, s);
+    else
+        read_lanes<kE4m3, false>(a, s);
 }
 
 }  // namespace
@@ -393,9 +395,9 @@ hipError_t launch_kv_read(const bd_kv& kv, const int32_t* slots, int64_t T, uint
     const ReadArgs a{kv, slots, k_out, v_out, T * kv.num_heads, Div((uint32_t)kv.page_size),
                      Div((uint32_t)kv.num_heads), (int32_t)(kv.num_pages * kv.page_size)};
     if (kv.type == BD_E4M3)
-        read_lanes<true>(a, stream);
+        read_any<true>(a, stream);
     else
-        read_lanes<false>(a, stream);
+        read_any<false>(a, stream);
     return hipGetLastError();
 }
 

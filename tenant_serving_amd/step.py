@@ -257,7 +257,8 @@ class bd_kv_cache:
         kind = _typed("k", k, _HELD)
         _tensor("v", v)
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
-            raise ValueError("k and v must be alike: [num_pages, num_heads, page_size, head_dim], one dtype, one layout")
+            raise ValueError("k and v must be alike: [num_pages, num_heads, page_size, head_dim], one dtype, "
+                             "one layout")
         pages, heads, page, dim = k.shape
         if pages < 1 or not 1 <= heads <= 65535 or page % 8 or not 8 <= page <= 4096:
             raise ValueError("need pages, 1..65535 heads and a page size that is a multiple of 8, 8..4096 (got %s)"
@@ -425,7 +426,8 @@ def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
     """The checks of an attention's tensors, in full; raises or returns."""
     B = q.shape[0]
     if heads < 1 or heads > 65535 or heads % kv.num_heads:
-        raise ValueError("q's heads must be a multiple of the cache's %d, at most 65535 (got %d)" % (kv.num_heads, heads))
+        raise ValueError("q's heads must be a multiple of the cache's %d, at most 65535 (got %d)"
+                         % (kv.num_heads, heads))
     _tensor("page_table", page_table)
     if page_table.dtype != torch.int32:
         raise TypeError("page_table must be torch.int32 (got %s)" % page_table.dtype)
@@ -464,7 +466,8 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     scale = kv.head_dim ** -0.5 if scale is None else float(scale)
     if not abs(scale) <= 2.0 ** 60:
         raise ValueError("scale must be at most 2^60 (got %r)" % scale)
-    if not (lse is None and (out is None or _free(out, q, (B, heads, kv.head_dim), dev)) and type(page_table) is torch.Tensor and page_table.dim() == 2
+    if not (lse is None and (out is None or _free(out, q, (B, heads, kv.head_dim), dev))
+            and type(page_table) is torch.Tensor and page_table.dim() == 2
             and page_table.dtype is _INT and page_table.shape[0] == B and page_table.is_contiguous()
             and 1 <= page_table.shape[1] <= (1 << 24) // kv.page_size and page_table.get_device() == dev
             and _index("lengths", lengths, B, dev) and q.get_device() == dev and 1 <= heads <= 65535
