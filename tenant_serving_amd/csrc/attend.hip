@@ -32,7 +32,8 @@
 // itself.  The loads of a tile are in flight while the one before it is worked
 // on, across the ends of rows too.  A row of units that ends up in several workgroups leaves fp32
 // partial results (sum, maximum, unnormalised output) in the workspace, and
-// join_kernel adds them in workgroup order.
+// join_kernel adds them in workgroup order.  Where the table has room for few
+// units a row stays in one piece instead, and nothing is joined.
 #include "step_internal.h"
 
 namespace bd {
@@ -41,15 +42,27 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kTile = 32;                  // tokens of a wave
 constexpr int kUnit = kWaves * kTile;      // tokens of a unit
+// A kernel's width: head_dim rounded up to 64, 96, 128, 192 or 256.  96 and 192
+// against the next power of two, for which a load's lanes would idle: 31
+// sequences of up to 1013 tokens, 32 heads, e4m3, 37.0 -> 30.8 us at 96 and 73.2
+// -> 48.3 at 192 (fp32 queries).  Head sizes between go where their value loads
+// are the better ones: 80 in bf16 to 128 (lanes of 8 columns, not 4 and 2; 64
+// sequences of up to 2048, 32 heads, 148 there, 181 at 96), 144 to 176 in e4m3
+// to 256 (of 16 columns, not 8 and 4; 176: 177 there, 206 at 192).
+constexpr int width_of(int dim, bool e4m3) {
+    return dim <= 64 ? 64 : dim == 96 || (dim < 96 && e4m3) ? 96 : dim <= 128 ? 128 :
+           dim == 192 || (dim < 192 && !e4m3) ? 192 : 256;
+}
 // Workgroups at most: what 256 CUs hold of them by their registers and LDS, so
-// that all start at once.  Three per CU at head_dim 64 (against two, 31
+// that all start at once.  Three per CU at width 64 (against two, 31
 // sequences of 4000 tokens, 32 heads, e4m3: 135 -> 117 us), two at 128 (with
-// 768 of them for 512 places, 64 of 8192 tokens in e4m3 173 -> 230 us).  At 256
-// the registers of two spill but for e4m3 with bf16 queries (8 of 16384 tokens,
-// head_dim 192, 110 -> 81 us; in bf16, 8 of 8192, two would take 86 -> 107).
+// 768 of them for 512 places, 64 of 8192 tokens in e4m3 173 -> 230 us) and at
+// 192 (31 of up to 1013 tokens, 32 heads, e4m3: one 61.2, two 48.4).  At 256
+// the registers of two spill but for e4m3 with bf16 queries (in bf16, 8 of 8192
+// tokens, two would take 86 -> 107).
 constexpr int kCUs = 256;
-constexpr int per_cu(int dim, bool split_q, bool e4m3) {
-    return dim <= 64 ? 3 : dim <= 128 || (e4m3 && !split_q) ? 2 : 1;
+constexpr int per_cu(int width, bool split_q, bool e4m3) {
+    return width <= 64 ? 3 : width <= 192 || (e4m3 && !split_q) ? 2 : 1;
 }
 // What a row costs beside its units, in units.  Without it the workgroups that
 // get many short rows come last: 64 sequences of up to 16381 tokens in e4m3
@@ -65,6 +78,7 @@ struct Shape {
     int32_t rows;                               // rows of units per sequence: heads * tiles
     int32_t capacity, groups;                   // tokens a table row holds; workgroups launched
     int32_t crosses, by_row;                    // entries of the workspace's table
+    int32_t whole;                              // rows stay in one piece, see is_whole
 };
 
 struct Args {
@@ -206,12 +220,16 @@ struct Dwords {
 template <int N>
 __device__ __forceinline__ Dwords<N> load_dwords(const void* p) {
     Dwords<N> r;
-    if constexpr (N == 1) {
+    if constexpr (N == 0) {
+    } else if constexpr (N == 1) {
         r.d[0] = *static_cast<const uint32_t*>(p);  // rows of half a cache line, whose other half comes next
     } else if constexpr (N == 2) {
         typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
         const u32x2_t v = __builtin_nontemporal_load(static_cast<const u32x2_t*>(p));
         r.d[0] = v.x, r.d[1] = v.y;
+    } else if constexpr (N % 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.d[i] = __builtin_nontemporal_load(static_cast<const uint32_t*>(p) + i);
     } else {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
@@ -229,33 +247,41 @@ __device__ __forceinline__ void clear(Dwords<N>& r) {
 
 __device__ __forceinline__ void flip(uint4& v, uint32_t mask) { v.x ^= mask, v.y ^= mask, v.z ^= mask, v.w ^= mask; }
 
-// kDC: head_dim rounded up to 64, 128 or 256.  kFull: head_dim is kDC.
+// kDC: the width, see width_of.  kFull: head_dim is kDC.
 // kSplitQ: fp32 queries as two bf16 terms.
 template <int kDC, bool kFull, bool kE4m3, bool kSplitQ>
 __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void attend_kernel(const Args p) {
     constexpr int NS = kDC / 32;              // k-steps of a score product
-    constexpr int DV = kDC / 16;              // value columns of a lane
-    constexpr int KL = kE4m3 ? NS / 2 : NS;   // 16-byte loads of a key row per lane
-    constexpr int VD = kE4m3 ? DV / 4 : DV / 2;  // dwords of a value row per lane
     constexpr int kSize = kE4m3 ? 1 : 2;      // bytes of a held value
+    constexpr int KL = (NS * kSize + 1) / 2;  // loads of a key row per lane: 16 bytes each, but
+    constexpr bool kOdd = kE4m3 && NS % 2;    // the last one 8 (one k-step of codes)
+    // Value columns of a lane: DV1 neighbouring ones of the first 16 DV1, and
+    // where those are not all, DV2 neighbouring ones of the rest (at 96 and 192,
+    // where a lane's share of all columns is no load's size, or ends past head_dim).
+    constexpr int DV = kDC / 16, DV1 = DV % 3 == 0 && (!kFull || DV * kSize % 4) ? DV / 3 * 2 : DV, DV2 = DV - DV1;
+    constexpr int kMin = kDC == 64 ? 0 : kDC <= 128 ? 64 : 128;  // head_dim is more than that
+    constexpr int VD = (DV * kSize + 3) / 4;  // dwords of a value row per lane
+    constexpr int VB1 = DV1 * kSize, VB2 = DV2 * kSize;
     constexpr int kPad = kDC + 4;
-    // Two of each, used in turn by the rows: one barrier a row.  At head_dim
-    // 256 with e4m3 and bf16 queries one, and the queries in LDS instead of
-    // registers, or a CU would hold one workgroup instead of two.
-    constexpr bool kTight = kDC == 256 && per_cu(kDC, kSplitQ, kE4m3) == 2;
-    constexpr int kTurns = kTight ? 1 : 2;
+    // Two of each, used in turn by the rows: one barrier a row.  Past head_dim
+    // 128 one, where a CU then holds two workgroups instead of one; at 256, and
+    // for fp32 queries on bf16 keys, with the queries in LDS instead of registers.
+    constexpr bool kOneTurn = kDC > 128 && per_cu(kDC, kSplitQ, kE4m3) == 2;
+    constexpr bool kTight = kOneTurn && (kDC == 256 || (kSplitQ && !kE4m3));
+    constexpr int kTurns = kOneTurn ? 1 : 2;
     __shared__ float so[kTurns][kWaves][16][kPad];
     __shared__ float sm[kTurns][kWaves][16], sl[kTurns][kWaves][16];
     __shared__ uint4 sq[kTight ? (kSplitQ ? 2 : 1) : 1][kTight ? NS : 1][64];
-    constexpr int NR = kTight ? NS / kWaves : NS;  // k-steps whose queries a wave loads
+    constexpr int NR = kTight ? (NS + kWaves - 1) / kWaves : NS;  // k-steps whose queries a wave loads
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
-    // where no row has more than one unit, the line needs no lengths
-    const bool single = p.s.capacity <= kUnit;
+    // rows in one piece: a row is one place of the line, which needs no lengths
+    const bool whole = p.s.whole;
+    const int cost = whole ? 0 : kRowCost;
     Line line;
-    if (!single) line.scan(p);
-    const Cut cut(single ? p.a.B * p.s.rows * (kRowCost + 1) : line.total, p.s.groups);
+    if (!whole) line.scan(p);
+    const Cut cut(whole ? p.a.B * p.s.rows : line.total, p.s.groups);
     const int w = blockIdx.x;
     Cross* crosses = reinterpret_cast<Cross*>(p.a.part);
     const bool by_row = p.s.by_row;
@@ -264,9 +290,9 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
     const int u = cut.start(w);
     const int end = cut.start(w + 1);
     int at, len0, b0;  // the current row's first place; the first sequence
-    if (single) {
-        b0 = u / (p.s.rows * (kRowCost + 1));
-        at = b0 * p.s.rows * (kRowCost + 1);
+    if (whole) {
+        b0 = u / p.s.rows;
+        at = b0 * p.s.rows;
         len0 = uni(p.a.lengths[b0]);
     } else {
         b0 = line.holder_of(p, u, &at, &len0);
@@ -283,7 +309,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
         x.b = b, x.row = row, x.unit = unit, x.len = len;
         x.un = units_of(len, p.s.capacity);
         const int upto = end - row_at - kRowCost;  // of its units, as far as this workgroup goes
-        x.n = (upto < x.un ? upto : x.un) - unit;
+        x.n = (whole || upto >= x.un ? x.un : upto) - unit;
         x.tokens = len > p.s.capacity || len < 0 ? 0 : len;
         x.t0 = unit * kUnit + wave * kTile;
         x.stop = x.tokens < (unit + x.n) * kUnit ? x.tokens : (unit + x.n) * kUnit;
@@ -292,10 +318,10 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
         x.nq = p.s.group - x.q0 < 16 ? p.s.group - x.q0 : 16;
         return x;
     };
-    const int span0 = kRowCost + units_of(len0, p.s.capacity), row0 = (u - at) / span0;
+    const int span0 = whole ? 1 : kRowCost + units_of(len0, p.s.capacity), row0 = (u - at) / span0;
     at += row0 * span0;
-    if (at + kRowCost >= end) return;  // no unit of its own
-    const int into = u - at - kRowCost;
+    if (at + cost >= end) return;  // no unit of its own
+    const int into = u - at - cost;
     Piece now = piece_at(b0, len0, row0, into > 0 ? into : 0, at);
     bool first_piece = true;
 
@@ -303,7 +329,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
     // page numbers a tile earlier, the keys as soon as the scores are done
     // with the registers, the values after the sums.  A row's first tile and
     // its queries are loaded while the row before it is summed up.
-    Dwords<4> kk[2][KL];
+    Dwords<4> kk[2][KL];  // of the odd one, two
     Dwords<VD> vv[8];
     float ks[2];
     uint2 vs;
@@ -339,8 +365,15 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
 #pragma unroll
             for (int s = 0; s < KL; ++s) {
                 clear(kk[h][s]);
-                if (kFull || (s * 64 + g * 16) / kSize < p.s.dim)
-                    kk[h][s] = load_dwords<4>(static_cast<const char*>(p.a.kv.k) + at + s * 64);
+                const char* k = static_cast<const char*>(p.a.kv.k) + at + s * 64;
+                if (kOdd && s == KL - 1) {
+                    if (kFull || s * 64 + 32 <= kMin || s * 64 + g * 8 < p.s.dim) {
+                        const Dwords<2> r = load_dwords<2>(k - g * 8);
+                        kk[h][s].d[0] = r.d[0], kk[h][s].d[1] = r.d[1];
+                    }
+                } else if (kFull || (s * 64 + 64) / kSize <= kMin || (s * 64 + g * 16) / kSize < p.s.dim) {
+                    kk[h][s] = load_dwords<4>(k);
+                }
             }
             at += 4 * token_bytes;
             if (kE4m3) ks[h] = scale_of(p.a.kv.k_scales[wh.sc + (i16 & 3) + 4 * h]);
@@ -349,12 +382,24 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
     const auto load_values = [&](const Piece& x, Group at_page) {
         const Where wh = locate(p, at_page, x.head);
         bad |= wh.bad;
-        uint64_t at = opaque(wh.at + i16 * DV * kSize);
+        // lanes behind head_dim hold some other columns, which are not used
+        uint64_t at = opaque(wh.at + (kFull || i16 * DV1 < p.s.dim ? i16 * VB1 : 0));
+        const uint32_t rest = DV2 == 0 ? 0 : kFull || 16 * DV1 + i16 * DV2 < p.s.dim ? 16 * VB1 + i16 * VB2 : 0;
+        uint64_t at2 = opaque(wh.at + rest);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            clear(vv[j]);
-            if (kFull || i16 * DV < p.s.dim) vv[j] = load_dwords<VD>(static_cast<const char*>(p.a.kv.v) + at);
+            const Dwords<VB1 / 4> r = load_dwords<VB1 / 4>(static_cast<const char*>(p.a.kv.v) + at);
+#pragma unroll
+            for (int i = 0; i < VB1 / 4; ++i) vv[j].d[i] = r.d[i];
             at += token_bytes;
+            if constexpr (VB2 == 2) {
+                vv[j].d[VD - 1] = *reinterpret_cast<const uint16_t*>(static_cast<const char*>(p.a.kv.v) + at2);
+            } else {
+                const Dwords<VB2 / 4> r2 = load_dwords<VB2 / 4>(static_cast<const char*>(p.a.kv.v) + at2);
+#pragma unroll
+                for (int i = 0; i < VB2 / 4; ++i) vv[j].d[VB1 / 4 + i] = r2.d[i];
+            }
+            if constexpr (DV2 > 0) at2 += token_bytes;
         }
         if (kE4m3) vs = *reinterpret_cast<const uint2*>(p.a.kv.v_scales + wh.sc);
     };
@@ -365,9 +410,9 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const int s = kTight ? i * kWaves + wave : i;
-            const int d = kE4m3 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
+            const int d = kE4m3 && !(kOdd && s == NS - 1) ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
             raw[i].zero();
-            if (i16 < x.nq && (kFull || d < p.s.dim)) raw[i].load(p.a.q, at + d);
+            if (s < NS && i16 < x.nq && (kFull || d < p.s.dim)) raw[i].load(p.a.q, at + d);
         }
     };
 
@@ -395,8 +440,8 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
     for (int turn = 0;; turn ^= kTurns - 1) {
         const int t0 = now.t0, stop = now.stop, nq = now.nq, tokens = now.tokens;
         // what comes next, and its first page numbers
-        const int next_at = at + kRowCost + now.un;
-        const bool last = next_at + kRowCost >= end;
+        const int next_at = at + (whole ? 1 : kRowCost + now.un);
+        const bool last = next_at + cost >= end;
         Groups next_pages{};
         if (!last) {
             const Piece next = piece_after(now, next_at);
@@ -420,7 +465,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
             flip(qh[s], p.flip);
             if constexpr (kSplitQ) flip(ql[s], p.flip);
             raw[s].zero();  // not kept through the tiles
-            if constexpr (kTight) {
+            if (kTight && s * kWaves + wave < NS) {
                 sq[0][s * kWaves + wave][lane] = qh[s];
                 if constexpr (kSplitQ) sq[1][s * kWaves + wave][lane] = ql[s];
             }
@@ -611,7 +656,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
         }
 
         // the wave's result, then the workgroup's: heads i16, values
-        // (4 g + r) DV + j of acc[j][r]
+        // (4 g + r) DV1 + j of acc[j][r], 16 DV1 + (4 g + r) DV2 + j of acc[DV1 + j][r]
         l += __shfl_xor(l, 16, 64);
         l += __shfl_xor(l, 32, 64);
         if (was_bad) l = __builtin_nanf("");
@@ -620,19 +665,30 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int j = 0; j < DV; j += 4)
-                    *reinterpret_cast<float4*>(&so[turn][wave][i16][(4 * g + r) * DV + j]) =
-                        make_float4(acc[j][r], acc[j + 1][r], acc[j + 2][r], acc[j + 3][r]);
+                for (int j = 0; j < DV1; j += DV1 % 4 ? 2 : 4) {
+                    float* o = &so[turn][wave][i16][(4 * g + r) * DV1 + j];
+                    if constexpr (DV1 % 4)
+                        *reinterpret_cast<float2*>(o) = make_float2(acc[j][r], acc[j + 1][r]);
+                    else
+                        *reinterpret_cast<float4*>(o) =
+                            make_float4(acc[j][r], acc[j + 1][r], acc[j + 2][r], acc[j + 3][r]);
+                }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = DV1; j < DV; j += 2)
+                    *reinterpret_cast<float2*>(&so[turn][wave][i16][16 * DV1 + (4 * g + r) * DV2 + j - DV1]) =
+                        make_float2(acc[j][r], acc[j + 1][r]);
         }
         __syncthreads();
 
-        const bool whole = now.n == now.un;
+        const bool all = now.n == now.un;
         const int which = first_piece ? 0 : 1;
         const int d4 = p.s.dim / 4;
-        float* part = whole ? nullptr : place(p, w, which);
-        if (now.unit == 0 && crosses && threadIdx.x == 0 && (by_row || !whole)) {
+        float* part = all ? nullptr : place(p, w, which);
+        if (now.unit == 0 && crosses && threadIdx.x == 0 && (by_row || !all)) {
             const int id = now.b * p.s.rows + now.row;
-            crosses[by_row ? id : w] = Cross{id, whole ? -1 : w * 2 + which, cut.group_of(next_at - 1), 0};
+            crosses[by_row ? id : w] = Cross{id, all ? -1 : w * 2 + which, cut.group_of(next_at - 1), 0};
         }
         for (int i = threadIdx.x; i < nq * d4; i += kWaves * 64) {
             const int q = i / d4, d = (i - q * d4) * 4;
@@ -648,7 +704,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
                 L += sl[turn][v][q] * f;
                 o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
             }
-            if (whole) {
+            if (all) {
                 const float inv = now.len <= 0 ? 0.0f : 1.0f / L;
                 const int64_t at = (int64_t)now.b * p.a.Hq + now.head * p.s.group + now.q0 + q;
                 *reinterpret_cast<uint2*>(p.a.out + at * p.s.dim + d) =
@@ -661,7 +717,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
             }
         }
         if (last) break;
-        if constexpr (kTight) __syncthreads();
+        if constexpr (kOneTurn) __syncthreads();
         at = next_at;
         now = next;
         first_piece = false;
@@ -732,8 +788,25 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
     }
 }
 
-Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages, bool q_fp32,
-               bool e4m3) {
+// Whether each row stays in one piece, a workgroup to a row: then no join is
+// launched (4 to 5 us) and no lengths are scanned, but the longest row is the
+// shortest time, and nothing evens the others out.  Split against whole (us;
+// rows of equal length / random ones up to it):
+//   head_dim 64, e4m3, fp32 queries: 64 rows of 768 tokens 15.6 -> 12.0 / 14.2
+//     -> 10.9, of 1024 13.6 -> 15.0; 512 rows of 1024 24.4 -> 18.9 / 19.4 ->
+//     16.5, of 1536 30.1 -> 25.3 / 21.6 -> 22.8, of 2048 34.9 -> 32.4 / 23.6 -> 27.5
+//   head_dim 128, bf16: 64 rows of 384 tokens 13.9 -> 11.4, of 768 15.2 -> 16.7;
+//     256 rows of 768 28.3 -> 21.2 / 20.6 -> 17.9, of 1024 32.9 -> 26.6 / 22.1 ->
+//     21.7; 768 of 1024 74.9 -> 66.9 / 47.4 -> 53.8
+// and at 192 and 256, 256 or more rows of 768 gain 0 to 33% (e4m3 and bf16,
+// but 512 random ones in bf16 at 256: 10% lost).
+bool is_whole(int64_t rows, int64_t capacity, int64_t D) {
+    const int units = D <= 64 ? (rows < 256 ? 6 : rows < 512 ? 8 : 12) : rows < 256 ? 3 : 6;
+    return capacity <= units * kUnit;
+}
+
+// per_cu: workgroups per CU at most
+Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages, int per_cu) {
     Shape s;
     s.heads = (int32_t)H;
     s.dim = (int32_t)D;
@@ -746,14 +819,17 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     s.tiles = (s.group + 15) / 16;
     s.rows = s.heads * s.tiles;
     s.capacity = (int32_t)(page_size * max_pages);
-    const int64_t per_row = s.capacity <= kUnit ? 1 : (s.capacity + kUnit - 1) / kUnit;
-    const int64_t units = B * s.rows * (per_row == 1 ? 1 : per_row + kRowCost);
-    // a capacity of one unit splits nothing: a workgroup per row of units
-    const int64_t most = per_row == 1 ? int64_t(1) << 20 : kCUs * per_cu((int)D, q_fp32, e4m3);
+    s.whole = is_whole(B * s.rows, s.capacity, D);
+    const int64_t units = B * s.rows * (s.whole ? 1 : (s.capacity + kUnit - 1) / kUnit + kRowCost);
+    const int64_t most = s.whole ? int64_t(1) << 20 : kCUs * per_cu;
     s.groups = (int32_t)(units < most ? units : most);
     s.by_row = B * s.rows <= s.groups;
     s.crosses = s.by_row ? (int32_t)(B * s.rows) : s.groups;
     return s;
+}
+
+size_t workspace_of(const Shape& s) {
+    return s.whole ? 0 : (size_t)s.crosses * sizeof(Cross) + (size_t)s.groups * 2 * 16 * (s.dim + 2) * sizeof(float);
 }
 
 template <int kDC, bool kFull>
@@ -775,39 +851,36 @@ void go(const Args& p, bool q_fp32, hipStream_t s) {
 }  // namespace
 
 size_t attend_workspace_bytes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages) {
-    if (page_size * max_pages <= kUnit) return 0;
-    // bf16 queries on e4m3: no fewer workgroups than any other call's
-    const Shape s = shape_of(B, Hq, H, D, page_size, max_pages, false, true);
-    return (size_t)s.crosses * sizeof(Cross) + (size_t)s.groups * 2 * 16 * (D + 2) * sizeof(float);
+    // the size does not know the types: as for those that take the most workgroups
+    int most = 1;
+    for (int types = 0; types < 4; ++types) {
+        const int n = per_cu(width_of((int)D, types & 2), types & 1, types & 2);
+        most = n > most ? n : most;
+    }
+    const Shape s = shape_of(B, Hq, H, D, page_size, max_pages, most);
+    return workspace_of(s);
 }
 
 hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
     const auto unit16 = [&](int64_t stride) { return (uint32_t)(stride * (a.kv.type == BD_E4M3 ? 1 : 2) / 16); };
-    Args p{a, shape_of(a.B, a.Hq, a.kv.num_heads, a.kv.head_dim, a.kv.page_size, a.max_pages, q_fp32,
-                     a.kv.type == BD_E4M3),
+    Args p{a, shape_of(a.B, a.Hq, a.kv.num_heads, a.kv.head_dim, a.kv.page_size, a.max_pages,
+                     per_cu(width_of(a.kv.head_dim, a.kv.type == BD_E4M3), q_fp32, a.kv.type == BD_E4M3)),
            (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride), unit16(a.kv.token_stride),
            (uint32_t)(a.kv.num_heads * a.kv.page_size),
            __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f),
            a.scale < 0.0f ? 0x80008000u : 0u};
     const int D = a.kv.head_dim;
-    if (D <= 64) {
-        if (D == 64)
-            go<64, true>(p, q_fp32, stream);
-        else
-            go<64, false>(p, q_fp32, stream);
-    } else if (D <= 128) {
-        if (D == 128)
-            go<128, true>(p, q_fp32, stream);
-        else
-            go<128, false>(p, q_fp32, stream);
-    } else {
-        if (D == 256)
-            go<256, true>(p, q_fp32, stream);
-        else
-            go<256, false>(p, q_fp32, stream);
+    if (workspace_of(p.s) > attend_workspace_bytes(a.B, a.Hq, a.kv.num_heads, D, a.kv.page_size, a.max_pages))
+        return hipErrorInvalidValue;  // what is laid out here is what the caller was told to bring
+    switch (width_of(D, a.kv.type == BD_E4M3)) {
+        case 64: D == 64 ? go<64, true>(p, q_fp32, stream) : go<64, false>(p, q_fp32, stream); break;
+        case 96: D == 96 ? go<96, true>(p, q_fp32, stream) : go<96, false>(p, q_fp32, stream); break;
+        case 128: D == 128 ? go<128, true>(p, q_fp32, stream) : go<128, false>(p, q_fp32, stream); break;
+        case 192: D == 192 ? go<192, true>(p, q_fp32, stream) : go<192, false>(p, q_fp32, stream); break;
+        default: D == 256 ? go<256, true>(p, q_fp32, stream) : go<256, false>(p, q_fp32, stream);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.s.capacity <= kUnit) return e;
+    if (e != hipSuccess || p.s.whole) return e;
     // about two workgroups per CU: a row's heads on as many as that leaves
     const int nq = p.s.group < 16 ? p.s.group : 16;
     const int per = 2 * kCUs / p.s.crosses < 1 ? 1 : 2 * kCUs / p.s.crosses;

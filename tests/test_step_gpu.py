@@ -618,7 +618,7 @@ def test_attend_through_the_c_abi(bd):
         B, hq, D = q.shape
         gq, gt, gl = q.to(DEV), table.to(DEV), lens_t.to(DEV)
         need = lib.bd_attend_workspace_bytes(B, hq, 2, D, page, table.shape[1])
-        assert (need == 0) == (table.shape[1] * page <= 128)
+        assert (need == 0) == (table.shape[1] * page <= 384)
         mem = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device=DEV)
         out = torch.empty((B, hq, D), dtype=BF, device=DEV)
         lse = torch.empty((B, hq), dtype=F32, device=DEV)
@@ -630,6 +630,53 @@ def test_attend_through_the_c_abi(bd):
             assert st == 0
             check_attend(c, q, lens, slots, out, lse, D ** -0.5)
         assert (mem[:4096] == 0xA5).all() and (mem[4096 + need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("dim", [64, 80, 96, 112, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("kind", [BF, E4])
+@pytest.mark.parametrize("q_t", [BF, F32])
+def test_attend_dims(bd, dim, kind, q_t):
+    """Every head size and type with more units than workgroups, in a workspace of just the size asked for, which knows
+    no types: nothing is written around it.  Then rows of few units, which no two workgroups share."""
+    import ctypes
+    from tenant_serving_amd import step
+    lib = step._library()
+    for base, B, rows in (([1930, 97, 0, 700], 260, (0, 1, 2, 3, 131, 136, 259)), ([380, 61, 0, 129], 20, range(20))):
+        print("attend dims", dim, kind, q_t, B, flush=True)
+        c, q, table, lens_t, slots = attend_case(bd, base, 2, 3, dim, 16, kind, q_t, "tokens")
+        # the base's sequences again and again, with the same pages
+        pick = torch.arange(B) * 3 % 4
+        first = np.concatenate([[0], np.cumsum(base)])
+        lens = [base[i] for i in pick]
+        slots = [t for i in pick for t in slots[first[i]:first[i + 1]]]
+        q, table, lens_t = (q[pick] * torch.linspace(0.5, 1, B)[:, None, None]).to(q_t), table[pick], lens_t[pick]
+        hq = q.shape[1]
+        gq, gt, gl = q.to(DEV), table.to(DEV), lens_t.to(DEV)
+        need = lib.bd_attend_workspace_bytes(B, hq, 2, dim, 16, table.shape[1])
+        assert (need > 0) == (B == 260)
+        mem = torch.full((need + (16 << 20),), 0xA5, dtype=torch.uint8, device=DEV)
+        out = torch.empty((B, hq, dim), dtype=BF, device=DEV)
+        lse = torch.empty((B, hq), dtype=F32, device=DEV)
+        st = lib.bd_attend(c.kv._ref, gq.data_ptr(), step._IN[q_t], step._Pair(hq * dim, dim), hq, gt.data_ptr(),
+                           table.shape[1], table.shape[1], gl.data_ptr(), B, dim ** -0.5, out.data_ptr(),
+                           lse.data_ptr(), mem.data_ptr() + (8 << 20), need,
+                           ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert st == 0
+        check_attend(c, q, lens, slots, out, lse, dim ** -0.5, rows)
+        assert (mem[:8 << 20] == 0xA5).all() and (mem[(8 << 20) + need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("B,page", [(5, 16), (66, 16), (300, 8), (1 << 20, 8), ((1 << 20) + 5, 8)])
+def test_attend_rows_in_one_piece(bd, B, page):
+    """Rows that are not split: few and many, up to more of them than workgroups, among empty and one-token ones."""
+    lens = [0, 1, 30, 64, 130, 7, 128, 129] if page == 16 else [0, 1, 8, 3]
+    c, q, table, lens_t, slots = attend_case(bd, lens, 1, 2, 16, page, E4, BF)
+    pick = torch.arange(B) * 5 % len(lens)
+    out, lse = run_attend(bd, c, q[pick].contiguous(), table[pick].contiguous(), lens_t[pick].contiguous())
+    alone, alone_lse = run_attend(bd, c, q, table, lens_t)
+    check_attend(c, q, lens, slots, alone, alone_lse, 0.25)
+    pick = pick.to(DEV)
+    assert same_bits(out, alone[pick]) and same_bits(lse, alone_lse[pick])
 
 
 def test_attend_fp32_queries_and_infinite_keys(bd):

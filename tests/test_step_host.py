@@ -83,9 +83,9 @@ def test_kv_refusals(lib):
 
 def test_attend_refusals(lib):
     kv = _kv()
-    need = lib.bd_attend_workspace_bytes(2, 4, 2, 64, 16, 20)
+    need = lib.bd_attend_workspace_bytes(2, 4, 2, 64, 16, 100)
     assert need > 0
-    base = dict(kv=ctypes.byref(kv), q=FAKE, q_type=0, qs=_pair(256, 64), heads=4, table=FAKE, stride=20, pages=20,
+    base = dict(kv=ctypes.byref(kv), q=FAKE, q_type=0, qs=_pair(256, 64), heads=4, table=FAKE, stride=100, pages=100,
                 lengths=FAKE, B=2, scale=0.125, out=FAKE, lse=FAKE, ws=FAKE, bytes=need, stream=None)
     call = lambda **c: lib.bd_attend(*{**base, **c}.values())  # noqa: E731
     for change, want in [(dict(kv=None), NULL), (dict(q=None), NULL), (dict(qs=None), NULL), (dict(table=None), NULL),
@@ -103,10 +103,12 @@ def test_attend_refusals(lib):
 
 def test_workspace_query(lib):
     f = lib.bd_attend_workspace_bytes
-    assert f(2, 4, 2, 64, 16, 8) == 0                       # 128 tokens at most: nothing is split
+    # a few hundred tokens at most: nothing is split
+    assert f(2, 4, 2, 64, 16, 8) == f(2, 4, 2, 64, 16, 24) == f(2, 4, 2, 256, 16, 24) == f(512, 4, 2, 256, 16, 48) == 0
     # two places for each workgroup, of 16 heads' sums, maxima and outputs; workgroups for every unit at most
     place = 16 * 66 * 4
-    assert 4 * 2 * 2 * place <= f(2, 4, 2, 64, 16, 9) <= 4 * (2 + 2) * 2 * place + 4096
+    assert 4 * 13 * 2 * place <= f(2, 4, 2, 64, 16, 100) <= 4 * (13 + 2) * 2 * place + 4096
+    assert f(512, 4, 2, 256, 16, 49) > 0
     assert f(64, 64, 8, 128, 16, 1024) == f(128, 64, 8, 128, 16, 1024)   # no more than the GPU's workgroups
     for bad in [(0, 4, 2, 64, 16, 9), (2, 3, 2, 64, 16, 9), (2, 4, 0, 64, 16, 9), (2, 4, 2, 72, 16, 9),
                 (2, 4, 2, 64, 12, 9), (2, 4, 2, 64, 16, 0), (2, 4, 2, 64, 16, 1 << 21)]:
