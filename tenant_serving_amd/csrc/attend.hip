@@ -736,8 +736,12 @@ __device__ __forceinline__ void add_part(float& M, float& L, float4& o, float m,
 }
 
 // Rows of units that several workgroups worked on: out = sum of their partial
-// outputs over the sum of their sums, each scaled to the common maximum.  The
-// heads of a row are shared out over grid y.
+// outputs over the sum of their sums, each scaled to the common maximum.  A
+// row's outputs are shared out over grid y, 4 values of one head to an item; the
+// lanes that a workgroup has beyond its items share out the partial results.
+// Bound by latency: the table's entry, then the partial results (1 row of 57908
+// tokens, 5 heads of 128, e4m3, 453 of them: a workgroup per head 11.6 us, one
+// per 8 items, whose lanes' sums are added in pairs, 6.0).
 __global__ __launch_bounds__(256) void join_kernel(const Args p) {
     __shared__ float4 red[256];
     __shared__ float redm[256], redl[256];
@@ -747,15 +751,15 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
     const int b = cross.id / p.s.rows, row = cross.id - b * p.s.rows;
     const int head = row / p.s.tiles, q0 = (row - head * p.s.tiles) * 16;
     const int nq = p.s.group - q0 < 16 ? p.s.group - q0 : 16;
-    // this workgroup's heads, and its work: 4 values of one head per item
-    const int qa = nq * (int)blockIdx.y / (int)gridDim.y, qe = nq * ((int)blockIdx.y + 1) / (int)gridDim.y;
-    const int lanes = p.s.dim / 4, items = (qe - qa) * lanes;
+    const int lanes = p.s.dim / 4, all = nq * lanes;
+    const int first = all * (int)blockIdx.y / (int)gridDim.y;
+    const int items = all * ((int)blockIdx.y + 1) / (int)gridDim.y - first;
     // lanes beyond the items take every sets-th partial result
     const int sets = items >= 256 ? 1 : items > 0 ? 256 / items : 1;
     const int set = (int)threadIdx.x / (items < 256 && items > 0 ? items : 256);
     for (int i0 = 0; i0 < items; i0 += 256) {
         const int i = sets > 1 ? (int)threadIdx.x - set * items : i0 + (int)threadIdx.x;
-        const int q = qa + i / lanes, d = i % lanes * 4;
+        const int q = (first + i) / lanes, d = (first + i) % lanes * 4;
         float4 o = make_float4(0, 0, 0, 0);
         float M = kNegInf, L = 0.0f;
         if (i < items && set < sets) {
@@ -771,12 +775,17 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
             redm[threadIdx.x] = M;
             redl[threadIdx.x] = L;
             red[threadIdx.x] = o;
-            __syncthreads();
-            if (set == 0)
-                for (int k = 1; k < sets; ++k) {
-                    const int at = k * items + (int)threadIdx.x;
+            for (int n = sets, half; n > 1; n = half) {
+                half = (n + 1) / 2;
+                __syncthreads();
+                if (set < n - half) {
+                    const int at = (int)threadIdx.x + half * items;
                     add_part(M, L, o, redm[at], redl[at], red[at]);
+                    redm[threadIdx.x] = M;
+                    redl[threadIdx.x] = L;
+                    red[threadIdx.x] = o;
                 }
+            }
         }
         if (set == 0 && i < items) {
             const float inv = 1.0f / L;
@@ -881,11 +890,11 @@ hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.s.whole) return e;
-    // about two workgroups per CU: a row's heads on as many as that leaves
-    const int nq = p.s.group < 16 ? p.s.group : 16;
-    const int per = 2 * kCUs / p.s.crosses < 1 ? 1 : 2 * kCUs / p.s.crosses;
-    hipLaunchKernelGGL(join_kernel, dim3((unsigned)p.s.crosses, (unsigned)(nq < per ? nq : per)), dim3(256), 0, stream,
-                       p);
+    // about two workgroups per CU: a row's items, 8 or more, on as many as that leaves
+    const int most = (p.s.group < 16 ? p.s.group : 16) * D / 32;
+    const int per = 2 * kCUs / p.s.crosses;
+    const int y = most < per ? most : per;
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)p.s.crosses, (unsigned)(y < 1 ? 1 : y)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
