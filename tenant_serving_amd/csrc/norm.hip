@@ -12,8 +12,9 @@
 // A group of 32 columns of the e4m3 result is four neighbouring lanes, whose
 // largest magnitude two lane exchanges give.  For this result the sums and
 // products are 64-bit: in 32 bits a few codes in a million fall on the other
-// side of their border, and the extra work hides behind the memory (8192 x 8192
-// with an fp32 residual 134.9 -> 136.3 us).
+// side of their border.  The extra work hides behind the memory where there is a
+// residual (8192 x 8192 with an fp32 one 134.9 us in 32 bits, 134.5 in 64);
+// without one it is what bounds the call (2048 x 16384 from bf16 32 us, 3.2 TB/s).
 #include "step_internal.h"
 
 #include <type_traits>
@@ -21,16 +22,14 @@
 namespace bd {
 namespace {
 
-// A double as the fp32 next to it whose last bit is odd, unless it is an fp32
-// itself: what is rounded to fewer bits from there (and a comparison with
-// numbers of fewer bits) comes out as from the double.
+// A double cut to fp32, the last bit set where that dropped anything: what is
+// rounded to fewer bits from there (and a comparison with numbers of fewer bits)
+// comes out as from the double.
 __device__ __forceinline__ float to_odd(double y) {
     const float f = (float)y;
-    const double off = y - (double)f;
-    const uint32_t b = __float_as_uint(f);
-    // towards y: one more in magnitude where f fell short of it
-    const uint32_t step = (off > 0.0) == (f > 0.0f) ? 1u : 0xffffffffu;
-    return __uint_as_float(off != 0.0 && off == off && !(b & 1) ? b + step : b);
+    const double back = (double)f;
+    const uint32_t cut = __float_as_uint(f) - (uint32_t)(fabs(back) > fabs(y));
+    return __uint_as_float(cut | (uint32_t)(back != y));
 }
 
 template <int NT>
@@ -140,8 +139,16 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
             uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t b = finite_bits(h[c][i]);
+                const uint32_t b = __float_as_uint(h[c][i]) & 0x7fffffffu;
                 top = b > top ? b : top;
+            }
+            if (__ballot(top >= 0x7f800000u)) {  // rare: what is not finite does not count
+                top = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t b = finite_bits(h[c][i]);
+                    top = b > top ? b : top;
+                }
             }
             // lanes past d hold zeros (or NaN, which counts as 0)
 #pragma unroll
@@ -169,17 +176,26 @@ void go(const NormArgs& a, hipStream_t s) {
     for (int64_t row0 = 0; row0 < a.M; row0 += most) {
         const int64_t n = a.M - row0 < most ? a.M - row0 : most;
         const unsigned grid = (unsigned)(NT == 64 ? (n + 3) / 4 : n);
-        hipLaunchKernelGGL((norm_kernel<kX32, kRes, kE4m3, kStream, NT, C>), dim3(grid), dim3(kNormBlock<NT>), 0, s, a, row0);
+        hipLaunchKernelGGL((norm_kernel<kX32, kRes, kE4m3, kStream, NT, C>), dim3(grid), dim3(kNormBlock<NT>), 0, s, a,
+                           row0);
     }
 }
 
+// Few lanes with several chunks each: their loads are in flight together, and a
+// CU holds several rows.  2048 rows in e4m3 with an fp32 residual, this choice
+// against twice the lanes or the next power of two of chunks: 6000 wide 30.5 ->
+// 28.3 us, 9272 53.8 -> 43.4, 12000 66.2 -> 52.1, 16384 81.5 -> 78.2; past 16384
+// 512 lanes would lose (28672 156.5 -> 165.5).
 template <bool kX32, int kRes, bool kE4m3, bool kStream>
 void pick(const NormArgs& a, hipStream_t s) {
     if (a.d <= 512) return go<kX32, kRes, kE4m3, kStream, 64, 1>(a, s);
     if (a.d <= 2048) return go<kX32, kRes, kE4m3, kStream, 256, 1>(a, s);
     if (a.d <= 4096) return go<kX32, kRes, kE4m3, kStream, 256, 2>(a, s);
+    if (a.d <= 6144) return go<kX32, kRes, kE4m3, kStream, 256, 3>(a, s);
     if (a.d <= 8192) return go<kX32, kRes, kE4m3, kStream, 256, 4>(a, s);
-    if (a.d <= 16384) return go<kX32, kRes, kE4m3, kStream, 1024, 2>(a, s);
+    if (a.d <= 12288) return go<kX32, kRes, kE4m3, kStream, 512, 3>(a, s);
+    if (a.d <= 16384) return go<kX32, kRes, kE4m3, kStream, 512, 4>(a, s);
+    if (a.d <= 24576) return go<kX32, kRes, kE4m3, kStream, 1024, 3>(a, s);
     if (a.d <= 32768) return go<kX32, kRes, kE4m3, kStream, 1024, 4>(a, s);
     return go<kX32, kRes, kE4m3, kStream, 1024, 8>(a, s);
 }

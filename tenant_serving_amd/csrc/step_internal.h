@@ -81,12 +81,12 @@ __device__ __forceinline__ float scale_of(int byte) { return __uint_as_float((ui
 __device__ __forceinline__ float inv_scale_of(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 
 // Four values times inv -> four e4m3 codes (v_cvt_pk_fp8_f32, nearest even).
-// Infinities become NaN here, since the conversion's own answer for them
-// depends on a mode bit.
+// Infinities become NaN here (infinity times zero), since the conversion's own
+// answer for them depends on a mode bit.
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d, float inv) {
-    const float nan = __builtin_nanf("");
     const auto prep = [&](float x) {
-        return (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u ? x * inv : nan;
+        const float t = x * inv;
+        return __builtin_fmaf(t, 0.0f, t);
     };
     int r = __builtin_amdgcn_cvt_pk_fp8_f32(prep(a), prep(b), 0, false);
     r = __builtin_amdgcn_cvt_pk_fp8_f32(prep(c), prep(d), r, true);

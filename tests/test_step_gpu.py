@@ -102,6 +102,30 @@ def test_norm(bd, M, d, x_t, res_t):
         check_e4m3(c[0], c[1], want, d)
 
 
+@pytest.mark.parametrize("d", [6144, 6152, 12288, 12296, 16376, 24576, 24584])
+def test_norm_between_widths(bd, d):
+    test_norm(bd, 2, d, F32, BF)
+    test_norm(bd, 2, d, BF, F32)
+    test_norm(bd, 2, d, BF, None)
+
+
+def test_norm_products_below_fp32(bd):
+    """Products between 0 and the least fp32 number, whose codes are zeros, next to larger ones."""
+    d = 96
+    x = torch.full((3, d), 2.0 ** -30)
+    x[:, ::3] *= -1
+    x[:, 5] = 1.0
+    x[2, 40] = float("nan")
+    gain = torch.full((d,), 2.0 ** -133).to(BF)
+    gain[::7] *= -1
+    gain[5], gain[70] = 2.0 ** -100, 0.0
+    codes, scales = bd.bd_rms_norm_e4m3(x.to(DEV), gain.to(DEV), 1e-5)
+    want, _ = ref.rms_norm(x, gain[None], 1e-5)
+    assert 0 < np.abs(want[0, 6]) < 2.0 ** -150
+    check_e4m3(codes, scales, want, d)
+    assert ((codes[:2].cpu().view(torch.uint8)[:, 6:] & 127) == 0).all()
+
+
 def test_norm_forms(bd):
     x, res, gain, ids = on_gpu(*norm_inputs(6, 72, F32, BF, BF, 4))
     y, r = bd.bd_rms_norm(x, gain, residual=res, variant_ids=ids)
