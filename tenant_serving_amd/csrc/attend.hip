@@ -33,7 +33,7 @@
 // on, across the ends of rows too.  A row of units that ends up in several workgroups leaves fp32
 // partial results (sum, maximum, unnormalised output) in the workspace, and
 // join_kernel adds them in workgroup order.  Where the table has room for few
-// units a row stays in one piece instead, and nothing is joined.
+// units a row stays in one piece instead, and nothing is joined (see is_whole).
 #include "step_internal.h"
 
 namespace bd {
@@ -79,6 +79,7 @@ struct Shape {
     int32_t capacity, groups;                   // tokens a table row holds; workgroups launched
     int32_t crosses, by_row;                    // entries of the workspace's table
     int32_t whole;                              // rows stay in one piece, see is_whole
+    int32_t ordered;                            // of them, a workgroup each, the longest first
 };
 
 struct Args {
@@ -151,6 +152,38 @@ struct Line {
         return uni(b);
     }
 };
+
+// Of at most kSorted sequences the one that has `rank` before it when they are
+// sorted by falling units, then by index.
+constexpr int kSorted = 256;
+__device__ __forceinline__ int sequence_of_rank(const Args& p, int rank, int* length) {
+    const int lane = threadIdx.x & 63;
+    int len[kSorted / 64], units[kSorted / 64];
+#pragma unroll
+    for (int i = 0; i < kSorted / 64; ++i) {
+        const bool own = i * 64 + lane < p.a.B;
+        len[i] = own ? p.a.lengths[i * 64 + lane] : 0;
+        units[i] = own ? units_of(len[i], p.s.capacity) : 0;
+    }
+    for (int u = (p.s.capacity + kUnit - 1) / kUnit; u >= 1; --u) {
+#pragma unroll
+        for (int i = 0; i < kSorted / 64; ++i) {
+            if (i * 64 >= p.a.B) break;
+            const uint64_t of = __ballot(units[i] == u);
+            const int n = __popcll(of);
+            if (rank < n) {
+                const int before =
+                    __builtin_amdgcn_mbcnt_hi((uint32_t)(of >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)of, 0));
+                const int l = uni(__ffsll((unsigned long long)__ballot(before == rank && units[i] == u)) - 1);
+                *length = __builtin_amdgcn_readlane(len[i], l);
+                return i * 64 + l;
+            }
+            rank -= n;
+        }
+    }
+    *length = 0;
+    return 0;  // not reached: the ranks are those of the sequences
+}
 
 // Workgroup w of W takes the places [start(w), start(w + 1)).  A row's units
 // before place u are those of its places before u, less kRowCost: what is cut
@@ -293,7 +326,11 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
     if (whole) {
         b0 = u / p.s.rows;
         at = b0 * p.s.rows;
-        len0 = uni(p.a.lengths[b0]);
+        if (p.s.ordered) {
+            b0 = sequence_of_rank(p, b0, &len0);
+        } else {
+            len0 = uni(p.a.lengths[b0]);
+        }
     } else {
         b0 = line.holder_of(p, u, &at, &len0);
     }
@@ -799,18 +836,26 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
 
 // Whether each row stays in one piece, a workgroup to a row: then no join is
 // launched (4 to 5 us) and no lengths are scanned, but the longest row is the
-// shortest time, and nothing evens the others out.  Split against whole (us;
-// rows of equal length / random ones up to it):
+// shortest time.  With more rows than workgroups at a time they are taken
+// longest first (1024 rows of 128, bf16, random up to 768 tokens 42.0 -> 35.2
+// us), up to kSorted sequences.  Split against whole (us; rows of equal length /
+// random ones up to it):
 //   head_dim 64, e4m3, fp32 queries: 64 rows of 768 tokens 15.6 -> 12.0 / 14.2
 //     -> 10.9, of 1024 13.6 -> 15.0; 512 rows of 1024 24.4 -> 18.9 / 19.4 ->
-//     16.5, of 1536 30.1 -> 25.3 / 21.6 -> 22.8, of 2048 34.9 -> 32.4 / 23.6 -> 27.5
+//     16.5, of 2048 34.9 -> 32.4 / 23.6 -> 27.5
 //   head_dim 128, bf16: 64 rows of 384 tokens 13.9 -> 11.4, of 768 15.2 -> 16.7;
-//     256 rows of 768 28.3 -> 21.2 / 20.6 -> 17.9, of 1024 32.9 -> 26.6 / 22.1 ->
-//     21.7; 768 of 1024 74.9 -> 66.9 / 47.4 -> 53.8
-// and at 192 and 256, 256 or more rows of 768 gain 0 to 33% (e4m3 and bf16,
-// but 512 random ones in bf16 at 256: 10% lost).
-bool is_whole(int64_t rows, int64_t capacity, int64_t D) {
-    const int units = D <= 64 ? (rows < 256 ? 6 : rows < 512 ? 8 : 12) : rows < 256 ? 3 : 6;
+//     256 rows of 1024 26% / 7% less, of 1536 17% less / 8% more; sorted, 1024
+//     rows of 2048 2% / 11% less
+// and alike at 192 and 256.  Sorted rows of 2560 tokens and more are level or
+// better too, but one long row among short ones would be seen by then.
+bool is_whole(int64_t B, int64_t rows, int64_t capacity, int64_t D) {
+    int units;
+    if (B <= kSorted && rows > kCUs * (D <= 64 ? 3 : 2))
+        units = 16;
+    else if (rows >= 256)
+        units = D <= 64 && rows >= 512 ? 12 : 8;
+    else
+        units = D <= 64 ? 6 : 3;
     return capacity <= units * kUnit;
 }
 
@@ -828,10 +873,11 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     s.tiles = (s.group + 15) / 16;
     s.rows = s.heads * s.tiles;
     s.capacity = (int32_t)(page_size * max_pages);
-    s.whole = is_whole(B * s.rows, s.capacity, D);
+    s.whole = is_whole(B, B * s.rows, s.capacity, D);
     const int64_t units = B * s.rows * (s.whole ? 1 : (s.capacity + kUnit - 1) / kUnit + kRowCost);
     const int64_t most = s.whole ? int64_t(1) << 20 : kCUs * per_cu;
     s.groups = (int32_t)(units < most ? units : most);
+    s.ordered = s.whole && s.capacity > kUnit && B <= kSorted && s.groups == B * s.rows && s.groups > kCUs * per_cu;
     s.by_row = B * s.rows <= s.groups;
     s.crosses = s.by_row ? (int32_t)(B * s.rows) : s.groups;
     return s;

@@ -703,6 +703,25 @@ def test_attend_rows_in_one_piece(bd, B, page):
     assert same_bits(out, alone[pick]) and same_bits(lse, alone_lse[pick])
 
 
+@pytest.mark.parametrize("B,heads,dim,kind", [(256, 4, 16, BF), (65, 12, 64, E4), (130, 4, 96, BF)])
+def test_attend_longest_first(bd, B, heads, dim, kind):
+    """More rows in one piece than workgroups at a time, which take them by length: bad lengths among them too."""
+    base = [0, 700, 1, 129, 300, 128, 2, 1023]
+    c, q, table, lens_t, slots = attend_case(bd, base, heads, 1, dim, 8, kind, BF)
+    first = np.concatenate([[0], np.cumsum(base)])
+    pick = torch.arange(B) * 5 % 8
+    lens = [base[i] for i in pick]
+    slots = [t for i in pick for t in slots[first[i]:first[i + 1]]]
+    given = lens_t[pick].clone()
+    bad = list(range(7, B, 50))
+    for i in bad:
+        given[i] = 2 ** 31 - 1 if i % 100 == 7 else 1025
+    out, lse = run_attend(bd, c, q[pick].contiguous(), table[pick].contiguous(), given)
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    fine = [i for i in range(B) if i not in bad]
+    check_attend(c, q[pick], lens, slots, out, lse, dim ** -0.5, fine[:24] + fine[-8:])
+
+
 def test_attend_fp32_queries_and_infinite_keys(bd):
     """fp32 queries against keys with infinities: a score of -infinity drops out, whatever the queries' second term."""
     lens = [70, 300]

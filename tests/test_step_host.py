@@ -104,11 +104,12 @@ def test_attend_refusals(lib):
 def test_workspace_query(lib):
     f = lib.bd_attend_workspace_bytes
     # a few hundred tokens at most: nothing is split
-    assert f(2, 4, 2, 64, 16, 8) == f(2, 4, 2, 64, 16, 24) == f(2, 4, 2, 256, 16, 24) == f(512, 4, 2, 256, 16, 48) == 0
+    assert f(2, 4, 2, 64, 16, 8) == f(2, 4, 2, 64, 16, 24) == f(2, 4, 2, 256, 16, 24) == f(512, 4, 2, 256, 16, 64) == 0
     # two places for each workgroup, of 16 heads' sums, maxima and outputs; workgroups for every unit at most
     place = 16 * 66 * 4
     assert 4 * 13 * 2 * place <= f(2, 4, 2, 64, 16, 100) <= 4 * (13 + 2) * 2 * place + 4096
-    assert f(512, 4, 2, 256, 16, 49) > 0
+    assert f(512, 4, 2, 256, 16, 65) > 0 and f(2, 4, 2, 256, 16, 25) > 0
+    assert f(256, 6, 3, 256, 16, 128) == 0 and f(256, 6, 3, 256, 16, 129) > 0
     assert f(64, 64, 8, 128, 16, 1024) == f(128, 64, 8, 128, 16, 1024)   # no more than the GPU's workgroups
     for bad in [(0, 4, 2, 64, 16, 9), (2, 3, 2, 64, 16, 9), (2, 4, 0, 64, 16, 9), (2, 4, 2, 72, 16, 9),
                 (2, 4, 2, 64, 12, 9), (2, 4, 2, 64, 16, 0), (2, 4, 2, 64, 16, 1 << 21)]:
