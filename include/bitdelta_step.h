@@ -159,7 +159,8 @@ bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t*
  *               tokens of all sequences are split evenly over the GPU; the
  *               fp32 partial results of a sequence that several workgroups
  *               share live there until they are joined, in a fixed order.
- *               Its contents on entry do not matter.
+ *               Its contents on entry do not matter.  Where the table holds
+ *               few tokens for each sequence nothing is split, and it is 0.
  * Scores, the running maximum and sum and the output sums are fp32; fp32
  * queries and the softmax weights enter the matrix products as two bf16
  * terms each, so no input or weight is cut to 8 bits (but where a row of the
