@@ -150,7 +150,9 @@ bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t*
  *               last token in its page does not matter, NaN included.
  *               A length over max_pages * page_size, or a looked-up page
  *               outside [0, num_pages), gives rows of NaN.
- *   scale       multiplies the scores; of any sign, 2^60 at most.
+ *   scale       multiplies the scores q . k; of any sign, 2^60 at most in
+ *               magnitude.  Scores may be of any size before and after it:
+ *               only a q . k itself past fp32's range counts as infinite.
  *   out         [B, num_q_heads, head_dim] bf16, 16-byte aligned.
  *   lse         [B, num_q_heads] fp32, the natural logarithm of
  *               sum_j exp(scale * q . k_j); NULL if not wanted.

@@ -1,8 +1,8 @@
 // Attention of one new token per sequence over the paged key-value cache.
 //
-//   out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c q.k_j - m),  c = scale log2(e)
+//   out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c (q.k_j - m)),  c = scale log2(e)
 //
-// with m the running maximum of c q.k_j: one pass over the cache, which is
+// with m the running maximum of q.k_j: one pass over the cache, which is
 // read exactly once, so the kernel is bound by HBM.
 //
 // Layout.  The query heads that share a key-value head (up to 16 of them) are
@@ -19,8 +19,11 @@
 //           tokens of one value column: a lane loads its piece of 8 value
 //           rows (16 bytes at head_dim 128) and pairs them up with byte
 //           permutes, one per two values.
-// The running maximum moves only when a score passes it by 2^10, which one
+// The running maximum moves only when a weight would pass 2^10, which one
 // compare and a ballot find out: then the wave exchanges maxima and rescales.
+// It is kept as a score, without c: the difference is taken first, so that the
+// largest score's weight is 2^0 however large the scores are (2^(c q.k_j - c m)
+// has the rounding error of c m in its exponent, which is past 128 from 2^31 on).
 // The weights enter as two bf16 terms (their sum holds 16 bits), and so do
 // fp32 queries: the matrix units idle most of the time here, and an output
 // is then as exact as its own rounding.
@@ -69,7 +72,7 @@ constexpr int per_cu(int width, bool split_q, bool e4m3) {
 // 187 -> 178 us, 31 of up to 1013 with 32 key-value heads 27.7 -> 22.7 (16 of
 // up to 4099 in bf16 28.9 -> 30.0).
 constexpr int kRowCost = 2;
-constexpr float kLazy = 10.0f;             // log2: how far a score may pass the running maximum
+constexpr float kLazy = 10.0f;             // log2: how large a weight may be before the maximum moves
 constexpr float kNegInf = -__builtin_inff();
 
 struct Shape {
@@ -92,6 +95,12 @@ struct Args {
                                             // it, -infinity (a score behind the end) stays what it is
     uint32_t flip;                          // the queries' sign bits where scale is negative
 };
+
+// The logarithm of a row's sum from its maximum (of the scores, which have the
+// sign of scale in them) and its sum of weights.
+__device__ __forceinline__ float lse_of(const Args& p, float m, float l) {
+    return __builtin_fmaf(m, __builtin_fabsf(p.a.scale), __builtin_amdgcn_logf(l) * 0.69314718055994531f);
+}
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -573,13 +582,12 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
             float mx = sc[0];
 #pragma unroll
             for (int j = 1; j < 8; ++j) mx = fmaxf(mx, sc[j]);
-            mx *= c;
-            if (__ballot(mx > m + kLazy)) {
+            if (__ballot((mx - m) * c > kLazy)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
                 mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
                 const float up = fmaxf(m, mx);
                 const float to = up == kNegInf ? 0.0f : up;
-                const float f = __builtin_amdgcn_exp2f(m - to);
+                const float f = __builtin_amdgcn_exp2f((m - to) * c);
                 m = up;
                 mm = to;
                 l *= f;
@@ -589,7 +597,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
             float pr[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                pr[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j], c, -mm));
+                pr[j] = __builtin_amdgcn_exp2f((sc[j] - mm) * c);
                 l += pr[j];
             }
             const uint4 ph = narrow_bf16x8(pr);
@@ -675,6 +683,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
                     const float x = keep[(4 * j + r) * 64];
                     acc[j][r] = !lost && x * 0.0f == 0.0f ? x : acc[j][r] * 0.5f;
                 }
+            if (lost) m *= 0.5f;  // of scores taken twice
         }
 
         // worked out again, so that it takes no registers through the tiles
@@ -736,7 +745,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
 #pragma unroll
             for (int v = 0; v < kWaves; ++v) {
                 // a wave without tokens has sum and output 0 (or a NaN sum where a page was bad)
-                const float f = sm[turn][v][q] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(sm[turn][v][q] - M);
+                const float f = sm[turn][v][q] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((sm[turn][v][q] - M) * p.c);
                 const float4 x = *reinterpret_cast<const float4*>(&so[turn][v][q][d]);
                 L += sl[turn][v][q] * f;
                 o.x += x.x * f, o.y += x.y * f, o.z += x.z * f, o.w += x.w * f;
@@ -747,7 +756,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
                 *reinterpret_cast<uint2*>(p.a.out + at * p.s.dim + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
                 if (p.a.lse && d == 0)
-                    p.a.lse[at] = now.len <= 0 ? kNegInf : (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+                    p.a.lse[at] = now.len <= 0 ? kNegInf : lse_of(p, M, L);
             } else {
                 *reinterpret_cast<float4*>(part + 32 + q * p.s.dim + d) = o;
                 if (d == 0) part[2 * q] = M, part[2 * q + 1] = L;
@@ -763,10 +772,10 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
 
 // Adds a partial result (maximum m, sum l, unnormalised output x) to a running
 // one.  A part whose scores are all -infinity has sum and output 0 (or NaN).
-__device__ __forceinline__ void add_part(float& M, float& L, float4& o, float m, float l, float4 x) {
+__device__ __forceinline__ void add_part(float c, float& M, float& L, float4& o, float m, float l, float4 x) {
     const float to = fmaxf(M, m);
-    const float f = M == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(M - to);
-    const float g = m == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+    const float f = M == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((M - to) * c);
+    const float g = m == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((m - to) * c);
     M = to;
     L = L * f + l * g;
     o.x = o.x * f + x.x * g, o.y = o.y * f + x.y * g, o.z = o.z * f + x.z * g, o.w = o.w * f + x.w * g;
@@ -805,7 +814,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
                 const float* part = place(p, w, w == w0 ? which0 : 0);
                 const float2 ml = *reinterpret_cast<const float2*>(part + 2 * q);
                 const float4 x = *reinterpret_cast<const float4*>(part + 32 + q * p.s.dim + d);
-                add_part(M, L, o, ml.x, ml.y, x);
+                add_part(p.c, M, L, o, ml.x, ml.y, x);
             }
         }
         if (sets > 1) {
@@ -817,7 +826,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
                 __syncthreads();
                 if (set < n - half) {
                     const int at = (int)threadIdx.x + half * items;
-                    add_part(M, L, o, redm[at], redl[at], red[at]);
+                    add_part(p.c, M, L, o, redm[at], redl[at], red[at]);
                     redm[threadIdx.x] = M;
                     redl[threadIdx.x] = L;
                     red[threadIdx.x] = o;
@@ -829,7 +838,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
             const int64_t at = (int64_t)b * p.a.Hq + head * p.s.group + q0 + q;
             *reinterpret_cast<uint2*>(p.a.out + at * p.s.dim + d) =
                 make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-            if (p.a.lse && d == 0) p.a.lse[at] = (M + __builtin_amdgcn_logf(L)) * 0.69314718055994531f;
+            if (p.a.lse && d == 0) p.a.lse[at] = lse_of(p, M, L);
         }
     }
 }
