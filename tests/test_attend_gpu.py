@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from tests import step_reference as ref
-from tests.test_step_gpu import BF, DEV, E4, F32, U, attend_case, bd, gen_of, run_attend  # noqa: F401
+from tests.test_step_gpu import (BF, DEV, E4, EDGES, F32, U, attend_case, bd, check_attend, gen_of,  # noqa: F401
+                                 run_attend, same_bits)
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,171 @@ def test_large_scores(bd, scale, wide):
                     assert np.all(np.abs(out[b] - want) <= tol), (b, np.abs(out[b] - want).max())
                     # one rounding of the product, one of the logarithm of a number of ties
                     assert np.all(np.abs(lse[b] - want_lse) <= 4 * U * np.abs(want_lse) + 16 * U)
+
+
+# ----------------------------------------------------------------------------
+# rows that are split and joined, by wide tables
+
+@pytest.mark.parametrize("dim", [16, 48, 64, 80, 96, 112, 128, 144, 176, 192, 240, 256])
+@pytest.mark.parametrize("kind", [BF, E4])
+@pytest.mark.parametrize("q_t", [BF, F32])
+def test_wide_lengths(bd, dim, kind, q_t):
+    print("wide", dim, kind, q_t, flush=True)
+    for heads, group, page, layout in ((2, 4, 16, "heads"), (1, 8, 24, "tokens")):
+        c, q, table, lens, slots = attend_case(bd, EDGES, heads, group, dim, page, kind, q_t, layout)
+        table = widened(table, page)
+        assert is_split(c, q, table)
+        out, lse = run_attend(bd, c, q, table, lens)
+        check_attend(c, q, EDGES, slots, out, lse, dim ** -0.5)
+        again, lse2 = run_attend(bd, c, q, table, lens)
+        assert same_bits(out, again) and same_bits(lse, lse2)
+
+
+@pytest.mark.parametrize("heads,group", [(1, 1), (3, 1), (2, 2), (1, 7), (2, 16), (1, 17), (2, 33), (1, 64), (9, 3)])
+def test_wide_head_layouts(bd, heads, group):
+    """Rows of one unit and of two dozen, each cut wherever it can be; more than 16 query heads to a key-value head,
+    the last 16 not all there; and some of the same rows while thousands of others are there, where few are cut."""
+    print("wide heads", heads, group, flush=True)
+    for kind, dim, page in ((E4, 64, 8), (BF, 128, 48)):
+        lens = [5, 0, 3000, 64, 200]
+        c, q, table, lens_t, slots = attend_case(bd, lens, heads, group, dim, page, kind, BF, "both")
+        table = widened(table, page)
+        assert is_split(c, q, table)
+        out, lse = run_attend(bd, c, q, table, lens_t)
+        check_attend(c, q, lens, slots, out, lse, dim ** -0.5)
+        pick = torch.arange(203) * 3 % 5
+        many, many_lse = run_attend(bd, c, q[pick].contiguous(), table[pick].contiguous(), lens_t[pick])
+        first = np.concatenate([[0], np.cumsum(lens)])
+        own = [t for i in pick for t in slots[first[i]:first[i + 1]]]
+        check_attend(c, q[pick], [lens[i] for i in pick], own, many, many_lse, dim ** -0.5, rows=(0, 1, 2, 4, 119, 202))
+
+
+@pytest.mark.parametrize("B", [65, 513, 4099, 100003])
+def test_wide_many_sequences(bd, B):
+    """More sequences than a wave has lanes, most of them short: the line of units is worked out over all of them."""
+    lens = [0, 1, 30, 64, 130, 7, 128, 129]
+    c, q, table, lens_t, slots = attend_case(bd, lens, 1, 2, 32, 16, E4, BF)
+    table = widened(table, 16)
+    pick = torch.arange(B) * 5 % len(lens)
+    q_all, table_all, lens_all = q[pick].contiguous(), table[pick].contiguous(), lens_t[pick].contiguous()
+    bad = list(range(11, B, 97))
+    lens_all[bad] = 4097
+    assert is_split(c, q_all, table_all)
+    out, lse = run_attend(bd, c, q_all, table_all, lens_all)
+    alone, alone_lse = run_attend(bd, c, q, table, lens_t)
+    check_attend(c, q, lens, slots, alone, alone_lse, 32 ** -0.5)
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    # a row may be cut elsewhere in another batch: two bf16 roundings and the sums' own
+    fine = np.setdiff1d(np.arange(B), bad)
+    o, a = ref.to64(out)[fine], ref.to64(alone)[pick.numpy()][fine]
+    assert np.all(np.abs(o - a) <= 2.0 ** -7 * np.abs(a) + 2.0 ** -14)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
+def test_wide_scales(bd, scale):
+    for kind in (BF, E4):
+        lens = [1, 40, 400]
+        c, q, table, lens_t, slots = attend_case(bd, lens, 2, 2, 64, 16, kind, BF, spread=3.0)
+        out, lse = run_attend(bd, c, q, widened(table, 16), lens_t, scale)
+        check_attend(c, q, lens, slots, out, lse, scale)
+
+
+@pytest.mark.parametrize("up", [1, -1])
+@pytest.mark.parametrize("kind", [BF, E4])
+def test_wide_rising_scores(bd, kind, up):
+    """Scores that rise by far more than the running maximum's slack from part to part, and fall."""
+    c, q, table, lens_t, slots = attend_case(bd, [600], 1, 2, 64, 16, kind, BF)
+    k = torch.zeros((600, 1, 64))
+    k[:, 0, 0] = up * torch.arange(600).float()
+    v = torch.randn((600, 1, 64), generator=gen_of(2))
+    q = torch.zeros((1, 2, 64), dtype=BF)
+    q[0, 0, 0], q[0, 1, 0] = 1.0, 0.125
+    s = torch.tensor(slots, dtype=torch.int32)
+    c.expect(k, v, s)
+    bd.bd_kv_write(c.kv, k.to(DEV), v.to(DEV), s.to(DEV))
+    out, lse = run_attend(bd, c, q, widened(table, 16), lens_t, 1.0)
+    check_attend(c, q, [600], slots, out, lse, 1.0)
+
+
+@pytest.mark.parametrize("q_t", [BF, F32])
+def test_wide_infinite_and_nan_rows(bd, q_t):
+    """Infinities and NaN in some parts of a row, the others finite: the joined row is what the formula gives."""
+    lens = [700, 700, 700, 700, 700, 140]
+    c, q, table, lens_t, slots = attend_case(bd, lens, 1, 2, 32, 16, BF, q_t)
+    table = widened(table, 16)
+    assert is_split(c, q, table)
+    first = np.concatenate([[0], np.cumsum(lens)])
+    T = int(first[-1])
+    k = torch.randn((T, 1, 32), generator=gen_of(3)).to(BF)
+    v = torch.randn((T, 1, 32), generator=gen_of(4)).to(BF)
+    q = q.abs() + 0.1
+    inf = float("inf")
+    k[first[0] + 128:first[0] + 256, 0, 0] = -inf     # a part whose scores are all -infinity
+    k[first[0] + 640:first[0] + 700, 0, 1] = -inf     # the last one too
+    v[first[1] + 300, 0, 3] = inf                     # an infinite value in a middle part
+    k[first[2] + 650, 0, 1] = float("nan")            # NaN scores in the last part
+    v[first[3] + 5, 0, 2] = float("nan")              # a NaN value in the first
+    k[first[4]:first[4] + 128, 0, 5] = -inf           # the first part all -infinity
+    k[first[5]:, 0, 0] = -inf                         # every score of both parts: NaN, as in the formula
+    s = torch.tensor(slots, dtype=torch.int32)
+    c.expect(k, v, s)
+    bd.bd_kv_write(c.kv, k.to(DEV), v.to(DEV), s.to(DEV))
+    out, lse = run_attend(bd, c, q, table, lens_t)
+    o = ref.to64(out)
+    if q_t == BF:
+        check_attend(c, q, lens, slots, out, lse, 32 ** -0.5, rows=(0, 4))
+    else:
+        assert np.isfinite(o[[0, 4]]).all() and lse[[0, 4]].isfinite().all()
+    assert np.isposinf(o[1, :, 3]).all() and np.isfinite(np.delete(o[1], 3, 1)).all()
+    assert np.isnan(o[2]).all() and lse[2].isnan().all()
+    assert np.isnan(o[3, :, 2]).all() and np.isfinite(np.delete(o[3], 2, 1)).all()
+    assert np.isnan(o[5]).all()
+
+
+def test_wide_pages_and_lengths_out_of_range(bd):
+    for kind in (BF, E4):
+        lens = [200, 900, 200, 30, 1000, 50]
+        c, q, table, lens_t, slots = attend_case(bd, lens, 2, 2, 64, 16, kind, BF)
+        bad, bad_len = widened(table, 16), lens_t.clone()
+        bad[1, 56] = -1                      # the last page in use, in the last part
+        bad[2, 0] = c.kv.num_pages
+        bad[4, 30] = 2 ** 31 - 1             # a middle part
+        bad_len[3] = -5
+        bad_len[5] = 4097
+        out, lse = run_attend(bd, c, q, bad, bad_len)
+        for b in (1, 2, 4, 5):
+            assert out[b].isnan().all() and lse[b].isnan().all()
+        assert (out[3] == 0).all() and (lse[3] == -float("inf")).all()
+        check_attend(c, q, lens, slots, out, lse, 0.125, rows=(0,))
+
+
+def test_wide_graph(bd):
+    """A captured call on a wide table, replayed while the lengths change so that rows are cut elsewhere each time, with
+    eager calls of other sizes between the replays; every replay against the eager result and the formula."""
+    longest = [2000, 700, 1, 300]
+    for kind in (E4, BF):
+        c, q, table, lens_t, slots = attend_case(bd, longest, 2, 4, 64, 16, kind, BF)
+        table = widened(table, 16)
+        assert is_split(c, q, table)
+        gq, gt, gl = q.to(DEV), table.to(DEV), lens_t.to(DEV)
+        lse = torch.empty(q.shape[:2], dtype=F32, device=DEV)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            bd.bd_attend(gq, c.kv, gt, gl, lse=lse)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = bd.bd_attend(gq, c.kv, gt, gl, lse=lse)
+        first = np.concatenate([[0], np.cumsum(longest)])
+        for lens in ([2000, 700, 1, 300], [1, 1, 1, 1], [0, 0, 0, 0], [129, 700, 0, 128], [1999, 0, 1, 299], [2000, 700, 1, 300]):
+            gl.copy_(torch.tensor(lens))
+            held.fill_(7.0)
+            lse.fill_(7.0)
+            graph.replay()
+            got, got_lse = held.clone(), lse.clone()
+            bd.bd_attend(gq[:1], c.kv, gt[:1, :8], torch.full_like(gl[:1], 100))
+            torch.cuda.synchronize()
+            eager, eager_lse = run_attend(bd, c, q, table, torch.tensor(lens, dtype=torch.int32))
+            assert same_bits(got, eager) and same_bits(got_lse, eager_lse), lens
+            own = [t for b, n in enumerate(lens) for t in slots[first[b]:first[b] + n]]
+            check_attend(c, q, lens, own, got, got_lse, 0.125)
