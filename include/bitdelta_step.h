@@ -164,10 +164,10 @@ bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t*
  *               Its contents on entry do not matter.  Where the table holds
  *               few tokens for each sequence nothing is split, and it is 0.
  * Scores, the running maximum and sum and the output sums are fp32; fp32
- * queries and the softmax weights enter the matrix products as two bf16
- * terms each, so no input or weight is cut to 8 bits (but where a row of the
+ * queries enter the matrix products as three bf16 terms, which hold all of
+ * their bits, the softmax weights as two, 16 bits (but where a row of the
  * sequence itself holds infinities: what they reach is summed with one term
- * each, as a second one would make NaN of them).  The same inputs and
+ * each, as further ones would make NaN of them).  The same inputs and
  * batch give bitwise the same outputs.  B == 0 is a no-op.
  * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _WORKSPACE, _HIP,
  * _DEVICE.

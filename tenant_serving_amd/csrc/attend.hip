@@ -24,9 +24,10 @@
 // It is kept as a score, without c: the difference is taken first, so that the
 // largest score's weight is 2^0 however large the scores are (2^(c q.k_j - c m)
 // has the rounding error of c m in its exponent, which is past 128 from 2^31 on).
-// The weights enter as two bf16 terms (their sum holds 16 bits), and so do
-// fp32 queries: the matrix units idle most of the time here, and an output
-// is then as exact as its own rounding.
+// The weights enter as two bf16 terms (their sum holds 16 bits, and an output
+// is then as exact as its own rounding), fp32 queries as three, which hold all
+// of their 24 bits: lse is an fp32 result, and two terms left its scores' error
+// at 2^-17 of them.  The matrix units idle most of the time here.
 //
 // Work split.  A unit is 128 tokens of one (sequence, key-value head, 16
 // query heads), four waves with a tile each.  The units of the whole batch
@@ -290,7 +291,7 @@ __device__ __forceinline__ void clear(Dwords<N>& r) {
 __device__ __forceinline__ void flip(uint4& v, uint32_t mask) { v.x ^= mask, v.y ^= mask, v.z ^= mask, v.w ^= mask; }
 
 // kDC: the width, see width_of.  kFull: head_dim is kDC.
-// kSplitQ: fp32 queries as two bf16 terms.
+// kSplitQ: fp32 queries as three bf16 terms.
 template <int kDC, bool kFull, bool kE4m3, bool kSplitQ>
 __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void attend_kernel(const Args p) {
     constexpr int NS = kDC / 32;              // k-steps of a score product
@@ -307,13 +308,14 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
     constexpr int kPad = kDC + 4;
     // Two of each, used in turn by the rows: one barrier a row.  Past head_dim
     // 128 one, where a CU then holds two workgroups instead of one; at 256, and
-    // for fp32 queries on bf16 keys, with the queries in LDS instead of registers.
+    // for fp32 queries, with the queries in LDS instead of registers.
     constexpr bool kOneTurn = kDC > 128 && per_cu(kDC, kSplitQ, kE4m3) == 2;
-    constexpr bool kTight = kOneTurn && (kDC == 256 || (kSplitQ && !kE4m3));
+    constexpr bool kTight = kOneTurn && (kDC == 256 || kSplitQ);
+    constexpr int QT = kSplitQ ? 3 : 1;
     constexpr int kTurns = kOneTurn ? 1 : 2;
     __shared__ float so[kTurns][kWaves][16][kPad];
     __shared__ float sm[kTurns][kWaves][16], sl[kTurns][kWaves][16];
-    __shared__ uint4 sq[kTight ? (kSplitQ ? 2 : 1) : 1][kTight ? NS : 1][64];
+    __shared__ uint4 sq[kTight ? QT : 1][kTight ? NS : 1][64];
     constexpr int NR = kTight ? (NS + kWaves - 1) / kWaves : NS;  // k-steps whose queries a wave loads
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
@@ -494,26 +496,27 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
             if (next.t0 < next.stop) next_pages = load_pages(next, next.t0);
         }
 
-        uint4 qh[NR], ql[NR];
+        uint4 qt[QT][NR];  // the terms, the largest first
 #pragma unroll
         for (int s = 0; s < NR; ++s) {
             if constexpr (kSplitQ) {
                 float f[8], back[8];
                 raw[s].widen(f);
-                qh[s] = narrow_bf16x8(f);
-                widen_bf16x8(qh[s], back);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] -= back[j];
-                ql[s] = narrow_bf16x8(f);
+                for (int k = 0; k < QT; ++k) {
+                    qt[k][s] = narrow_bf16x8(f);
+                    widen_bf16x8(qt[k][s], back);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] -= back[j];
+                }
             } else {
-                qh[s] = raw[s].a;
+                qt[0][s] = raw[s].a;
             }
-            flip(qh[s], p.flip);
-            if constexpr (kSplitQ) flip(ql[s], p.flip);
             raw[s].zero();  // not kept through the tiles
-            if (kTight && s * kWaves + wave < NS) {
-                sq[0][s * kWaves + wave][lane] = qh[s];
-                if constexpr (kSplitQ) sq[1][s * kWaves + wave][lane] = ql[s];
+#pragma unroll
+            for (int k = 0; k < QT; ++k) {
+                flip(qt[k][s], p.flip);
+                if (kTight && s * kWaves + wave < NS) sq[k][s * kWaves + wave][lane] = qt[k][s];
             }
         }
         if constexpr (kTight) __syncthreads();
@@ -547,17 +550,16 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
                         const Dwords<4>& r = kk[h][s];
                         kb = make_uint4(r.d[0], r.d[1], r.d[2], r.d[3]);
                     }
-                    uint4 hi, lo;
-                    if constexpr (kTight) {
-                        hi = sq[0][s][lane];
-                        if constexpr (kSplitQ) lo = sq[lost ? 0 : 1][s][lane];
-                    } else {
-                        hi = qh[s];
-                        if constexpr (kSplitQ) lo = ql[s];
+#pragma unroll
+                    for (int k = QT - 1; k >= 0; --k) {
+                        uint4 qk;
+                        if constexpr (kTight)
+                            qk = sq[lost ? 0 : k][s][lane];
+                        else
+                            qk = qt[k][s];
+                        x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kb), as_bf16x8(qk), x, 0, 0, 0);
                     }
-                    if constexpr (kSplitQ)
-                        x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kb), as_bf16x8(lo), x, 0, 0, 0);
-                    x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(kb), as_bf16x8(hi), x, 0, 0, 0);
+                    if (kTight && kSplitQ) __builtin_amdgcn_sched_barrier(0);  // or all terms wait in registers
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sc[4 * h + r] = x[r];
@@ -644,11 +646,12 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
             }
         }
 
-        // A second term breaks on infinities: it is of either sign or zero,
+        // Further terms break on infinities: they are of either sign or zero,
         // and infinity minus itself or times zero is NaN.  So where a sum is
         // not finite the wave goes over its tokens again with one term, taken
-        // twice and halved, and takes what was lost from there.  The queries'
-        // second term only goes where the scores broke.
+        // as often as there are terms and divided by their number, and takes
+        // what was lost from there.  The queries' further terms only go where
+        // the scores broke.
         if (!pass) {
             float z = 0.0f;
 #pragma unroll
@@ -664,8 +667,10 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
                     for (int r = 0; r < 4; ++r) keep[(4 * j + r) * 64] = acc[j][r];
                 if (lost) {
 #pragma unroll
-                    for (int s = 0; s < NR; ++s) ql[s] = qh[s];
-                    c *= 0.5f;
+                    for (int s = 0; s < NR; ++s)
+#pragma unroll
+                        for (int k = 1; k < QT; ++k) qt[k][s] = qt[0][s];
+                    c *= 1.0f / QT;
                 }
                 pass = 1;
                 pages = load_pages(now, t0);
@@ -683,7 +688,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
                     const float x = keep[(4 * j + r) * 64];
                     acc[j][r] = !lost && x * 0.0f == 0.0f ? x : acc[j][r] * 0.5f;
                 }
-            if (lost) m *= 0.5f;  // of scores taken twice
+            if (lost) m *= 1.0f / QT;  // of scores taken that often
         }
 
         // worked out again, so that it takes no registers through the tiles

@@ -227,3 +227,37 @@ def test_wide_graph(bd):
             assert same_bits(got, eager) and same_bits(got_lse, eager_lse), lens
             own = [t for b, n in enumerate(lens) for t in slots[first[b]:first[b] + n]]
             check_attend(c, q, lens, own, got, got_lse, 0.125)
+
+
+@pytest.mark.parametrize("dim", [16, 64, 96, 128, 160, 192, 256])
+@pytest.mark.parametrize("kind", [BF, E4])
+@pytest.mark.parametrize("wide", [False, True])
+def test_fp32_queries_hold_their_bits(bd, dim, kind, wide):
+    """Scores of fp32 queries in all of their 24 bits.  Every key has one value that is not 0, a power of two, so that a
+    score is one query value times it, exactly, in whatever terms and order it is summed; two terms of 8 bits would be
+    off by up to 2^-17 of it.  The tokens' scores differ by 0 or more than 2^7 (after scale), so lse is the largest score
+    and the logarithm of how many have it: one rounding of each product and of the sum."""
+    print("fp32 queries", dim, kind, wide, flush=True)
+    lens, scale = [1, 130, 300], 0.75
+    c, q, table, lens_t, slots = attend_case(bd, lens, 2, 3, dim, 16, kind, F32)
+    table = widened(table, 16) if wide else table
+    T, gen = len(slots), gen_of(dim)
+    at = torch.randint(0, dim, (T, 2), generator=gen)
+    k = torch.zeros((T, 2, dim)).scatter_(2, at[..., None], 1.0)
+    v = torch.randn((T, 2, dim), generator=gen)
+    # the values of one query: 2^10 apart, with random bits behind
+    step = torch.stack([torch.randperm(dim, generator=gen) for _ in range(len(lens) * 6)]).view(len(lens), 6, dim)
+    q = step.float() * 2.0 ** 10 + torch.rand(step.shape, generator=gen) * 2.0 ** 9 + 0.1
+    s = torch.tensor(slots, dtype=torch.int32)
+    c.expect(k, v, s)
+    bd.bd_kv_write(c.kv, k.to(DEV), v.to(DEV), s.to(DEV))
+    out, lse = run_attend(bd, c, q, table, lens_t, scale)
+    first = 0
+    for b, n in enumerate(lens):
+        kr = np.stack([c.row64(0, x) for x in slots[first:first + n]])
+        vr = np.stack([c.row64(1, x) for x in slots[first:first + n]])
+        first += n
+        want, want_lse, _ = ref.attend(ref.to64(q)[b], kr, vr, scale)
+        assert np.all(np.abs(ref.to64(lse)[b] - want_lse) <= 4 * U * np.abs(want_lse) + 16 * U)
+        tol = 2.0 ** -8 * np.abs(want) + (n + 64) * U * np.abs(vr).max()
+        assert np.all(np.abs(ref.to64(out)[b] - want) <= tol)
