@@ -63,9 +63,11 @@ typedef enum bd_type {
  *                the last one of the rest.  NULL for BD_BF16.
  * d: a multiple of 8, 8 .. 65536.  eps >= 0.  x, residual, residual_out,
  * gain, out: 16-byte aligned (out: 8 for BD_E4M3).  M == 0 is a no-op.
- * fp32 throughout for a bf16 result; for codes the sum, root and products are
- * 64-bit and y is rounded once, to its code.  Fixed order: the same inputs give
- * bitwise the same outputs.
+ * fp32 throughout for a bf16 result (a row whose squares leave fp32's range is
+ * scaled by a power of two first, so h may be of any size); for codes the sum,
+ * root and products are 64-bit and y is rounded once, to its code (a finite y
+ * past the largest fp32 number counts as that).  Fixed order: the same inputs
+ * give bitwise the same outputs.
  * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _HIP, _DEVICE.
  * ------------------------------------------------------------------------- */
 bd_status bd_rms_norm(const void* x, int32_t x_type, const void* residual, void* residual_out,

@@ -82,7 +82,6 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
     }
 
     float h[C][8];
-    Sum sum = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int e = (c * NT + tid) * 8;
@@ -102,19 +101,51 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
                 p[1] = make_float4(h[c][4], h[c][5], h[c][6], h[c][7]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fma((Sum)h[c][i], (Sum)h[c][i], sum);
     }
-    sum = wave_sum(sum);
-    if (NT > 64) {
-        __shared__ Sum part[NT / 64];
-        if ((tid & 63) == 0) part[tid >> 6] = sum;
-        __syncthreads();
-        sum = 0;
+    // the mean square of the row times `by`, in all of its lanes
+    __shared__ Sum part[2][NT / 64];
+    const auto mean_square = [&](int turn, Sum by) {
+        Sum sum = 0;
 #pragma unroll
-        for (int w = 0; w < NT / 64; ++w) sum += part[w];
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const Sum x = (Sum)h[c][i] * by;
+                sum = fma(x, x, sum);
+            }
+        }
+        sum = wave_sum(sum);
+        if (NT > 64) {
+            if ((tid & 63) == 0) part[turn][tid >> 6] = sum;
+            __syncthreads();
+            sum = 0;
+            if constexpr (kE4m3) {
+#pragma unroll
+                for (int w = 0; w < NT / 64; ++w) sum += part[turn][w];
+            } else {  // through one register, not one for each wave
+                const int of = __float_as_int(part[turn][tid & (NT / 64 - 1)]);
+#pragma unroll
+                for (int w = 0; w < NT / 64; ++w) sum += __int_as_float(__builtin_amdgcn_readlane(of, w));
+            }
+        }
+        return sum / (Sum)a.d;
+    };
+    Sum under = mean_square(0, 1) + (Sum)a.eps;
+    // Squares past fp32's range, or so small that they lose bits or vanish and
+    // eps does not cover it: the row times a power of two, and eps times its
+    // square, give the same y.  2^-76 takes the sum of 65536 of the largest
+    // squares to 2^120; 2^90 takes one below 65536 times 2^-80 to 2^116, and the
+    // least square to 2^-118.  Every lane of the row has the same sum and takes
+    // the same way.
+    float by = 1.0f;
+    if constexpr (!kE4m3) {
+        const float all = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(under)));
+        if (all > 0x1p100f || all < 0x1p-80f) {
+            by = all > 1.0f ? 0x1p-76f : 0x1p90f;
+            under = mean_square(1, by) + a.eps * by * by;
+        }
     }
-    const Sum rstd = known ? (Sum)1 / sqrt(sum / (Sum)a.d + (Sum)a.eps) : (Sum)__builtin_nanf("");
+    const Sum rstd = known ? (Sum)1 / sqrt(under) : (Sum)__builtin_nanf("");
 
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -133,7 +164,7 @@ __global__ __launch_bounds__(kNormBlock<NT>) void norm_kernel(const NormArgs a, 
             if constexpr (kE4m3)
                 h[c][i] = to_odd((double)h[c][i] * rstd * (double)g[i]);
             else
-                h[c][i] = h[c][i] * rstd * g[i];
+                h[c][i] = h[c][i] * by * rstd * g[i];
         }
         if (kE4m3) {
             uint32_t top = 0;
