@@ -91,6 +91,8 @@ bd_status bd_rms_norm(const void* x, int32_t x_type, const void* residual, void*
  *   head_dim   a multiple of 16, 16 .. 256.
  *   strides    in elements, >= 0, multiples of 16 bytes and below 2^36 bytes;
  *              distinct rows must not overlap.  k, v: 16-byte aligned.
+ * Rows of k, rows of v, k_scales and v_scales lie apart from each other (k's
+ * and v's may lie in the gaps of each other's strides).
  * The struct is read during the call only.
  * ------------------------------------------------------------------------- */
 typedef struct bd_kv {

@@ -112,6 +112,20 @@ def _at(t):
     return t.data_ptr() if t is not None else None
 
 
+def _on_rows(base, steps, row, lo, hi):
+    """Whether the addresses [lo, hi) meet rows of `row` bytes that start at base plus any number i < n of each step
+    (step, n) of steps, which fall, each past the extent of all smaller ones."""
+    left = hi - 1 - base
+    if left < 0 or lo >= hi:
+        return False
+    last = base   # where the last row that starts before hi does
+    for step, n in steps:
+        i = min(n - 1, left // step)
+        last += i * step
+        left -= i * step
+    return last + row > lo
+
+
 def _refuse_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales):
     """Every check of a norm's arguments, in full; raises or returns."""
     _typed("x", x, _IN)
@@ -284,11 +298,18 @@ class bd_kv_cache:
                 raise ValueError("rows of k overlap (strides %s)" % (tuple(k.stride()),))
             extent = s * (n - 1) + extent
         self._span = extent * size
+        self._steps, self._row = [(s * size, n) for s, n in reversed(steps)], dim * size
         if kind == BD_E4M3:
             for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
                 _plain(name, t, torch.uint8, (pages, heads, page))
                 if t.data_ptr() % 8:
                     raise ValueError("%s must be 8-byte aligned" % name)
+            if _overlap(k_scales, v_scales):
+                raise ValueError("k_scales overlaps v_scales")
+            for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+                for other, rows in (("k", k), ("v", v)):
+                    if _on_rows(rows.data_ptr(), self._steps, self._row, *_span(t)):
+                        raise ValueError("%s overlaps %s" % (name, other))
         elif k_scales is not None or v_scales is not None:
             raise ValueError("a bf16 cache has no scales")
         _same_gpu(k.device, (("v", v), ("k_scales", k_scales), ("v_scales", v_scales)))
