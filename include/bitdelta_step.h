@@ -113,9 +113,12 @@ typedef struct bd_kv {
 /* Writes the keys and values of T tokens into their slots.
  *
  *   k, v     T tokens of num_heads rows of head_dim values, in_type BD_BF16
- *            or BD_FP32, 16-byte aligned, apart from the cache's memory: token t's row of head h starts at
+ *            or BD_FP32, 16-byte aligned: token t's row of head h starts at
  *            element t * k_strides[0] + h * k_strides[1] (v likewise).  The
- *            strides are HOST arrays of two, multiples of 16 bytes.
+ *            strides are HOST arrays of two, multiples of 16 bytes.  These rows
+ *            and `slots` lie apart from the cache's rows and scale bytes (the
+ *            gaps of its strides are free); to move rows within a cache, copy
+ *            them out first.
  *   slots    [T] int32.  A slot below 0 or past the last page: that token is
  *            not written.  A slot named by several tokens holds the last of
  *            them afterwards.

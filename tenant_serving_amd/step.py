@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+from bisect import bisect_right
 
 import torch
 
@@ -43,6 +44,7 @@ class _KV(ctypes.Structure):
 
 
 _Pair = ctypes.c_int64 * 2
+_NO_END = 1 << 64
 
 
 def declare(lib):
@@ -124,6 +126,38 @@ def _on_rows(base, steps, row, lo, hi):
         last += i * step
         left -= i * step
     return last + row > lo
+
+
+def _any_on_rows(base, steps, row, starts, size):
+    """_on_rows of any [start, start + size) of an int64 tensor of starts."""
+    left = starts + (size - 1 - base)
+    reach = left >= 0
+    last = torch.full_like(starts, base)
+    for step, n in steps:
+        i = torch.div(left, step, rounding_mode="floor").clamp_(0, n - 1)
+        last += i * step
+        left -= i * step
+    return bool((reach & (last + row > starts)).any())
+
+
+def _apart(kv, lo, hi):
+    """Whether the addresses [lo, hi) are outside all spans of the cache's arrays."""
+    i = bisect_right(kv._bounds, lo)
+    return not i & 1 and (i == len(kv._bounds) or hi <= kv._bounds[i])
+
+
+def _refuse_on_cache(kv, named):
+    """Raises where a tensor's rows (its last axis is contiguous) meet what the cache holds; the gaps of the cache's
+    strides, and of the tensor's own, are not held."""
+    for name, t in named:
+        if not t.numel() or _apart(kv, *_span(t)):
+            continue
+        size = t.element_size()
+        starts = torch.tensor(t.data_ptr(), dtype=torch.int64)
+        for n, s in zip(t.shape[:-1], t.stride()):
+            starts = starts[..., None] + torch.arange(n) * (s * size)
+        if any(_any_on_rows(*array, starts, t.shape[-1] * size) for array in kv._arrays):
+            raise ValueError("%s overlaps the cache" % name)
 
 
 def _refuse_norm(out_type, x, gain, eps, residual, variant_ids, residual_out, out, scales):
@@ -266,6 +300,8 @@ class bd_kv_cache:
     k_scales, v_scales: uint8 [num_pages, num_heads, page_size] for float8_e4m3fn, one scale byte per row.
     The tensors are kept by reference; the checks run once, here."""
 
+    _bounds = _arrays = ()
+
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: torch.Tensor | None = None,
                  v_scales: torch.Tensor | None = None):
         kind = _typed("k", k, _HELD)
@@ -321,6 +357,18 @@ class bd_kv_cache:
         self._desc = _KV(k.data_ptr(), v.data_ptr(), _at(k_scales), _at(v_scales), kind, heads, dim, page, pages,
                          *stride[:3])
         self._ref = ctypes.addressof(self._desc)
+        # where the arrays are: each as _on_rows takes it, and the ends of their spans in rising order, those that meet
+        # taken together
+        self._arrays = [(t.data_ptr(), self._steps, self._row) for t in (k, v)]
+        self._arrays += [(t.data_ptr(), [], t.nbytes) for t in (k_scales, v_scales) if t is not None]
+        spans = sorted((at, at + (self._span if steps else row)) for at, steps, row in self._arrays)
+        bounds = []
+        for lo, hi in spans:
+            if bounds and lo <= bounds[-1]:
+                bounds[-1] = max(bounds[-1], hi)
+            else:
+                bounds += [lo, hi]
+        self._bounds = bounds
 
     @staticmethod
     def _interleaved(k, v, stride, size):
@@ -344,7 +392,8 @@ class bd_kv_cache:
 
 
 def _rows(name, t, kv_heads, dim):
-    """(type, strides) of [n, heads, dim] rows with any token and head stride."""
+    """(type, strides, n, heads, elements from the first to behind the last) of [n, heads, dim] rows with any token and
+    head stride."""
     try:
         n, heads, last = t.shape
         a, b, c = t.stride()
@@ -352,23 +401,23 @@ def _rows(name, t, kv_heads, dim):
         if last == dim and (heads == kv_heads or kv_heads is None) and c == 1 and n > 1 and heads > 1:
             unit = 7 if kind == BD_BF16 else 3   # elements of 16 bytes, less one
             if not (a | b) & unit and not t.data_ptr() & 15:
-                return kind, _Pair(a, b)
+                return kind, _Pair(a, b), n, heads, (n - 1) * a + (heads - 1) * b + dim
     except (AttributeError, KeyError, ValueError):
         pass
     kind = _typed(name, t, _IN)
     if t.dim() != 3 or (kv_heads is not None and t.shape[1] != kv_heads) or t.shape[2] != dim:
         raise ValueError("%s must be [n, %s, %d] (got %s)" % (name, kv_heads or "num_q_heads", dim, tuple(t.shape)))
-    a, b, c = t.stride()
-    if t.shape[0] <= 1:
+    (n, heads, _), (a, b, c) = t.shape, t.stride()
+    if n <= 1:
         a = 0
-    if t.shape[1] <= 1:
+    if heads <= 1:
         b = 0
     if c != 1:
         raise ValueError("%s's rows must be contiguous" % name)
     size = t.element_size()
     if a * size % 16 or b * size % 16 or t.data_ptr() % 16:
         raise ValueError("%s and its strides must be multiples of 16 bytes" % name)
-    return kind, _Pair(a, b)
+    return kind, _Pair(a, b), n, heads, (n - 1) * a + (heads - 1) * b + dim
 
 
 def _cache(kv):
@@ -385,21 +434,30 @@ def _index(name, t, n, dev):
 def bd_kv_write(kv: bd_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor):
     """Writes the rows k, v [T, num_heads, head_dim] (bf16 or fp32, any token and head strides) of T tokens into the
     cache's slots (int32 [T]; slot = page · page_size + place).  Slots below 0 or past the cache's end are skipped; of
-    several tokens with one slot the last stays."""
+    several tokens with one slot the last stays.  k, v and slots lie apart from the cache's rows (copy a view of them
+    first to move rows within one)."""
     _cache(kv)
-    kind, ks = _rows("k", k, kv.num_heads, kv.head_dim)
-    v_kind, vs = _rows("v", v, kv.num_heads, kv.head_dim)
-    T, dev = k.shape[0], kv._dev
-    if v_kind != kind or v.shape[0] != T:
+    kind, ks, T, _, k_reach = _rows("k", k, kv.num_heads, kv.head_dim)
+    v_kind, vs, v_n, _, v_reach = _rows("v", v, kv.num_heads, kv.head_dim)
+    dev = kv._dev
+    if v_kind != kind or v_n != T:
         raise ValueError("k and v must have one dtype and one number of tokens")
-    if not (_index("slots", slots, T, dev) and k.get_device() == dev and v.get_device() == dev):
+    # the ordinary call: k, v and all between them (one q, k, v result, mostly) and slots outside the cache's spans
+    k0, v0, ends = k.data_ptr(), v.data_ptr(), kv._bounds
+    at = bisect_right(ends, k0 if k0 < v0 else v0)
+    upto = ends[at] if at < len(ends) else _NO_END
+    if not (_index("slots", slots, T, dev) and k.get_device() == dev and v.get_device() == dev
+            and (not at & 1 and k0 + 4 * k_reach <= upto and v0 + 4 * v_reach <= upto
+                 or _apart(kv, k0, k0 + 4 * k_reach) and _apart(kv, v0, v0 + 4 * v_reach))
+            and _apart(kv, slots.data_ptr(), slots.data_ptr() + 4 * T)):
         _plain("slots", slots, torch.int32, (T,))
+        _refuse_on_cache(kv, (("k", k), ("v", v), ("slots", slots)))
         _same_gpu(kv.device, (("k", k), ("v", v), ("slots", slots)))
     if _current_device() != dev:
         with torch.cuda.device(dev):
             return bd_kv_write(kv, k, v, slots)
     lib = _declared or _library()
-    st = lib.bd_kv_write(kv._ref, k.data_ptr(), ks, v.data_ptr(), vs, kind, slots.data_ptr(), T, _stream_of(dev))
+    st = lib.bd_kv_write(kv._ref, k0, ks, v0, vs, kind, slots.data_ptr(), T, _stream_of(dev))
     if st:
         _check(lib, "bd_kv_write", st)
 
@@ -481,8 +539,7 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     counts the new one, whose row is in the cache by then.  A length of 0 gives zeros.  scale defaults to
     head_dim^-0.5.  lse, if given, is an fp32 [B, num_q_heads] tensor that receives the log of the softmax's sum."""
     _cache(kv)
-    kind, qs = _rows("q", q, None, kv.head_dim)
-    B, heads, _ = q.shape
+    kind, qs, B, heads, _ = _rows("q", q, None, kv.head_dim)
     dev = kv._dev
     scale = kv.head_dim ** -0.5 if scale is None else float(scale)
     if not abs(scale) <= 2.0 ** 60:
