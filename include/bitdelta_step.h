@@ -129,7 +129,8 @@ bd_status bd_kv_write(const bd_kv* kv, const void* k, const int64_t* k_strides, 
                       const int64_t* v_strides, int32_t in_type, const int32_t* slots, int64_t T, void* stream);
 
 /* Reads rows back: k_out, v_out [T, num_heads, head_dim] bf16, 16-byte
- * aligned; the exact value of every held row.  A slot below 0 gives zeros (a
+ * aligned, apart from each other, the slots and the cache's rows and scale
+ * bytes; the exact value of every held row.  A slot below 0 gives zeros (a
  * padding token), one past the last page NaN.  T == 0 is a no-op.
  * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _HIP, _DEVICE. */
 bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t* k_out, uint16_t* v_out,

@@ -462,20 +462,43 @@ def bd_kv_write(kv: bd_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.
         _check(lib, "bd_kv_write", st)
 
 
+def _given(t, dtype, shape, dev):
+    """Whether t is a contiguous tensor of this kind on the device."""
+    return (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev)
+
+
+def _read_to(kv, out, slots, shape, dev):
+    """Whether out is two tensors that a read may write to, as it nearly always is."""
+    if type(out) not in (tuple, list) or len(out) != 2:
+        return False
+    k, v = out
+    if not (_given(k, torch.bfloat16, shape, dev) and _given(v, torch.bfloat16, shape, dev)):
+        return False
+    k0, v0, s0, size = k.data_ptr(), v.data_ptr(), slots.data_ptr(), k.nbytes
+    k1, v1, s1 = k0 + size, v0 + size, s0 + slots.nbytes
+    return ((k1 <= v0 or v1 <= k0) and (k1 <= s0 or s1 <= k0) and (v1 <= s0 or s1 <= v0) and _apart(kv, k0, k1)
+            and _apart(kv, v0, v1))
+
+
 def bd_kv_read(kv: bd_kv_cache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None):
     """The rows of T slots (int32 [T]) as bf16 (k, v), each [T, num_heads, head_dim], exactly as held.  Slots below 0
-    give zeros, slots past the cache's end NaN."""
+    give zeros, slots past the cache's end NaN.  out, if given, lies apart from the cache's rows and from slots."""
     _cache(kv)
     _tensor("slots", slots)
     dev, n = kv._dev, slots.numel()
     shape = (n, kv.num_heads, kv.head_dim)
-    if out is not None or not _index("slots", slots, n, dev):
+    if not (_index("slots", slots, n, dev) and (out is None or _read_to(kv, out, slots, shape, dev))):
         _plain("slots", slots, torch.int32, shape[:1])
         given = [] if out is None else list(zip(("out[0]", "out[1]"), out, strict=True))
         for name, t in given:
             _plain(name, t, torch.bfloat16, shape)
         if given and n and _overlap(*out):
             raise ValueError("out[0] overlaps out[1]")
+        for name, t in given:
+            if n and _overlap(t, slots):
+                raise ValueError("%s overlaps slots" % name)
+        _refuse_on_cache(kv, given)
         _same_gpu(kv.device, [("slots", slots)] + given)
     if _current_device() != dev:
         with torch.cuda.device(dev):

@@ -90,3 +90,30 @@ def test_written_rows_in_the_gaps_of_the_cache(monkeypatch):
         bd.bd_kv_write(kv, flat[2 * 2048:].as_strided((3, 2, 64), (8192, 1024, 1)), far[:3], slots[:3])
     with pytest.raises(ValueError, match="k overlaps the cache"):
         bd.bd_kv_write(kv, cut, far[:3], slots[:3])
+
+
+def test_rows_read_back_apart_from_the_cache_and_the_slots(monkeypatch):
+    k, v = (torch.zeros((6, 2, 16, 64), dtype=BF) for _ in range(2))
+    slots = torch.zeros(16, dtype=torch.int32)
+    out = [torch.zeros((16, 2, 64), dtype=BF) for _ in range(2)]
+    kv = _cache(monkeypatch, k, v)
+    rows = k.view(-1)[2048:4096].view(16, 2, 64)
+    for a, b, match in ((rows, out[1], r"out\[0\] overlaps the cache"), (out[0], v.view(-1)[:2048].view(16, 2, 64), r"out\[1\] overlaps the cache"),
+                        (out[0], out[1], "GPU")):
+        with pytest.raises(ValueError, match=match):
+            bd.bd_kv_read(kv, slots, out=(a, b))
+    with pytest.raises(ValueError, match=r"out\[1\] overlaps slots"):
+        bd.bd_kv_read(kv, out[1].view(torch.int32).view(-1)[-16:], out=out)
+    s = [torch.zeros(16 * 2 * 64 * 2, dtype=torch.uint8) for _ in range(2)]
+    k8, v8 = (torch.zeros((6, 2, 16, 64), dtype=torch.uint8).view(E4) for _ in range(2))
+    kv = _cache(monkeypatch, k8, v8, *(t[-192:].view(6, 2, 16) for t in s))
+    for i in (0, 1):
+        with pytest.raises(ValueError, match=r"out\[0\] overlaps the cache"):
+            bd.bd_kv_read(kv, slots, out=(s[i].view(BF).view(16, 2, 64), out[1]))
+    # in the gaps of the cache's strides
+    both = torch.zeros((6, 2, 2, 16, 64), dtype=BF)
+    kv = _cache(monkeypatch, both[:, 0], torch.zeros_like(both)[:, 0])
+    with pytest.raises(ValueError, match="GPU"):
+        bd.bd_kv_read(kv, slots, out=(both[2, 1].view(16, 2, 64), out[1]))
+    with pytest.raises(ValueError, match="overlaps the cache"):
+        bd.bd_kv_read(kv, slots, out=(both[2, 0].view(16, 2, 64), out[1]))
