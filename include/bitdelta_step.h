@@ -163,7 +163,8 @@ bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t*
  *               only a q . k itself past fp32's range counts as infinite.
  *   out         [B, num_q_heads, head_dim] bf16, 16-byte aligned.
  *   lse         [B, num_q_heads] fp32, the natural logarithm of
- *               sum_j exp(scale * q . k_j); NULL if not wanted.
+ *               sum_j exp(scale * q . k_j); NULL if not wanted.  out and lse
+ *               lie apart from each other and from all that is read.
  *   workspace   device scratch of at least bd_attend_workspace_bytes(...)
  *               bytes, 16-byte aligned; may be NULL when that is 0.  The
  *               tokens of all sequences are split evenly over the GPU; the

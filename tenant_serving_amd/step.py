@@ -45,6 +45,7 @@ class _KV(ctypes.Structure):
 
 _Pair = ctypes.c_int64 * 2
 _NO_END = 1 << 64
+_SIZE = (2, 4, 1)  # bytes of a value, by its type
 
 
 def declare(lib):
@@ -443,12 +444,12 @@ def bd_kv_write(kv: bd_kv_cache, k: torch.Tensor, v: torch.Tensor, slots: torch.
     if v_kind != kind or v_n != T:
         raise ValueError("k and v must have one dtype and one number of tokens")
     # the ordinary call: k, v and all between them (one q, k, v result, mostly) and slots outside the cache's spans
-    k0, v0, ends = k.data_ptr(), v.data_ptr(), kv._bounds
+    k0, v0, size, ends = k.data_ptr(), v.data_ptr(), _SIZE[kind], kv._bounds
     at = bisect_right(ends, k0 if k0 < v0 else v0)
     upto = ends[at] if at < len(ends) else _NO_END
     if not (_index("slots", slots, T, dev) and k.get_device() == dev and v.get_device() == dev
-            and (not at & 1 and k0 + 4 * k_reach <= upto and v0 + 4 * v_reach <= upto
-                 or _apart(kv, k0, k0 + 4 * k_reach) and _apart(kv, v0, v0 + 4 * v_reach))
+            and (not at & 1 and k0 + size * k_reach <= upto and v0 + size * v_reach <= upto
+                 or _apart(kv, k0, k0 + size * k_reach) and _apart(kv, v0, v0 + size * v_reach))
             and _apart(kv, slots.data_ptr(), slots.data_ptr() + 4 * T)):
         _plain("slots", slots, torch.int32, (T,))
         _refuse_on_cache(kv, (("k", k), ("v", v), ("slots", slots)))
@@ -515,13 +516,31 @@ def bd_kv_read(kv: bd_kv_cache, slots: torch.Tensor, out: tuple[torch.Tensor, to
     return k, v
 
 
-def _free(out, q, shape, dev):
-    """Whether out is a bf16 tensor of this shape that lies apart from contiguous queries."""
-    if not (type(out) is torch.Tensor and out.dtype == torch.bfloat16 and out.shape == shape and out.is_contiguous()
-            and out.get_device() == dev and q.is_contiguous()):
-        return False
-    a, b = out.data_ptr(), q.data_ptr()
-    return a + out.nbytes <= b or b + q.nbytes <= a
+def _attend_to(kv, q0, q1, page_table, lengths, out, lse, B, heads, dev):
+    """Whether out and lse, as far as given, are tensors that an attention may write to, as they nearly always are: of
+    the right kind, apart from each other and from all that it reads (queries from q0 up to q1)."""
+    mine = []
+    if out is not None:
+        if not _given(out, torch.bfloat16, (B, heads, kv.head_dim), dev):
+            return False
+        mine.append(out)
+    if lse is not None:
+        if not _given(lse, torch.float32, (B, heads), dev):
+            return False
+        mine.append(lse)
+    used = [(q0, q1)]
+    for t in (page_table, lengths):
+        used.append((t.data_ptr(), t.data_ptr() + t.nbytes))
+    for t in mine:
+        lo = t.data_ptr()
+        hi = lo + t.nbytes
+        if not _apart(kv, lo, hi):
+            return False
+        for a, b in used:
+            if a < hi and lo < b:
+                return False
+        used.append((lo, hi))
+    return True
 
 
 def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
@@ -545,12 +564,13 @@ def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
     if lse is not None:
         _plain("lse", lse, torch.float32, (B, heads))
     every = (("q", q), ("page_table", page_table), ("lengths", lengths), ("out", out), ("lse", lse))
-    _same_gpu(kv.device, every)
-    every = [(name, t) for name, t in every if t is not None and t.numel()]
-    for name, t in every:
-        for other, o in every:
+    given = [(name, t) for name, t in every if t is not None and t.numel()]
+    for name, t in given:
+        for other, o in given:
             if name in ("out", "lse") and other != name and _overlap(t, o):
                 raise ValueError("%s overlaps %s" % (name, other))
+    _refuse_on_cache(kv, [(name, t) for name, t in given if name in ("out", "lse")])
+    _same_gpu(kv.device, every)
 
 
 def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -560,19 +580,22 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     q [B, num_q_heads, head_dim] is bf16 or fp32 (any token and head strides); num_q_heads is a multiple of the cache's
     heads.  page_table int32 [B, max_pages] (rows may be strided) and lengths int32 [B] say which tokens: lengths
     counts the new one, whose row is in the cache by then.  A length of 0 gives zeros.  scale defaults to
-    head_dim^-0.5.  lse, if given, is an fp32 [B, num_q_heads] tensor that receives the log of the softmax's sum."""
+    head_dim^-0.5.  lse, if given, is an fp32 [B, num_q_heads] tensor that receives the log of the softmax's sum.  out
+    and lse lie apart from each other and from all that is read."""
     _cache(kv)
-    kind, qs, B, heads, _ = _rows("q", q, None, kv.head_dim)
+    kind, qs, B, heads, reach = _rows("q", q, None, kv.head_dim)
     dev = kv._dev
     scale = kv.head_dim ** -0.5 if scale is None else float(scale)
     if not abs(scale) <= 2.0 ** 60:
         raise ValueError("scale must be at most 2^60 (got %r)" % scale)
-    if not (lse is None and (out is None or _free(out, q, (B, heads, kv.head_dim), dev))
-            and type(page_table) is torch.Tensor and page_table.dim() == 2
+    q0 = q.data_ptr()
+    if not (type(page_table) is torch.Tensor and page_table.dim() == 2
             and page_table.dtype is _INT and page_table.shape[0] == B and page_table.is_contiguous()
             and 1 <= page_table.shape[1] <= (1 << 24) // kv.page_size and page_table.get_device() == dev
             and _index("lengths", lengths, B, dev) and q.get_device() == dev and 1 <= heads <= 65535
-            and heads % kv.num_heads == 0):
+            and heads % kv.num_heads == 0
+            and (out is None and lse is None
+                 or _attend_to(kv, q0, q0 + reach * _SIZE[kind], page_table, lengths, out, lse, B, heads, dev))):
         _refuse_attend(q, kv, page_table, lengths, out, lse, heads)
     if _current_device() != dev:
         with torch.cuda.device(dev):
@@ -586,7 +609,7 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
         else:
             out = torch.empty((B, heads, kv.head_dim), dtype=torch.bfloat16, device=kv.device)
     ws = _workspace(nbytes, kv.device)
-    st = lib.bd_attend(kv._ref, q.data_ptr(), kind, qs, heads, page_table.data_ptr(),
+    st = lib.bd_attend(kv._ref, q0, kind, qs, heads, page_table.data_ptr(),
                        page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, out.data_ptr(),
                        lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None, nbytes,
                        _stream_of(dev))

@@ -215,7 +215,8 @@ def test_wide_graph(bd):
         with torch.cuda.graph(graph):
             held = bd.bd_attend(gq, c.kv, gt, gl, lse=lse)
         first = np.concatenate([[0], np.cumsum(longest)])
-        for lens in ([2000, 700, 1, 300], [1, 1, 1, 1], [0, 0, 0, 0], [129, 700, 0, 128], [1999, 0, 1, 299], [2000, 700, 1, 300]):
+        for lens in ([2000, 700, 1, 300], [1, 1, 1, 1], [0, 0, 0, 0], [129, 700, 0, 128], [1999, 0, 1, 299],
+                     [2000, 700, 1, 300]):
             gl.copy_(torch.tensor(lens))
             held.fill_(7.0)
             lse.fill_(7.0)

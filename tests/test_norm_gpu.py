@@ -25,7 +25,8 @@ def test_squares_past_fp32(bd, d, x_t, res_t):
     x[3, : d // 2] *= 2.0 ** -60
     x[6, 0] = 2.0 ** -20                  # one larger value in a small row
     x = x.to(x_t)
-    res = None if res_t is None else (torch.randn((len(sizes), d), generator=gen) * torch.tensor(sizes)[:, None]).to(res_t)
+    res = torch.randn((len(sizes), d), generator=gen) * torch.tensor(sizes)[:, None]
+    res = None if res_t is None else res.to(res_t)
     gain = (1 + 0.3 * torch.randn((2, d), generator=gen)).to(BF if d % 16 else F32)
     ids = torch.arange(len(sizes), dtype=torch.int32) % 2
     gx, gr, gg, gi = on_gpu(x, res, gain, ids)
