@@ -160,7 +160,8 @@ bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t*
  *               outside [0, num_pages), gives rows of NaN.
  *   scale       multiplies the scores q . k; of any sign, 2^60 at most in
  *               magnitude.  Scores may be of any size before and after it:
- *               only a q . k itself past fp32's range counts as infinite.
+ *               only a q . k itself past fp32's range counts as infinite,
+ *               and an fp32 query value that rounds to infinity in bf16.
  *   out         [B, num_q_heads, head_dim] bf16, 16-byte aligned.
  *   lse         [B, num_q_heads] fp32, the natural logarithm of
  *               sum_j exp(scale * q . k_j); NULL if not wanted.  out and lse

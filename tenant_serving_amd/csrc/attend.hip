@@ -75,6 +75,9 @@ constexpr int per_cu(int width, bool split_q, bool e4m3) {
 constexpr int kRowCost = 2;
 constexpr float kLazy = 10.0f;             // log2: how large a weight may be before the maximum moves
 constexpr float kNegInf = -__builtin_inff();
+// Times the least fp32 number -infinity (a score behind the end) stays what it is,
+// times 0 it would not; and no difference of scores times it is worth 2^-20.
+constexpr float kLeastC = 0x1p-149f;
 
 struct Shape {
     int32_t heads, dim, page_size, pg8, magic;  // pg8: groups of 8 tokens in a page
@@ -92,8 +95,7 @@ struct Args {
     uint32_t pages;                         // of the cache
     uint32_t page16, head16, token16;       // its strides in units of 16 bytes
     uint32_t page_scales;                   // scale bytes of a page
-    float c;                                // |scale| log2(e), no smaller than the least normal number: times
-                                            // it, -infinity (a score behind the end) stays what it is
+    float c;                                // |scale| log2(e), no smaller than kLeastC
     uint32_t flip;                          // the queries' sign bits where scale is negative
 };
 
@@ -670,7 +672,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kE4m3)) void atte
                     for (int s = 0; s < NR; ++s)
 #pragma unroll
                         for (int k = 1; k < QT; ++k) qt[k][s] = qt[0][s];
-                    c *= 1.0f / QT;
+                    c = fmaxf(c * (1.0f / QT), kLeastC);
                 }
                 pass = 1;
                 pages = load_pages(now, t0);
@@ -936,7 +938,7 @@ hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
                      per_cu(width_of(a.kv.head_dim, a.kv.type == BD_E4M3), q_fp32, a.kv.type == BD_E4M3)),
            (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride), unit16(a.kv.token_stride),
            (uint32_t)(a.kv.num_heads * a.kv.page_size),
-           __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 1.17549435e-38f),
+           __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, kLeastC),
            a.scale < 0.0f ? 0x80008000u : 0u};
     const int D = a.kv.head_dim;
     if (workspace_of(p.s) > attend_workspace_bytes(a.B, a.Hq, a.kv.num_heads, D, a.kv.page_size, a.max_pages))

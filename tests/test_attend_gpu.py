@@ -262,3 +262,35 @@ def test_fp32_queries_hold_their_bits(bd, dim, kind, wide):
         assert np.all(np.abs(ref.to64(lse)[b] - want_lse) <= 4 * U * np.abs(want_lse) + 16 * U)
         tol = 2.0 ** -8 * np.abs(want) + (n + 64) * U * np.abs(vr).max()
         assert np.all(np.abs(ref.to64(out)[b] - want) <= tol)
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -149, 2.0 ** -140, 2.0 ** -127, -2.0 ** -126, 2.0 ** -112, -2.0 ** -110])
+@pytest.mark.parametrize("wide", [False, True])
+def test_small_scales_of_large_scores(bd, scale, wide):
+    """Scales down to 0, of scores up to 2^119 (whole numbers up to 2^12 times 2^107, exact): a weight's exponent is off by
+    the scale's own rounding, half of 2^-149 times the score at most or 2^-24 of it, and a few roundings."""
+    lens = [1, 40, 300, 129]
+    for q_t in (BF, F32):
+        for kind in (BF, E4):
+            print("small scales", scale, wide, q_t, kind, flush=True)
+            c, q, table, lens_t, slots = attend_case(bd, lens, 2, 2, 64, 16, kind, q_t)
+            table = widened(table, 16) if wide else table
+            T, gen = len(slots), gen_of(9)
+            k = torch.randint(-8, 9, (T, 2, 64), generator=gen).float() * 2.0 ** 107
+            v = torch.randn((T, 2, 64), generator=gen)
+            q = torch.randint(-8, 9, q.shape, generator=gen).to(q_t)
+            s = torch.tensor(slots, dtype=torch.int32)
+            c.expect(k, v, s)
+            bd.bd_kv_write(c.kv, k.to(DEV), v.to(DEV), s.to(DEV))
+            out, lse = run_attend(bd, c, q, table, lens_t, scale)
+            out, lse, at = ref.to64(out), ref.to64(lse), 0
+            for b, n in enumerate(lens):
+                kr = np.stack([c.row64(0, x) for x in slots[at:at + n]])
+                vr = np.stack([c.row64(1, x) for x in slots[at:at + n]])
+                at += n
+                want, want_lse, _ = ref.attend(ref.to64(q)[b], kr, vr, scale)
+                score = 2.0 ** 119
+                ds = 8 * U * score * abs(scale) + 2.0 ** -149 * score
+                tol = 2.0 ** -8 * np.abs(want) + np.abs(vr).max() * (np.expm1(2 * ds) + 2.0 ** -15 + (n + 64) * U)
+                assert np.all(np.abs(out[b] - want) <= tol), (b, np.abs(out[b] - want).max())
+                assert np.all(np.abs(lse[b] - want_lse) <= ds + 4 * U * np.abs(want_lse) + (n + 64) * U)
