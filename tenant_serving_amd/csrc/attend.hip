@@ -2,8 +2,8 @@
 //
 //   out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c (q.k_j - m)),  c = scale log2(e)
 //
-// with m the running maximum of q.k_j: one pass over the cache, which is
-// read exactly once, so the kernel is bound by HBM.
+// with m the running maximum of q.k_j: one pass over the cache for each 16
+// query heads that share a key-value head, bound by HBM.
 //
 // Layout.  The query heads that share a key-value head (up to 16 of them) are
 // the 16 columns of v_mfma_f32_16x16x32_bf16; a wave takes 32 tokens at a
@@ -883,7 +883,7 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     s.page_size = (int32_t)page_size;
     s.pg8 = (int32_t)(page_size / 8);
     // g8 / pg8 = umulhi(g8, magic): exact while g8 * pg8 < 2^32.  pg8 == 1
-    // would need 2^32; its magic is 0 and page_index adds g8.
+    // would need 2^32; its magic is 0 and look_up adds g8.
     s.magic = s.pg8 == 1 ? 0 : (int32_t)(uint32_t)((uint64_t(1) << 32) / s.pg8 + 1);
     s.group = (int32_t)(Hq / H);
     s.tiles = (s.group + 15) / 16;
@@ -903,19 +903,21 @@ size_t workspace_of(const Shape& s) {
     return s.whole ? 0 : (size_t)s.crosses * sizeof(Cross) + (size_t)s.groups * 2 * 16 * (s.dim + 2) * sizeof(float);
 }
 
+template <int kDC, bool kFull, bool kE4m3>
+void go_queries(const Args& p, bool q_fp32, hipStream_t s) {
+    const dim3 grid((unsigned)p.s.groups), block(kWaves * 64);
+    if (q_fp32)
+        hipLaunchKernelGGL((attend_kernel<kDC, kFull, kE4m3, true>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((attend_kernel<kDC, kFull, kE4m3, false>), grid, block, 0, s, p);
+}
+// The kernels that some head_dim has: below 96 (bf16) and 192 (e4m3) width_of goes elsewhere.
 template <int kDC, bool kFull>
 void go(const Args& p, bool q_fp32, hipStream_t s) {
-    const dim3 grid((unsigned)p.s.groups), block(kWaves * 64);
     if (p.a.kv.type == BD_E4M3) {
-        if (q_fp32)
-            hipLaunchKernelGGL((attend_kernel<kDC, kFull, true, true>), grid, block, 0, s, p);
-        else
-            hipLaunchKernelGGL((attend_kernel<kDC, kFull, true, false>), grid, block, 0, s, p);
+        if constexpr (kFull || kDC != 192) go_queries<kDC, kFull, true>(p, q_fp32, s);
     } else {
-        if (q_fp32)
-            hipLaunchKernelGGL((attend_kernel<kDC, kFull, false, true>), grid, block, 0, s, p);
-        else
-            hipLaunchKernelGGL((attend_kernel<kDC, kFull, false, false>), grid, block, 0, s, p);
+        if constexpr (kFull || kDC != 96) go_queries<kDC, kFull, false>(p, q_fp32, s);
     }
 }
 
