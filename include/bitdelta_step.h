@@ -62,7 +62,8 @@ typedef enum bd_type {
  *   scales       [M, ceil(d / 32)] uint8 for BD_E4M3: groups of 32 columns,
  *                the last one of the rest.  NULL for BD_BF16.
  * d: a multiple of 8, 8 .. 65536.  eps >= 0.  x, residual, residual_out,
- * gain, out: 16-byte aligned (out: 8 for BD_E4M3).  M == 0 is a no-op.
+ * gain, out: 16-byte aligned (out: 8 for BD_E4M3).  M <= 2^31 - 1; M == 0 is
+ * a no-op.
  * fp32 throughout for a bf16 result (a row whose squares leave fp32's range is
  * scaled by a power of two first, so h may be of any size); for codes the sum,
  * root and products are 64-bit and y is rounded once, to its code (a finite y
@@ -123,7 +124,8 @@ typedef struct bd_kv {
  *            not written.  A slot named by several tokens holds the last of
  *            them afterwards.
  * A BD_BF16 cache rounds once (nearest even); a BD_E4M3 cache holds each row
- * as one group.  Every other slot stays as it was.  T == 0 is a no-op.
+ * as one group.  Every other slot stays as it was.  T <= 2^28; T == 0 is a
+ * no-op.
  * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _HIP, _DEVICE. */
 bd_status bd_kv_write(const bd_kv* kv, const void* k, const int64_t* k_strides, const void* v,
                       const int64_t* v_strides, int32_t in_type, const int32_t* slots, int64_t T, void* stream);
@@ -131,7 +133,8 @@ bd_status bd_kv_write(const bd_kv* kv, const void* k, const int64_t* k_strides, 
 /* Reads rows back: k_out, v_out [T, num_heads, head_dim] bf16, 16-byte
  * aligned, apart from each other, the slots and the cache's rows and scale
  * bytes; the exact value of every held row.  A slot below 0 gives zeros (a
- * padding token), one past the last page NaN.  T == 0 is a no-op.
+ * padding token), one past the last page NaN.  T <= 2^31 - 1; T == 0 is a
+ * no-op.
  * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _HIP, _DEVICE. */
 bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t* k_out, uint16_t* v_out,
                      void* stream);
@@ -150,7 +153,10 @@ bd_status bd_kv_read(const bd_kv* kv, const int32_t* slots, int64_t T, uint16_t*
  *               two, multiples of 16 bytes).  num_q_heads is a multiple of
  *               num_heads, at most 65535.
  *   page_table  [B, max_pages] int32, rows table_stride elements apart.
- *               max_pages * page_size <= 2^24.
+ *               max_pages * page_size <= 2^24; with R = B * num_heads *
+ *               ceil(num_q_heads / num_heads / 16) rows of
+ *               U = ceil(max_pages * page_size / 128) units, R <= 2^23 and
+ *               R * (U + 4) <= 2^30.
  *   lengths     [B] int32: tokens to attend to, the new one among them (its
  *               row has been written by then).  0 or less: the sequence's
  *               rows of out are zeros, of lse -infinity.  Only the pages that
