@@ -38,6 +38,8 @@
 // partial results (sum, maximum, unnormalised output) in the workspace, and
 // join_kernel adds them in workgroup order.  Where the table has room for few
 // units a row stays in one piece instead, and nothing is joined (see is_whole).
+// fp32 queries' third term costs up to 4% (31 sequences of 4000 tokens, 32 heads
+// of 256, e4m3 59.4 -> 61.8 us; of 128, bf16 52.6 -> 52.7).
 #include "step_internal.h"
 
 namespace bd {

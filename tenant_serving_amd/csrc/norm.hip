@@ -14,7 +14,7 @@
 // products are 64-bit: in 32 bits a few codes in a million fall on the other
 // side of their border.  The extra work hides behind the memory where there is a
 // residual (8192 x 8192 with an fp32 one 134.9 us in 32 bits, 134.5 in 64);
-// without one it is what bounds the call (2048 x 16384 from bf16 32 us, 3.2 TB/s).
+// without one it is what bounds the call (2048 x 16384 from bf16 33 us, 3.1 TB/s).
 #include "step_internal.h"
 
 #include <type_traits>
@@ -39,8 +39,10 @@ constexpr int kNormBlock = NT == 64 ? 256 : NT;
 // as little of them can still be in the 256 MiB last-level cache then: 2048 x
 // 28672 of bf16 94 -> 82 us (5.7 TB/s), 8192 x 8192 with fp32 x 118 -> 106; below,
 // what the linear just wrote is found there (2048 x 8192 with fp32 x, 100 MB,
-// 29.6 against 30.8 us).  With an fp32 residual plain loads stay ahead (8192 x
-// 8192 to e4m3 135 against 141), without one they are level.
+// 29.6 against 30.8 us).  Narrow rows gain 0 to 6% (1048576 x 128 of bf16 324 ->
+// 304, 262144 x 512 with fp32 x 234 -> 224, 65536 x 2048 232 -> 227; to e4m3
+// they are level).  With an fp32 residual plain loads stay ahead (8192 x 8192 to
+// e4m3 135 against 141), without one they are level.
 constexpr int64_t kStreamBytes = int64_t(192) << 20;
 
 // kRes: 0 no residual, 1 bf16, 2 fp32.  NT lanes own a row (64: four rows to a
@@ -216,7 +218,9 @@ void go(const NormArgs& a, hipStream_t s) {
 // CU holds several rows.  2048 rows in e4m3 with an fp32 residual, this choice
 // against twice the lanes or the next power of two of chunks: 6000 wide 30.5 ->
 // 28.3 us, 9272 53.8 -> 43.4, 12000 66.2 -> 52.1, 16384 81.5 -> 78.2; past 16384
-// 512 lanes would lose (28672 156.5 -> 165.5).
+// 512 lanes would lose (28672 156.5 -> 165.5).  Past 32768 columns 8 chunks are
+// more than the 128 registers of 1024 lanes hold in most forms: 1024 x 65536 runs
+// at 2.9 to 5.8 TB/s to bf16 and 1.3 to 2.3 to e4m3.
 template <bool kX32, int kRes, bool kE4m3, bool kStream>
 void pick(const NormArgs& a, hipStream_t s) {
     if (a.d <= 512) return go<kX32, kRes, kE4m3, kStream, 64, 1>(a, s);

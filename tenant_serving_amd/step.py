@@ -9,7 +9,8 @@ there is no fallback.
 A step of a served model runs, per layer: ``bd_rms_norm`` (the residual added,
 each token normed with its variant's gain), the q, k, v linears,
 ``bd_kv_write``, ``bd_attend``, the output linear, ``bd_rms_norm`` again and
-the remaining linears.
+the remaining linears.  Rotary embeddings, where a model has them, are the
+caller's, on q and k before the cache.
 """
 
 from __future__ import annotations
@@ -581,7 +582,9 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     heads.  page_table int32 [B, max_pages] (rows may be strided) and lengths int32 [B] say which tokens: lengths
     counts the new one, whose row is in the cache by then.  A length of 0 gives zeros.  scale defaults to
     head_dim^-0.5.  lse, if given, is an fp32 [B, num_q_heads] tensor that receives the log of the softmax's sum.  out
-    and lse lie apart from each other and from all that is read."""
+    and lse lie apart from each other and from all that is read.  Where the table has room for few tokens (some
+    hundreds, whatever the lengths) nothing is split and no second kernel is launched: for short sequences a table no
+    wider than needed is faster."""
     _cache(kv)
     kind, qs, B, heads, reach = _rows("q", q, None, kv.head_dim)
     dev = kv._dev
