@@ -294,3 +294,39 @@ def test_small_scales_of_large_scores(bd, scale, wide):
                 tol = 2.0 ** -8 * np.abs(want) + np.abs(vr).max() * (np.expm1(2 * ds) + 2.0 ** -15 + (n + 64) * U)
                 assert np.all(np.abs(out[b] - want) <= tol), (b, np.abs(out[b] - want).max())
                 assert np.all(np.abs(lse[b] - want_lse) <= ds + 4 * U * np.abs(want_lse) + (n + 64) * U)
+
+
+@pytest.mark.parametrize("dim", [16, 64, 80, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("q_t", [BF, F32])
+@pytest.mark.parametrize("wide", [False, True])
+def test_infinite_keys_at_every_width(bd, dim, q_t, wide):
+    """A score of -infinity drops out and an infinite value stays in its column, wherever the queries' terms are held.
+    fp32 queries in a part that such a key broke are one bf16 term, half a step of it (2^-8) off."""
+    print("infinite keys", dim, q_t, wide, flush=True)
+    lens = [70, 300, 380]
+    c, q, table, lens_t, slots = attend_case(bd, lens, 1, 3, dim, 16, BF, q_t)
+    table = widened(table, 16) if wide else table[:, :24].contiguous()
+    gen = gen_of(dim)
+    k, v = (torch.randn((sum(lens), 1, dim), generator=gen).to(BF) for _ in range(2))
+    q = (q.abs() + 0.1).to(q_t)
+    k[5, 0, 0] = -float("inf")
+    k[200, 0, dim - 1] = -float("inf")
+    v[300, 0, 7] = float("inf")
+    s = torch.tensor(slots, dtype=torch.int32)
+    c.expect(k, v, s)
+    bd.bd_kv_write(c.kv, k.to(DEV), v.to(DEV), s.to(DEV))
+    out, lse = run_attend(bd, c, q, table, lens_t)
+    out, lse, at = ref.to64(out), ref.to64(lse), 0
+    for b, n in enumerate(lens):
+        kr = np.stack([c.row64(0, x) for x in slots[at:at + n]])
+        vr = np.stack([c.row64(1, x) for x in slots[at:at + n]])
+        at += n
+        want, want_lse, S = ref.attend(ref.to64(q)[b], kr, vr, dim ** -0.5)
+        one_term = q_t == F32 and b < 2
+        ds = (3 * dim + 8) * U * S + (2.0 ** -8 * S if one_term else 0.0)
+        vmax = np.abs(vr[np.isfinite(vr)]).max()
+        tol = 2.0 ** -8 * np.abs(want) + 2 * vmax * (np.expm1(2 * ds) + 2.0 ** -8 + (n + 64) * U)
+        inf = np.isinf(want)
+        assert np.array_equal(np.isinf(out[b]), inf) and (out[b][inf] > 0).all()
+        assert np.all(np.abs(out[b][~inf] - want[~inf]) <= tol[~inf])
+        assert np.all(np.abs(lse[b] - want_lse) <= ds + (n + 64) * U + 4 * U * np.abs(want_lse))
