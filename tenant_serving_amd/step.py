@@ -336,20 +336,36 @@ class bd_kv_cache:
                 raise ValueError("rows of k overlap (strides %s)" % (tuple(k.stride()),))
             extent = s * (n - 1) + extent
         self._span = extent * size
-        self._steps, self._row = [(s * size, n) for s, n in reversed(steps)], dim * size
         if kind == BD_E4M3:
             for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
                 _plain(name, t, torch.uint8, (pages, heads, page))
                 if t.data_ptr() % 8:
                     raise ValueError("%s must be 8-byte aligned" % name)
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("a bf16 cache has no scales")
+        # where the arrays are: each as _on_rows takes it, and the ends of their spans in rising order, those that meet
+        # taken together
+        row, steps = dim * size, [(s * size, n) for s, n in reversed(steps)]
+        self._arrays = [(k.data_ptr(), steps, row), (v.data_ptr(), steps, row)]
+        spans = [(at, at + self._span) for at, _, _ in self._arrays]
+        if kind == BD_E4M3:
+            for t in (k_scales, v_scales):
+                self._arrays.append((t.data_ptr(), [], t.nbytes))
+                spans.append((t.data_ptr(), t.data_ptr() + t.nbytes))
+        bounds = []
+        for lo, hi in sorted(spans):
+            if bounds and lo <= bounds[-1]:
+                bounds[-1] = max(bounds[-1], hi)
+            else:
+                bounds += [lo, hi]
+        self._bounds = bounds
+        if kind == BD_E4M3 and len(bounds) < 8:
             if _overlap(k_scales, v_scales):
                 raise ValueError("k_scales overlaps v_scales")
             for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
                 for other, rows in (("k", k), ("v", v)):
-                    if _on_rows(rows.data_ptr(), self._steps, self._row, *_span(t)):
+                    if _on_rows(rows.data_ptr(), steps, row, *_span(t)):
                         raise ValueError("%s overlaps %s" % (name, other))
-        elif k_scales is not None or v_scales is not None:
-            raise ValueError("a bf16 cache has no scales")
         _same_gpu(k.device, (("v", v), ("k_scales", k_scales), ("v_scales", v_scales)))
         if abs(k.data_ptr() - v.data_ptr()) < self._span and not self._interleaved(k, v, stride, size):
             raise ValueError("k and v overlap")
@@ -359,18 +375,6 @@ class bd_kv_cache:
         self._desc = _KV(k.data_ptr(), v.data_ptr(), _at(k_scales), _at(v_scales), kind, heads, dim, page, pages,
                          *stride[:3])
         self._ref = ctypes.addressof(self._desc)
-        # where the arrays are: each as _on_rows takes it, and the ends of their spans in rising order, those that meet
-        # taken together
-        self._arrays = [(t.data_ptr(), self._steps, self._row) for t in (k, v)]
-        self._arrays += [(t.data_ptr(), [], t.nbytes) for t in (k_scales, v_scales) if t is not None]
-        spans = sorted((at, at + (self._span if steps else row)) for at, steps, row in self._arrays)
-        bounds = []
-        for lo, hi in spans:
-            if bounds and lo <= bounds[-1]:
-                bounds[-1] = max(bounds[-1], hi)
-            else:
-                bounds += [lo, hi]
-        self._bounds = bounds
 
     @staticmethod
     def _interleaved(k, v, stride, size):
