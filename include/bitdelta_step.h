@@ -1,8 +1,8 @@
 /*
  * bitdelta_step.h -- what a serving step needs between the linears of
  * bitdelta.h: the RMS norm that makes a linear's bf16 x out of the previous
- * linear's result, the paged key-value cache, and the attention of one new
- * token over it.
+ * linear's result, rotary positions, the paged key-value cache, and the
+ * attention of new tokens over it.
  *
  * "Serving architecture" of the post (see bitdelta.h) keeps one base and many
  * deltas on a GPU, which leaves little of its memory for keys and values:
@@ -23,6 +23,14 @@
  *   on it: the division and the read-back are exact, and 448 is never passed.
  *   Code times scale is exact in bf16 (a value so large that it rounds to
  *   2^128 reads as infinity, as it does when rounded to bf16).
+ * - e2m1 groups.  32 neighbouring values of a row are held as OCP e2m1 codes
+ *   (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one scale byte: with a
+ *   the group's largest magnitude, e is the smallest whole number, at least
+ *   -125, for which a <= 6 * 2^e; the byte is e + 127 and the code of x is
+ *   x / 2^e rounded to e2m1 (nearest, ties to the even code).  A group with a
+ *   value that is not finite gets the byte 255, which makes NaN of all of it.
+ *   Code times scale is exact in bf16, as with e4m3; any other byte b stands
+ *   for 2^(b - 127).  Two codes share a byte, the first in its low half.
  * - Ids, slots, pages and lengths live on the device and cannot be checked on
  *   the host: each call says what it does with one out of range.  None makes
  *   it touch memory outside the arguments.
@@ -39,7 +47,8 @@ extern "C" {
 typedef enum bd_type {
     BD_BF16 = 0,
     BD_FP32 = 1,
-    BD_E4M3 = 2
+    BD_E4M3 = 2,
+    BD_E2M1 = 4
 } bd_type;
 
 /* ---------------------------------------------------------------------------
@@ -77,19 +86,61 @@ bd_status bd_rms_norm(const void* x, int32_t x_type, const void* residual, void*
                       int64_t M, int64_t d, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Rotary positions: the first `turned` columns of each row are turned in pairs
+ * by an angle that grows with the row's position,
+ *
+ *   a' = gain (a cos t - b sin t),  b' = gain (b cos t + a sin t)
+ *   t  = 2 pi positions[token] steps[i] / 2^64
+ *
+ * for pair i = (i, i + turned / 2), or (2 i, 2 i + 1) where `interleaved` is
+ * not 0.  The other columns stay (they are copied where out is not x).
+ *
+ *   rows        HOST array of `count` (1 or 2) tensors of one call, queries and
+ *               keys: x [T, heads, head_dim] in x_type, out in out_type (each
+ *               BD_BF16 or BD_FP32), 16-byte aligned.  Token t's row of head h
+ *               starts at element t * strides[0] + h * strides[1]; strides are
+ *               multiples of 16 bytes.  out may be x itself (same address,
+ *               strides and type); otherwise what is written lies apart from
+ *               all else of the call.  heads 1 .. 65535.
+ *   head_dim    a multiple of 16, 16 .. 256.   turned: even, 2 .. head_dim.
+ *   positions   [T] int32, of any size and sign: -p undoes p where gain is 1.
+ *   steps       [turned / 2] uint64, 8-byte aligned: the part of a turn that a
+ *               position adds, as a fraction of 2^64.  Its product with a
+ *               position wraps as the angle does, so that no position is too
+ *               far: a pair's angle is exact to 2^-32 of a turn (1.5e-9).
+ *   gain        finite (1 but where a scaled context asks for another).
+ * Products and sums are fp32, results rounded once.  T <= 2^31 - 1; T == 0 is
+ * a no-op.
+ * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _HIP, _DEVICE.
+ * ------------------------------------------------------------------------- */
+typedef struct bd_rotary_rows {
+    const void* x;
+    void* out;
+    int64_t x_strides[2];
+    int64_t out_strides[2];
+    int32_t heads;
+} bd_rotary_rows;
+
+bd_status bd_rotary(const bd_rotary_rows* rows, int32_t count, int32_t x_type, int32_t out_type, int32_t head_dim,
+                    int32_t turned, int32_t interleaved, const int32_t* positions, const uint64_t* steps,
+                    float gain, int64_t T, void* stream);
+
+/* ---------------------------------------------------------------------------
  * The paged key-value cache: two arrays of pages, each with `page_size`
  * tokens of `num_heads` rows of `head_dim` values.  Token `slot` is place
  * slot % page_size of page slot / page_size; its row of head h starts at
  * element page * page_stride + h * head_stride + place * token_stride, in
- * `k` and in `v` alike.
+ * `k` and in `v` alike.  An element is a value, or for BD_E2M1 a byte of two.
  *
- *   type       BD_BF16 or BD_E4M3 (one group per row).
+ *   type       BD_BF16, BD_E4M3 (one group per row) or BD_E2M1 (one group per
+ *              32 values of a row).
  *   k_scales, v_scales   BD_E4M3: [num_pages, num_heads, page_size] uint8,
+ *              BD_E2M1: [num_pages, num_heads, head_dim / 32, page_size],
  *              contiguous, 8-byte aligned; NULL for BD_BF16.
  *   num_pages  >= 1, num_pages * page_size <= 2^31 - 1.
  *   page_size  a multiple of 8, 8 .. 4096.
  *   num_heads  1 .. 65535.
- *   head_dim   a multiple of 16, 16 .. 256.
+ *   head_dim   a multiple of 16, 16 .. 256; for BD_E2M1 a multiple of 32.
  *   strides    in elements, >= 0, multiples of 16 bytes and below 2^36 bytes;
  *              distinct rows must not overlap.  k, v: 16-byte aligned.
  * Rows of k, rows of v, k_scales and v_scales lie apart from each other (k's
@@ -124,7 +175,7 @@ typedef struct bd_kv {
  *            not written.  A slot named by several tokens holds the last of
  *            them afterwards.
  * A BD_BF16 cache rounds once (nearest even); a BD_E4M3 cache holds each row
- * as one group.  Every other slot stays as it was.  T <= 2^28; T == 0 is a
+ * as one group, a BD_E2M1 cache as head_dim / 32 of them.  Every other slot stays as it was.  T <= 2^28; T == 0 is a
  * no-op.
  * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _HIP, _DEVICE. */
 bd_status bd_kv_write(const bd_kv* kv, const void* k, const int64_t* k_strides, const void* v,

@@ -17,7 +17,7 @@ LIBRARY = os.path.join(PKG, "libbitdelta.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["api.cpp", "cache.cpp", "compress.hip", "decode.hip", "shot.hip", "slice.hip", "gemv.hip", "quad.hip", "band.hip", "skinny.hip", "rowstream.hip", "prefill.hip",
-           "grouped.hip", "gdec.hip", "step_api.cpp", "norm.hip", "kv.hip", "attend.hip"]
+           "grouped.hip", "gdec.hip", "step_api.cpp", "norm.hip", "rotary.hip", "kv.hip", "attend.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,5 +1,6 @@
 // The paged key-value cache's rows, written (rounded to bf16, or held as e4m3
-// codes with one power-of-two scale) and read back.
+// codes with one power-of-two scale, or as e2m1 codes with one per 32 values)
+// and read back.
 //
 // Bound by HBM: every row is read once and written once.  A row is held by a
 // group of neighbouring lanes, 8 values each (the group rounded up to a power
@@ -43,20 +44,6 @@ constexpr int64_t kSmallGroups = 2048, kGroups = 1024;
 constexpr int64_t kSlice = 32768;
 static_assert(kSmallWrite <= 2 * kSmallGroups && kSlice <= 32 * kGroups, "tables of kv_write_kernel");
 
-// n / d for 0 <= n < 2^31 by a product: m = ceil(2^s / d) with s = 31 + ceil(log2 d)
-// is below 2^32 and too large by less than d / 2^s, which n cannot carry over.
-struct Div {
-    uint32_t d, m, shift;  // shift: s - 32
-    __host__ explicit Div(uint32_t by) : d(by) {
-        int up = 0;
-        while ((uint64_t(1) << up) < by) ++up;
-        m = (uint32_t)(((uint64_t(1) << (31 + up)) + by - 1) / by);
-        shift = up > 0 ? up - 1 : 0;
-        if (up == 0) m = 0;  // by 1: see by()
-    }
-    __device__ __forceinline__ uint32_t by(uint32_t n) const { return m ? __umulhi(n, m) >> shift : n; }
-};
-
 struct WriteArgs {
     bd_kv kv;
     const void* k;
@@ -95,7 +82,7 @@ __device__ __forceinline__ uint32_t group_max(uint32_t x) {
 // way.  A slot outside the range of its own (256 lanes, where these are one or
 // two), or without their bit in a table of 65536 (1024 lanes), is none of
 // them; the rest are compared.
-template <bool kX32, bool kE4m3, int kLanes, int kWide>
+template <bool kX32, int kHeld, int kLanes, int kWide>
 __global__ __launch_bounds__(kWide) void kv_write_kernel(const WriteArgs a) {
     constexpr int kMost = kWide == 256 ? 2 : 32;  // tokens of a workgroup
     __shared__ int own[kMost], dead[kMost];
@@ -138,7 +125,7 @@ __global__ __launch_bounds__(kWide) void kv_write_kernel(const WriteArgs a) {
         dead[tid] = s < 0;
         const int page = s < 0 ? 0 : (int)a.page.by((uint32_t)s), at = s < 0 ? 0 : s - page * a.kv.page_size;
         to_row[tid] = page * a.kv.page_stride + at * a.kv.token_stride;
-        to_scale[tid] = (int64_t)page * H * a.kv.page_size + at;
+        to_scale[tid] = (int64_t)page * H * (kHeld == BD_E2M1 ? a.kv.head_dim / kGroup4 : 1) * a.kv.page_size + at;
         if (s >= 0) {
             if (kWide == 256) {  // as unsigned, -1 is above every slot
                 atomicMin(reinterpret_cast<unsigned*>(&range[0]), (unsigned)s);
@@ -199,9 +186,26 @@ __global__ __launch_bounds__(kWide) void kv_write_kernel(const WriteArgs a) {
         const int i = (int)a.row.by((uint32_t)r), hv = r - i * 2 * H;
         const bool is_v = hv >= H;
         const int head = is_v ? hv - H : hv;
-        const int64_t to = to_row[i] + head * a.kv.head_stride + e;
+        const int64_t to = to_row[i] + head * a.kv.head_stride + (kHeld == BD_E2M1 ? e / 2 : e);
         const bool keep = !dead[i];
-        if (kE4m3) {
+        if (kHeld == BD_E2M1) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t b = __float_as_uint(f[x]) & 0x7fffffffu;
+                top = b > top ? b : top;
+            }
+            top = max_dpp<0x4e>(max_dpp<0xb1>(top));  // of four lanes
+            const int byte = scale_byte4(top);
+            const uint32_t codes = byte == kNanByte ? 0u : pack_e2m1x8(f, inv_scale_of(byte));
+            if (in && keep) {
+                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(is_v ? a.kv.v : a.kv.k) + to) = codes;
+                if (lane % 4 == 0) {
+                    const int64_t row = (int64_t)head * (a.kv.head_dim / kGroup4) + lane / 4;
+                    (is_v ? a.kv.v_scales : a.kv.k_scales)[to_scale[i] + row * a.kv.page_size] = (uint8_t)byte;
+                }
+            }
+        } else if (kHeld == BD_E4M3) {
             uint32_t top = 0;
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
@@ -224,11 +228,11 @@ __global__ __launch_bounds__(kWide) void kv_write_kernel(const WriteArgs a) {
     }
 }
 
-// Eight held values: bf16, or codes and their row's scale byte.
-template <bool kE4m3>
+// Eight held values: bf16, or codes and their group's scale byte.
+template <int kHeld>
 struct Held;
 template <>
-struct Held<false> {
+struct Held<BD_BF16> {
     uint4 w;
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const void* p, int64_t i, const uint8_t*, int64_t) {
@@ -237,7 +241,7 @@ struct Held<false> {
     __device__ __forceinline__ uint4 value() const { return w; }
 };
 template <>
-struct Held<true> {
+struct Held<BD_E4M3> {
     uint2 w;
     int byte;
     __device__ __forceinline__ void zero() { w = make_uint2(0, 0), byte = 127; }
@@ -252,6 +256,18 @@ struct Held<true> {
     }
 };
 
+template <>
+struct Held<BD_E2M1> {
+    uint32_t w;
+    int byte;
+    __device__ __forceinline__ void zero() { w = 0, byte = 127; }
+    __device__ __forceinline__ void load(const void* p, int64_t i, const uint8_t* scales, int64_t s) {
+        w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + i);
+        byte = scales[s];
+    }
+    __device__ __forceinline__ uint4 value() const { return e2m1x8_to_bf16(w, scale_of(byte)); }
+};
+
 struct ReadArgs {
     bd_kv kv;
     const int32_t* slots;
@@ -264,13 +280,13 @@ struct ReadArgs {
 
 // A lane reads its piece of kRows rows of keys and of as many rows of values
 // before it writes any of them.
-template <bool kE4m3, int kLanes, bool kStream>
+template <int kHeld, int kLanes, bool kStream>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(const ReadArgs a) {
     constexpr int kPer = kThreads / kLanes;  // rows at a time
     const int e = ((int)threadIdx.x % kLanes) * 8;
     if (e >= a.kv.head_dim) return;
     const int64_t r0 = (int64_t)blockIdx.x * (kPer * kReadRows) + threadIdx.x / kLanes;
-    Held<kE4m3> x[kReadRows][2];
+    Held<kHeld> x[kReadRows][2];
     int slot[kReadRows];
 #pragma unroll
     for (int i = 0; i < kReadRows; ++i) {
@@ -283,8 +299,11 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(const ReadArgs a) {
             slot[i] = a.slots[t];
             if (slot[i] >= 0 && slot[i] < a.capacity) {
                 const int page = (int)a.page.by((uint32_t)slot[i]), at = slot[i] - page * a.kv.page_size;
-                const int64_t from = page * a.kv.page_stride + head * a.kv.head_stride + at * a.kv.token_stride + e;
-                const int64_t sc = ((int64_t)page * a.kv.num_heads + head) * a.kv.page_size + at;
+                const int64_t from = page * a.kv.page_stride + head * a.kv.head_stride + at * a.kv.token_stride +
+                                     (kHeld == BD_E2M1 ? e / 2 : e);
+                int64_t sc = (int64_t)page * a.kv.num_heads + head;
+                if (kHeld == BD_E2M1) sc = sc * (a.kv.head_dim / kGroup4) + e / kGroup4;
+                sc = sc * a.kv.page_size + at;
                 x[i][0].load(a.kv.k, from, a.kv.k_scales, sc);
                 x[i][1].load(a.kv.v, from, a.kv.v_scales, sc);
             }
@@ -301,27 +320,27 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(const ReadArgs a) {
     }
 }
 
-template <bool kX32, bool kE4m3, int kLanes>
+template <bool kX32, int kHeld, int kLanes>
 void write_wide(const WriteArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)((a.T + a.per - 1) / a.per));
     if (a.T <= kSmallWrite)
-        hipLaunchKernelGGL((kv_write_kernel<kX32, kE4m3, kLanes, 256>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((kv_write_kernel<kX32, kHeld, kLanes, 256>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((kv_write_kernel<kX32, kE4m3, kLanes, 1024>), grid, dim3(1024), 0, s, a);
+        hipLaunchKernelGGL((kv_write_kernel<kX32, kHeld, kLanes, 1024>), grid, dim3(1024), 0, s, a);
 }
 
-template <bool kX32, bool kE4m3>
+template <bool kX32, int kHeld>
 void write_lanes(const WriteArgs& a, hipStream_t s) {
     const int lanes = a.kv.head_dim / 8;
     if (lanes <= 8)
-        write_wide<kX32, kE4m3, 8>(a, s);
+        write_wide<kX32, kHeld, 8>(a, s);
     else if (lanes <= 16)
-        write_wide<kX32, kE4m3, 16>(a, s);
+        write_wide<kX32, kHeld, 16>(a, s);
     else
-        write_wide<kX32, kE4m3, 32>(a, s);
+        write_wide<kX32, kHeld, 32>(a, s);
 }
 
-template <bool kE4m3, bool kStream>
+template <int kHeld, bool kStream>
 void read_lanes(ReadArgs a, hipStream_t s) {
     const int lanes = a.kv.head_dim / 8 <= 8 ? 8 : a.kv.head_dim / 8 <= 16 ? 16 : 32;
     const int64_t per = kThreads / lanes;
@@ -336,20 +355,20 @@ void read_lanes(ReadArgs a, hipStream_t s) {
         b.rows = n * a.kv.num_heads;
         const dim3 grid((unsigned)((b.rows + per * kReadRows - 1) / (per * kReadRows))), block(kThreads);
         if (lanes == 8)
-            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 8, kStream>), grid, block, 0, s, b);
+            hipLaunchKernelGGL((kv_read_kernel<kHeld, 8, kStream>), grid, block, 0, s, b);
         else if (lanes == 16)
-            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 16, kStream>), grid, block, 0, s, b);
+            hipLaunchKernelGGL((kv_read_kernel<kHeld, 16, kStream>), grid, block, 0, s, b);
         else
-            hipLaunchKernelGGL((kv_read_kernel<kE4m3, 32, kStream>), grid, block, 0, s, b);
+            hipLaunchKernelGGL((kv_read_kernel<kHeld, 32, kStream>), grid, block, 0, s, b);
     }
 }
 
-template <bool kE4m3>
+template <int kHeld>
 void read_any(const ReadArgs& a, hipStream_t s) {
     if (a.rows * a.kv.head_dim * 4 >= kStreamBytes)
-        read_lanes<kE4m3, true>(a, s);
+        read_lanes<kHeld, true>(a, s);
     else
-        read_lanes<kE4m3, false>(a, s);
+        read_lanes<kHeld, false>(a, s);
 }
 
 }  // namespace
@@ -373,17 +392,12 @@ hipError_t launch_kv_write(const bd_kv& kv, const void* k, Strides2 ks, const vo
                           static_cast<const char*>(v) + t0 * vs.token * size, ks, vs, slots + t0,
                           Div((uint32_t)kv.page_size), Div((uint32_t)(2 * kv.num_heads)), (int32_t)n, (int32_t)per,
                           (int32_t)(kv.num_pages * kv.page_size)};
-        if (kv.type == BD_E4M3) {
-            if (fp32)
-                write_lanes<true, true>(a, stream);
-            else
-                write_lanes<false, true>(a, stream);
-        } else {
-            if (fp32)
-                write_lanes<true, false>(a, stream);
-            else
-                write_lanes<false, false>(a, stream);
-        }
+        if (kv.type == BD_E4M3)
+            fp32 ? write_lanes<true, BD_E4M3>(a, stream) : write_lanes<false, BD_E4M3>(a, stream);
+        else if (kv.type == BD_E2M1)
+            fp32 ? write_lanes<true, BD_E2M1>(a, stream) : write_lanes<false, BD_E2M1>(a, stream);
+        else
+            fp32 ? write_lanes<true, BD_BF16>(a, stream) : write_lanes<false, BD_BF16>(a, stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -395,9 +409,11 @@ hipError_t launch_kv_read(const bd_kv& kv, const int32_t* slots, int64_t T, uint
     const ReadArgs a{kv, slots, k_out, v_out, T * kv.num_heads, Div((uint32_t)kv.page_size),
                      Div((uint32_t)kv.num_heads), (int32_t)(kv.num_pages * kv.page_size)};
     if (kv.type == BD_E4M3)
-        read_any<true>(a, stream);
+        read_any<BD_E4M3>(a, stream);
+    else if (kv.type == BD_E2M1)
+        read_any<BD_E2M1>(a, stream);
     else
-        read_any<false>(a, stream);
+        read_any<BD_BF16>(a, stream);
     return hipGetLastError();
 }
 

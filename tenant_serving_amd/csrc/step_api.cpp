@@ -22,19 +22,20 @@ bd_status finish(hipError_t e) {
 
 bd_status check_kv(const bd_kv* kv) {
     if (!kv || !kv->k || !kv->v) return BD_ERR_NULL;
-    if (kv->type != BD_BF16 && kv->type != BD_E4M3) return BD_ERR_MODE;
-    if (kv->type == BD_E4M3 && (!kv->k_scales || !kv->v_scales)) return BD_ERR_NULL;
+    if (kv->type != BD_BF16 && kv->type != BD_E4M3 && kv->type != BD_E2M1) return BD_ERR_MODE;
+    const bool codes = kv->type != BD_BF16;
+    if (codes && (!kv->k_scales || !kv->v_scales)) return BD_ERR_NULL;
     if (kv->num_heads < 1 || kv->num_heads > 65535 || kv->head_dim < 16 || kv->head_dim > 256 ||
-        kv->head_dim % 16 != 0 || kv->page_size < 8 || kv->page_size > 4096 || kv->page_size % 8 != 0 ||
+        kv->head_dim % (kv->type == BD_E2M1 ? bd::kGroup4 : 16) != 0 || kv->page_size < 8 || kv->page_size > 4096 || kv->page_size % 8 != 0 ||
         kv->num_pages < 1 || kv->num_pages > kMaxRows / kv->page_size)
         return BD_ERR_SHAPE;
-    const int64_t unit = kv->type == BD_E4M3 ? 16 : 8;  // elements of 16 bytes
+    const int64_t unit = codes ? 16 : 8;  // elements of 16 bytes
     for (const int64_t s : {kv->page_stride, kv->head_stride, kv->token_stride}) {
         if (s < 0 || s / unit >= int64_t(1) << 32) return BD_ERR_SHAPE;
         if (s % unit != 0) return BD_ERR_ALIGN;
     }
     if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return BD_ERR_ALIGN;
-    if (kv->type == BD_E4M3 && (!aligned(kv->k_scales, 8) || !aligned(kv->v_scales, 8))) return BD_ERR_ALIGN;
+    if (codes && (!aligned(kv->k_scales, 8) || !aligned(kv->v_scales, 8))) return BD_ERR_ALIGN;
     return BD_OK;
 }
 
@@ -84,6 +85,35 @@ bd_status bd_rms_norm(const void* x, int32_t x_type, const void* residual, void*
                                   out_type == BD_E4M3, static_cast<hipStream_t>(stream)));
 }
 
+bd_status bd_rotary(const bd_rotary_rows* rows, int32_t count, int32_t x_type, int32_t out_type, int32_t head_dim,
+                    int32_t turned, int32_t interleaved, const int32_t* positions, const uint64_t* steps,
+                    float gain, int64_t T, void* stream) {
+    if (!rows || !steps || (T > 0 && !positions)) return BD_ERR_NULL;
+    if (!in_type(x_type) || !in_type(out_type)) return BD_ERR_MODE;
+    if (count < 1 || count > 2 || head_dim < 16 || head_dim > 256 || head_dim % 16 != 0 || turned < 2 ||
+        turned > head_dim || turned % 2 != 0 || !std::isfinite(gain) || T < 0 || T > kMaxRows)
+        return BD_ERR_SHAPE;
+    bd::RotaryArgs a{};
+    for (int i = 0; i < count; ++i) {
+        const bd_rotary_rows& r = rows[i];
+        if (T > 0 && (!r.x || !r.out)) return BD_ERR_NULL;
+        if (r.heads < 1 || r.heads > 65535) return BD_ERR_SHAPE;
+        bd_status st = check_strides(r.x_strides, x_type);
+        if (st != BD_OK || (st = check_strides(r.out_strides, out_type)) != BD_OK) return st;
+        if (!aligned(r.x, 16) || !aligned(r.out, 16)) return BD_ERR_ALIGN;
+        a.x[i] = r.x, a.out[i] = r.out, a.heads[i] = r.heads;
+        a.xs[i] = {r.x_strides[0], r.x_strides[1]};
+        a.os[i] = {r.out_strides[0], r.out_strides[1]};
+    }
+    if (!aligned(positions, 4) || !aligned(steps, 8)) return BD_ERR_ALIGN;
+    if (T == 0) return BD_OK;
+    const bd_status st = bd::check_current_device(nullptr);
+    if (st != BD_OK) return st;
+    a.positions = positions, a.steps = steps, a.gain = gain, a.dim = head_dim, a.turned = turned, a.T = T;
+    return finish(bd::launch_rotary(a, x_type == BD_FP32, out_type == BD_FP32, interleaved != 0,
+                                    static_cast<hipStream_t>(stream)));
+}
+
 bd_status bd_kv_write(const bd_kv* kv, const void* k, const int64_t* k_strides, const void* v,
                       const int64_t* v_strides, int32_t type, const int32_t* slots, int64_t T, void* stream) {
     bd_status st = check_kv(kv);
@@ -124,7 +154,7 @@ bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_
     bd_status st = check_kv(kv);
     if (st != BD_OK) return st;
     if (!q_strides || (B > 0 && (!q || !page_table || !lengths || !out))) return BD_ERR_NULL;
-    if (!in_type(q_type)) return BD_ERR_MODE;
+    if (!in_type(q_type) || kv->type == BD_E2M1) return BD_ERR_MODE;
     if (B < 0 || table_stride < 0 || !(std::fabs(scale) <= kMaxScale) ||
         !attend_shape(B > 0 ? B : 1, num_q_heads, kv->num_heads, kv->head_dim, kv->page_size, max_pages))
         return BD_ERR_SHAPE;

@@ -31,10 +31,39 @@ struct NormArgs {
 // x_fp32; residual: 0 none, 1 bf16, 2 fp32
 hipError_t launch_norm(const NormArgs& a, bool x_fp32, int residual, bool e4m3, hipStream_t stream);
 
-// kv.hip
 struct Strides2 {
     int64_t token, head;
 };
+
+// n / d for 0 <= n < 2^31 by a product: m = ceil(2^s / d) with s = 31 + ceil(log2 d)
+// is below 2^32 and too large by less than d / 2^s, which n cannot carry over.
+struct Div {
+    uint32_t d, m, shift;  // shift: s - 32
+    __host__ explicit Div(uint32_t by) : d(by) {
+        int up = 0;
+        while ((uint64_t(1) << up) < by) ++up;
+        m = (uint32_t)(((uint64_t(1) << (31 + up)) + by - 1) / by);
+        shift = up > 0 ? up - 1 : 0;
+        if (up == 0) m = 0;  // by 1: see by()
+    }
+    __device__ __forceinline__ uint32_t by(uint32_t n) const { return m ? __umulhi(n, m) >> shift : n; }
+};
+
+// rotary.hip
+struct RotaryArgs {
+    const void* x[2];
+    void* out[2];
+    Strides2 xs[2], os[2];
+    int32_t heads[2];  // the second 0 where there is one tensor
+    const int32_t* positions;
+    const uint64_t* steps;
+    float gain;
+    int32_t dim, turned;
+    int64_t T;
+};
+hipError_t launch_rotary(const RotaryArgs& a, bool x_fp32, bool out_fp32, bool interleaved, hipStream_t stream);
+
+// kv.hip
 hipError_t launch_kv_write(const bd_kv& kv, const void* k, Strides2 ks, const void* v, Strides2 vs, bool fp32,
                            const int32_t* slots, int64_t T, hipStream_t stream);
 hipError_t launch_kv_read(const bd_kv& kv, const int32_t* slots, int64_t T, uint16_t* k_out, uint16_t* v_out,
@@ -98,6 +127,42 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
 template <bool kHigh>
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t codes, float scale) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, kHigh));
+}
+
+// ---------------------------------------------------------------------------
+// e2m1 groups
+
+constexpr int kGroup4 = 32;        // values of a group
+constexpr int kMinScaleByte4 = 2;  // 2^-125: half of it, the least code but 0, is a normal bf16 number
+constexpr int kNanByte = 255;
+
+// The scale byte of a group whose largest magnitude has these bits (6 = 1.5 * 2^2).
+__device__ __forceinline__ int scale_byte4(uint32_t bits) {
+    if (bits >= 0x7f800000u) return kNanByte;
+    const int b = (int)((bits + 0x3fffffu) >> 23) - 2;
+    return b < kMinScaleByte4 ? kMinScaleByte4 : b;
+}
+// Eight values times inv (the inverse of their scale, by which they are exact
+// but below the least code) -> eight e2m1 codes (v_cvt_scalef32_pk_fp4_f32,
+// nearest even).
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float* f, float inv) {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[0] * inv, f[1] * inv, 1.0f, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[2] * inv, f[3] * inv, 1.0f, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[4] * inv, f[5] * inv, 1.0f, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, f[6] * inv, f[7] * inv, 1.0f, 3);
+    return r;
+}
+// Two e2m1 codes (byte kByte of a dword) times the power of two whose exponent
+// scale has -> packed bf16 pair, exactly (v_cvt_scalef32_pk_bf16_fp4; an
+// exponent of 255 gives NaN, one of 0 is 2^-127).
+template <int kByte>
+__device__ __forceinline__ uint32_t e2m1x2_to_bf16(uint32_t codes, float scale) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, kByte));
+}
+__device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t codes, float scale) {
+    return make_uint4(e2m1x2_to_bf16<0>(codes, scale), e2m1x2_to_bf16<1>(codes, scale),
+                      e2m1x2_to_bf16<2>(codes, scale), e2m1x2_to_bf16<3>(codes, scale));
 }
 
 // ---------------------------------------------------------------------------

@@ -7,10 +7,9 @@ device.  Every step of the computation runs in the library's HIP kernels;
 there is no fallback.
 
 A step of a served model runs, per layer: ``bd_rms_norm`` (the residual added,
-each token normed with its variant's gain), the q, k, v linears,
-``bd_kv_write``, ``bd_attend``, the output linear, ``bd_rms_norm`` again and
-the remaining linears.  Rotary embeddings, where a model has them, are the
-caller's, on q and k before the cache.
+each token normed with its variant's gain), the q, k, v linears, ``bd_rotary``
+where the model has rotary positions, ``bd_kv_write``, ``bd_attend``, the
+output linear, ``bd_rms_norm`` again and the remaining linears.
 """
 
 from __future__ import annotations
@@ -24,10 +23,10 @@ import torch
 
 from .bitdelta import _check, _workspace, library
 
-BD_BF16, BD_FP32, BD_E4M3 = 0, 1, 2
+BD_BF16, BD_FP32, BD_E4M3, BD_E2M1 = 0, 1, 2, 4
 _IN = {torch.bfloat16: BD_BF16, torch.float32: BD_FP32}
 _INT = torch.int32
-_HELD = {torch.bfloat16: BD_BF16, torch.float8_e4m3fn: BD_E4M3}
+_HELD = {torch.bfloat16: BD_BF16, torch.float8_e4m3fn: BD_E4M3, torch.float4_e2m1fn_x2: BD_E2M1}
 _declared = None
 # the current stream's handle and device as plain numbers: a call of a few microseconds on the GPU has no room for the
 # objects around them (torch.cuda.current_stream takes 1.9 us, this 0.1)
@@ -55,7 +54,8 @@ def declare(lib):
     lib.bd_kv_write.argtypes = [p, p, p, p, p, i32, p, i64, p]
     lib.bd_kv_read.argtypes = [p, p, i64, p, p, p]
     lib.bd_attend.argtypes = [p, p, i32, p, i32, p, i64, i64, p, i64, f, p, p, p, sz, p]
-    for n in ("rms_norm", "kv_write", "kv_read", "attend"):
+    lib.bd_rotary.argtypes = [p, i32, i32, i32, i32, i32, i32, p, p, f, i64, p]
+    for n in ("rms_norm", "rotary", "kv_write", "kv_read", "attend"):
         getattr(lib, "bd_" + n).restype = ctypes.c_int
     lib.bd_attend_workspace_bytes.argtypes = [i64] * 6
     lib.bd_attend_workspace_bytes.restype = sz
@@ -298,8 +298,10 @@ class bd_kv_cache:
     """A paged key-value cache over the caller's tensors.
 
     k, v: [num_pages, num_heads, page_size, head_dim], bf16 or float8_e4m3fn, alike in shape, dtype and strides,
-    head_dim contiguous (a [num_pages, page_size, num_heads, head_dim] buffer goes in as its transpose(1, 2)).
-    k_scales, v_scales: uint8 [num_pages, num_heads, page_size] for float8_e4m3fn, one scale byte per row.
+    head_dim contiguous (a [num_pages, page_size, num_heads, head_dim] buffer goes in as its transpose(1, 2)); for 4
+    bits float4_e2m1fn_x2 [num_pages, num_heads, page_size, head_dim / 2], two codes to a byte.
+    k_scales, v_scales: for float8_e4m3fn uint8 [num_pages, num_heads, page_size], one scale byte per row; for
+    float4_e2m1fn_x2 uint8 [num_pages, num_heads, head_dim / 32, page_size], one per 32 columns of a row.
     The tensors are kept by reference; the checks run once, here."""
 
     _bounds = _arrays = ()
@@ -311,12 +313,14 @@ class bd_kv_cache:
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride():
             raise ValueError("k and v must be alike: [num_pages, num_heads, page_size, head_dim], one dtype, "
                              "one layout")
-        pages, heads, page, dim = k.shape
+        pages, heads, page, row = k.shape
+        dim = 2 * row if kind == BD_E2M1 else row
         if pages < 1 or not 1 <= heads <= 65535 or page % 8 or not 8 <= page <= 4096:
             raise ValueError("need pages, 1..65535 heads and a page size that is a multiple of 8, 8..4096 (got %s)"
                              % (tuple(k.shape),))
-        if dim % 16 or not 16 <= dim <= 256:
-            raise ValueError("head_dim must be a multiple of 16, 16..256 (got %d)" % dim)
+        least = 32 if kind == BD_E2M1 else 16
+        if dim % least or not 16 <= dim <= 256:
+            raise ValueError("head_dim must be a multiple of %d, %d..256 (got %d)" % (least, least, dim))
         if pages * page > 2 ** 31 - 1:
             raise ValueError("more than 2^31 - 1 slots")
         stride = list(k.stride())
@@ -330,25 +334,26 @@ class bd_kv_cache:
             raise ValueError("k, v and their strides must be multiples of 16 bytes")
         # distinct rows must not overlap: each axis steps over all of the smaller ones
         steps = sorted((s, n) for s, n in zip(stride[:3], k.shape[:3]) if n > 1)
-        extent = dim
+        extent = row
         for s, n in steps:
             if s < extent:
                 raise ValueError("rows of k overlap (strides %s)" % (tuple(k.stride()),))
             extent = s * (n - 1) + extent
         self._span = extent * size
-        if kind == BD_E4M3:
+        if kind != BD_BF16:
+            held = (pages, heads, page) if kind == BD_E4M3 else (pages, heads, dim // 32, page)
             for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-                _plain(name, t, torch.uint8, (pages, heads, page))
+                _plain(name, t, torch.uint8, held)
                 if t.data_ptr() % 8:
                     raise ValueError("%s must be 8-byte aligned" % name)
         elif k_scales is not None or v_scales is not None:
             raise ValueError("a bf16 cache has no scales")
         # where the arrays are: each as _on_rows takes it, and the ends of their spans in rising order, those that meet
         # taken together
-        row, steps = dim * size, [(s * size, n) for s, n in reversed(steps)]
+        row, steps = row * size, [(s * size, n) for s, n in reversed(steps)]
         self._arrays = [(k.data_ptr(), steps, row), (v.data_ptr(), steps, row)]
         spans = [(at, at + self._span) for at, _, _ in self._arrays]
-        if kind == BD_E4M3:
+        if kind != BD_BF16:
             for t in (k_scales, v_scales):
                 self._arrays.append((t.data_ptr(), [], t.nbytes))
                 spans.append((t.data_ptr(), t.data_ptr() + t.nbytes))
@@ -359,7 +364,7 @@ class bd_kv_cache:
             else:
                 bounds += [lo, hi]
         self._bounds = bounds
-        if kind == BD_E4M3 and len(bounds) < 8:
+        if kind != BD_BF16 and len(bounds) < 8:
             if _overlap(k_scales, v_scales):
                 raise ValueError("k_scales overlaps v_scales")
             for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
@@ -390,11 +395,15 @@ class bd_kv_cache:
     def empty(cls, num_pages: int, num_heads: int, page_size: int, head_dim: int, dtype: torch.dtype = torch.bfloat16,
               device="cuda"):
         """A cache of its own memory, contents undefined."""
-        shape = (num_pages, num_heads, page_size, head_dim)
-        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
-        if dtype != torch.float8_e4m3fn:
+        lead, row, held = (num_pages, num_heads, page_size), head_dim, (num_pages, num_heads, page_size)
+        if dtype == torch.float4_e2m1fn_x2:
+            if head_dim % 32:
+                raise ValueError("head_dim must be a multiple of 32 (got %d)" % head_dim)
+            row, held = head_dim // 2, (num_pages, num_heads, head_dim // 32, page_size)
+        k, v = (torch.empty((*lead, row), dtype=dtype, device=device) for _ in range(2))
+        if dtype not in (torch.float8_e4m3fn, torch.float4_e2m1fn_x2):
             return cls(k, v)
-        return cls(k, v, *(torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
+        return cls(k, v, *(torch.empty(held, dtype=torch.uint8, device=device) for _ in range(2)))
 
 
 def _rows(name, t, kv_heads, dim):
