@@ -246,6 +246,39 @@ bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_
                     const int32_t* lengths, int64_t B, float scale, uint16_t* out, float* lse,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* How the scores of an attention are formed, in place of scale * q . k alone:
+ *
+ *   s = scale * q . k
+ *   s = cap * tanh(s / cap)               where cap is not 0
+ *   s = s - slopes[i] * |p - j|           where slopes is not NULL, for query head i
+ *                                         at position p and the key of token j
+ *
+ * and which tokens are attended to: first <= j < last.
+ *
+ *   cap      0, or 2^-60 .. 2^60: no score is larger than it in magnitude.
+ *   slopes   [num_q_heads] fp32; finite.
+ *   first    int32, one number for each query token (each sequence of
+ *            bd_attend_scores): tokens before it are not attended to, and
+ *            pages that hold only such are not looked up.  0 or less, or NULL:
+ *            from the start.  What lies in masked places does not matter, NaN
+ *            included.  A query token that nothing is left for gets zeros, and
+ *            -infinity in lse.
+ *   last     int32, one number for each query token of bd_attend_prompt; NULL
+ *            for bd_attend_scores. */
+typedef struct bd_scores {
+    float cap;
+    const float* slopes;
+    const int32_t* first;
+    const int32_t* last;
+} bd_scores;
+
+/* bd_attend with formed scores (NULL: as bd_attend); the new token's position
+ * is lengths[b] - 1, the same workspace serves.  BD_ERR_MODE for scores->last. */
+bd_status bd_attend_scores(const bd_kv* kv, const void* q, int32_t q_type, const int64_t* q_strides,
+                           int32_t num_q_heads, const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                           const int32_t* lengths, int64_t B, float scale, const bd_scores* scores, uint16_t* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

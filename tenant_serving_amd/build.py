@@ -17,7 +17,9 @@ LIBRARY = os.path.join(PKG, "libbitdelta.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["api.cpp", "cache.cpp", "compress.hip", "decode.hip", "shot.hip", "slice.hip", "gemv.hip", "quad.hip", "band.hip", "skinny.hip", "rowstream.hip", "prefill.hip",
-           "grouped.hip", "gdec.hip", "step_api.cpp", "norm.hip", "rotary.hip", "kv.hip", "attend.hip"]
+           "grouped.hip", "gdec.hip", "step_api.cpp", "norm.hip", "rotary.hip", "kv.hip", "attend.hip",
+           "attend_bf16.hip", "attend_e4m3.hip", "attend_e2m1.hip", "attend_bf16_formed.hip", "attend_e4m3_formed.hip",
+           "attend_e2m1_formed.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

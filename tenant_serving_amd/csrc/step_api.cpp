@@ -48,6 +48,9 @@ bd_status check_strides(const int64_t* s, int32_t type) {
     return BD_OK;
 }
 
+// A cap of scores: none, or one whose inverse and square are ordinary numbers.
+bool cap_ok(float cap) { return cap == 0.0f || (cap >= 1.0f / kMaxScale && cap <= kMaxScale); }
+
 // Sizes of an attention call that its kernels can index.
 bool attend_shape(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages) {
     if (B < 1 || B > kMaxRows || H < 1 || H > 65535 || Hq < H || Hq > 65535 || Hq % H != 0) return false;
@@ -147,17 +150,22 @@ size_t bd_attend_workspace_bytes(int64_t B, int64_t num_q_heads, int64_t num_hea
     return bd::attend_workspace_bytes(B, num_q_heads, num_heads, head_dim, page_size, max_pages);
 }
 
-bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_t* q_strides,
+bd_status bd_attend_scores(const bd_kv* kv, const void* q, int32_t q_type, const int64_t* q_strides,
                     int32_t num_q_heads, const int32_t* page_table, int64_t table_stride, int64_t max_pages,
-                    const int32_t* lengths, int64_t B, float scale, uint16_t* out, float* lse,
+                    const int32_t* lengths, int64_t B, float scale, const bd_scores* scores,
+                    uint16_t* out, float* lse,
                     void* workspace, size_t workspace_bytes, void* stream) {
     bd_status st = check_kv(kv);
     if (st != BD_OK) return st;
     if (!q_strides || (B > 0 && (!q || !page_table || !lengths || !out))) return BD_ERR_NULL;
-    if (!in_type(q_type) || kv->type == BD_E2M1) return BD_ERR_MODE;
+    if (!in_type(q_type)) return BD_ERR_MODE;
     if (B < 0 || table_stride < 0 || !(std::fabs(scale) <= kMaxScale) ||
         !attend_shape(B > 0 ? B : 1, num_q_heads, kv->num_heads, kv->head_dim, kv->page_size, max_pages))
         return BD_ERR_SHAPE;
+    const bd_scores form = scores ? *scores : bd_scores{};
+    if (form.last) return BD_ERR_MODE;
+    if (!cap_ok(form.cap)) return BD_ERR_SHAPE;
+    if (!aligned(form.slopes, 4) || !aligned(form.first, 4)) return BD_ERR_ALIGN;
     if ((st = check_strides(q_strides, q_type)) != BD_OK) return st;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(lse, 4))
         return BD_ERR_ALIGN;
@@ -168,8 +176,16 @@ bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_
     if ((st = bd::check_current_device(nullptr)) != BD_OK) return st;
     const bd::AttendArgs a{*kv, q, {q_strides[0], q_strides[1]}, page_table, lengths, out, lse,
                            need > 0 ? static_cast<float*>(workspace) : nullptr, table_stride, (int32_t)max_pages, (int32_t)B,
-                           num_q_heads, scale};
+                           num_q_heads, scale, form.cap, form.slopes, form.first};
     return finish(bd::launch_attend(a, q_type == BD_FP32, static_cast<hipStream_t>(stream)));
+}
+
+bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_t* q_strides,
+                    int32_t num_q_heads, const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                    const int32_t* lengths, int64_t B, float scale, uint16_t* out, float* lse,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    return bd_attend_scores(kv, q, q_type, q_strides, num_q_heads, page_table, table_stride, max_pages, lengths, B,
+                            scale, nullptr, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -84,8 +84,44 @@ struct AttendArgs {
     int64_t table_stride;
     int32_t max_pages, B, Hq;
     float scale;
+    float cap;             // 0: none
+    const float* slopes;   // may be null
+    const int32_t* first;  // may be null
 };
 hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream);
+
+// Scores capped: cap tanh(x / cap).  tanh y = 1 - 2 / (1 + e^(2 y)) loses what is
+// small against 1, so where all of the wave's |y| are below 1/4 its Taylor series
+// up to y^9 takes their place (the next term is below 2^-26 of the result), which
+// needs neither exponential nor reciprocal and is the usual case: scores are small
+// against a cap.  Where some are larger, each lane takes what suits it.
+template <int kN>
+__device__ __forceinline__ void cap_scores(float* x, float cap) {
+    const float inv = 1.0f / cap;
+    float big = 0.0f;
+    float y[kN], small[kN];
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        y[j] = x[j] * inv;
+        big = fmaxf(big, __builtin_fabsf(y[j]));
+        const float q = y[j] * y[j];
+        float a = __builtin_fmaf(q, 2.1869489e-02f, -5.3968254e-02f);
+        a = __builtin_fmaf(a, q, 1.3333333e-01f);
+        a = __builtin_fmaf(a, q, -3.3333333e-01f);
+        small[j] = __builtin_fmaf(a * q, y[j], y[j]);
+    }
+    if (__ballot(big > 0.25f)) {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+            const float e = __builtin_amdgcn_exp2f(y[j] * 2.8853900817779268f);  // 2 log2(e)
+            const float t = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + e), 1.0f);
+            x[j] = cap * (__builtin_fabsf(y[j]) <= 0.25f ? small[j] : t);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kN; ++j) x[j] = cap * small[j];
+    }
+}
 
 // ---------------------------------------------------------------------------
 // e4m3 groups

@@ -43,6 +43,11 @@ class _KV(ctypes.Structure):
                 ("token_stride", ctypes.c_int64)]
 
 
+class _Scores(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("first", ctypes.c_void_p),
+                ("last", ctypes.c_void_p)]
+
+
 _Pair = ctypes.c_int64 * 2
 _NO_END = 1 << 64
 _SIZE = (2, 4, 1)  # bytes of a value, by its type
@@ -54,8 +59,9 @@ def declare(lib):
     lib.bd_kv_write.argtypes = [p, p, p, p, p, i32, p, i64, p]
     lib.bd_kv_read.argtypes = [p, p, i64, p, p, p]
     lib.bd_attend.argtypes = [p, p, i32, p, i32, p, i64, i64, p, i64, f, p, p, p, sz, p]
+    lib.bd_attend_scores.argtypes = [p, p, i32, p, i32, p, i64, i64, p, i64, f, p, p, p, p, sz, p]
     lib.bd_rotary.argtypes = [p, i32, i32, i32, i32, i32, i32, p, p, f, i64, p]
-    for n in ("rms_norm", "rotary", "kv_write", "kv_read", "attend"):
+    for n in ("rms_norm", "rotary", "kv_write", "kv_read", "attend", "attend_scores"):
         getattr(lib, "bd_" + n).restype = ctypes.c_int
     lib.bd_attend_workspace_bytes.argtypes = [i64] * 6
     lib.bd_attend_workspace_bytes.restype = sz
@@ -530,7 +536,7 @@ def bd_kv_read(kv: bd_kv_cache, slots: torch.Tensor, out: tuple[torch.Tensor, to
     return k, v
 
 
-def _attend_to(kv, q0, q1, page_table, lengths, out, lse, B, heads, dev):
+def _attend_to(kv, q0, q1, page_table, lengths, out, lse, B, heads, dev, more=()):
     """Whether out and lse, as far as given, are tensors that an attention may write to, as they nearly always are: of
     the right kind, apart from each other and from all that it reads (queries from q0 up to q1)."""
     mine = []
@@ -543,7 +549,7 @@ def _attend_to(kv, q0, q1, page_table, lengths, out, lse, B, heads, dev):
             return False
         mine.append(lse)
     used = [(q0, q1)]
-    for t in (page_table, lengths):
+    for t in (page_table, lengths, *more):
         used.append((t.data_ptr(), t.data_ptr() + t.nbytes))
     for t in mine:
         lo = t.data_ptr()
@@ -557,7 +563,17 @@ def _attend_to(kv, q0, q1, page_table, lengths, out, lse, B, heads, dev):
     return True
 
 
-def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
+def _cap(cap):
+    """A cap of scores as the library takes it."""
+    if cap is None:
+        return 0.0
+    cap = float(cap)
+    if not 2.0 ** -60 <= cap <= 2.0 ** 60:
+        raise ValueError("cap must be 2^-60 .. 2^60 (got %r)" % cap)
+    return cap
+
+
+def _refuse_attend(q, kv, page_table, lengths, out, lse, heads, slopes=None, first=None):
     """The checks of an attention's tensors, in full; raises or returns."""
     B = q.shape[0]
     if heads < 1 or heads > 65535 or heads % kv.num_heads:
@@ -573,11 +589,16 @@ def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
     if page_table.shape[1] * kv.page_size > 1 << 24:
         raise ValueError("page_table holds more than 2^24 tokens per sequence")
     _plain("lengths", lengths, torch.int32, (B,))
+    if slopes is not None:
+        _plain("slopes", slopes, torch.float32, (heads,))
+    if first is not None:
+        _plain("first", first, torch.int32, (B,))
     if out is not None:
         _plain("out", out, torch.bfloat16, (B, heads, kv.head_dim))
     if lse is not None:
         _plain("lse", lse, torch.float32, (B, heads))
-    every = (("q", q), ("page_table", page_table), ("lengths", lengths), ("out", out), ("lse", lse))
+    every = (("q", q), ("page_table", page_table), ("lengths", lengths), ("slopes", slopes), ("first", first),
+             ("out", out), ("lse", lse))
     given = [(name, t) for name, t in every if t is not None and t.numel()]
     for name, t in given:
         for other, o in given:
@@ -588,7 +609,8 @@ def _refuse_attend(q, kv, page_table, lengths, out, lse, heads):
 
 
 def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, lengths: torch.Tensor,
-              scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None):
+              scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+              cap: float | None = None, slopes: torch.Tensor | None = None, first: torch.Tensor | None = None):
     """softmax(scale · q kᵀ) v of one new token per sequence over the cache; bf16 [B, num_q_heads, head_dim].
 
     q [B, num_q_heads, head_dim] is bf16 or fp32 (any token and head strides); num_q_heads is a multiple of the cache's
@@ -597,38 +619,53 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     head_dim^-0.5.  lse, if given, is an fp32 [B, num_q_heads] tensor that receives the log of the softmax's sum.  out
     and lse lie apart from each other and from all that is read.  Where the table has room for few tokens (some
     hundreds, whatever the lengths) nothing is split and no second kernel is launched: for short sequences a table no
-    wider than needed is faster."""
+    wider than needed is faster.
+
+    cap makes cap · tanh(score / cap) of the scores, slopes (fp32 [num_q_heads]) takes slopes · distance off them after
+    that, and first (int32 [B]) leaves out the tokens before it: a window of w tokens has first = lengths − w.  Pages
+    that hold only tokens before first need not be in the table any more."""
     _cache(kv)
     kind, qs, B, heads, reach = _rows("q", q, None, kv.head_dim)
     dev = kv._dev
     scale = kv.head_dim ** -0.5 if scale is None else float(scale)
     if not abs(scale) <= 2.0 ** 60:
         raise ValueError("scale must be at most 2^60 (got %r)" % scale)
+    formed, limit = cap is not None or slopes is not None or first is not None, _cap(cap)
     q0 = q.data_ptr()
     if not (type(page_table) is torch.Tensor and page_table.dim() == 2
             and page_table.dtype is _INT and page_table.shape[0] == B and page_table.is_contiguous()
             and 1 <= page_table.shape[1] <= (1 << 24) // kv.page_size and page_table.get_device() == dev
             and _index("lengths", lengths, B, dev) and q.get_device() == dev and 1 <= heads <= 65535
             and heads % kv.num_heads == 0
+            and (not formed or (slopes is None or _given(slopes, torch.float32, (heads,), dev))
+                 and (first is None or _index("first", first, B, dev)))
             and (out is None and lse is None
-                 or _attend_to(kv, q0, q0 + reach * _SIZE[kind], page_table, lengths, out, lse, B, heads, dev))):
-        _refuse_attend(q, kv, page_table, lengths, out, lse, heads)
+                 or _attend_to(kv, q0, q0 + reach * _SIZE[kind], page_table, lengths, out, lse, B, heads, dev,
+                               [t for t in (slopes, first) if t is not None]))):
+        _refuse_attend(q, kv, page_table, lengths, out, lse, heads, slopes, first)
     if _current_device() != dev:
         with torch.cuda.device(dev):
-            return bd_attend(q, kv, page_table, lengths, scale, out, lse)
+            return bd_attend(q, kv, page_table, lengths, scale, out, lse, cap, slopes, first)
     lib = _declared or _library()
     pages = page_table.shape[1]
     nbytes = _attend_bytes(B, heads, kv.num_heads, kv.head_dim, kv.page_size, pages)
+    scores = None
+    if formed:
+        scores = ctypes.byref(_Scores(limit, _at(slopes), _at(first), None))
     if out is None:
         if kind == BD_BF16 and q.is_contiguous():
             out = torch.empty_like(q)
         else:
             out = torch.empty((B, heads, kv.head_dim), dtype=torch.bfloat16, device=kv.device)
     ws = _workspace(nbytes, kv.device)
-    st = lib.bd_attend(kv._ref, q0, kind, qs, heads, page_table.data_ptr(),
-                       page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, out.data_ptr(),
-                       lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None, nbytes,
-                       _stream_of(dev))
+    args = (out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None,
+            nbytes, _stream_of(dev))
+    if formed:
+        st = lib.bd_attend_scores(kv._ref, q0, kind, qs, heads, page_table.data_ptr(),
+                                  page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, scores, *args)
+    else:
+        st = lib.bd_attend(kv._ref, q0, kind, qs, heads, page_table.data_ptr(),
+                           page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, *args)
     if st:
         _check(lib, "bd_attend", st)
     return out

@@ -32,17 +32,16 @@ def quantise4(rows):
     """[..., dim] float64 -> (codes 0..15 uint8 [..., dim], scale bytes [..., dim / 32]); codes of a group that holds
     something not finite are 0."""
     flat = rows.reshape(-1, 32)
-    codes, bytes_ = np.zeros(flat.shape, np.uint8), np.empty(flat.shape[0], np.uint8)
+    fine = np.isfinite(flat).all(1)
+    y = np.abs(np.where(fine[:, None], flat, 0.0))
+    m, e = np.frexp(y.max(1))                       # a = m 2^e, m from 1/2: 6 2^(e - 3) is three quarters of 2^e
+    e = np.maximum(np.where(m > 0, e - 3 + (m > 0.75), -125), -125)
+    y = y / 2.0 ** e[:, None].astype(np.float64)
     mid = (E2M1[1:] + E2M1[:-1]) / 2
-    for i, r in enumerate(flat):
-        if not np.isfinite(r).all():
-            bytes_[i] = 255
-            continue
-        bytes_[i] = scale_byte4(np.abs(r).max())
-        y = np.abs(r) / 2.0 ** (int(bytes_[i]) - 127)
-        lo, hi = np.searchsorted(mid, y, side="left"), np.searchsorted(mid, y, side="right")
-        code = np.where(lo == hi, lo, np.where(lo % 2 == 0, lo, hi))
-        codes[i] = code | np.signbit(r) * 8
+    lo, hi = np.searchsorted(mid, y, side="left"), np.searchsorted(mid, y, side="right")
+    codes = np.where(lo == hi, lo, np.where(lo % 2 == 0, lo, hi)) | np.signbit(flat) * 8
+    codes = np.where(fine[:, None], codes, 0).astype(np.uint8)
+    bytes_ = np.where(fine, e + 127, 255).astype(np.uint8)
     return codes.reshape(rows.shape), bytes_.reshape(rows.shape[:-1] + (rows.shape[-1] // 32,))
 
 
@@ -61,3 +60,46 @@ def pack4(codes):
 
 def unpack4(packed):
     return np.stack((packed & 15, packed >> 4), -1).reshape(packed.shape[:-1] + (packed.shape[-1] * 2,))
+
+
+def scores(q, k, scale, cap=0.0, slopes=None, position=0):
+    """Formed scores [Hq, n] of queries [Hq, D] and their heads' keys [Hq, n, D], and the largest sum of |q k| scale."""
+    with np.errstate(all="ignore"):
+        prod = q[:, None, :] * k
+        s = prod.sum(2) * scale
+        a = np.abs(prod * scale).sum(2)
+        if cap:
+            s = cap * np.tanh(s / cap)
+        if slopes is not None:
+            s = s - slopes[:, None] * np.abs(position - np.arange(k.shape[1]))[None, :]
+    return s, a[np.isfinite(a)].max(initial=0.0)
+
+
+def attend(q, k_rows, v_rows, scale, cap=0.0, slopes=None, first=0, last=None, position=None):
+    """One query token: q [Hq, D], rows [n, H, D] (float64) -> (out [Hq, D], lse [Hq], largest sum of |q k| scale over
+    the tokens seen); tokens outside [first, last) are as if they were not there."""
+    hq, d = q.shape
+    n, h, _ = k_rows.shape
+    last = n if last is None else min(last, n)
+    first = max(first, 0)
+    position = n - 1 if position is None else position
+    if first >= last:
+        return np.zeros((hq, d)), np.full(hq, -np.inf), 0.0
+    pick = np.arange(hq) // (hq // h)
+    seen = slice(first, last)
+    k = k_rows[seen][:, pick].transpose(1, 0, 2)
+    v = v_rows[seen][:, pick].transpose(1, 0, 2)
+    s, reach = scores(q, k, scale, cap, slopes, position - first)
+    with np.errstate(all="ignore"):
+        top = s.max(1, keepdims=True)
+        p = np.exp(s - top)
+        out = (p[:, None, :] @ v)[:, 0] / p.sum(1)[:, None] if np.isfinite(v).all() else \
+            (p[:, :, None] * v).sum(1) / p.sum(1)[:, None]
+        return out, top[:, 0] + np.log(p.sum(1)), reach
+
+
+def score_error(dim, reach, cap=0.0, slope_reach=0.0):
+    """How far a score is off at most: dim products and sums and a few more, the capping's 2^-19 of what it caps (tanh is
+    off by 2^-21 where its argument is past a quarter, and by less of its result below), the distance's product and sum."""
+    u = 2.0 ** -24
+    return (dim + 8) * u * reach + (2.0 ** -19 * min(reach, cap) if cap else 0.0) + 3 * u * slope_reach

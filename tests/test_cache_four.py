@@ -43,14 +43,13 @@ class Cache:
         self.scales = [t.cpu().numpy().copy() for t in scales]
 
     def expect(self, k, v, slots):
-        for t, s in enumerate(slots.tolist()):
-            if not 0 <= s < self.slots:
-                continue
-            p, at = divmod(s, self.page)
-            for i, x in enumerate((k, v)):
-                codes, bytes_ = ref.quantise4(x[t].double().numpy())
-                self.rows[i][p, :, at] = ref.pack4(codes)
-                self.scales[i][p, :, :, at] = bytes_
+        for i, x in enumerate((k, v)):
+            codes, bytes_ = ref.quantise4(x.double().numpy())
+            packed = ref.pack4(codes)
+            for t, s in enumerate(slots.tolist()):
+                if 0 <= s < self.slots:
+                    p, at = divmod(s, self.page)
+                    self.rows[i][p, :, at], self.scales[i][p, :, :, at] = packed[t], bytes_[t]
 
     def check(self):
         for i, (t, s) in enumerate(((self.kv.k, self.kv.k_scales), (self.kv.v, self.kv.v_scales))):
@@ -81,6 +80,11 @@ def test_reference():
     assert byte.tolist() == [[127]]
     assert codes[0, :16].tolist() == [7, 6, 7, 6, 4, 4, 2, 2, 0, 1, 15, 14, 8, 10, 0, 6]
     assert np.array_equal(ref.unpack4(ref.pack4(codes)), codes)
+    # scale bytes by halving and doubling
+    x = np.zeros((500, 32))
+    x[:, 7] = np.random.default_rng(1).standard_normal(500).astype(np.float32) * 2.0 ** np.linspace(-140, 127, 500)
+    x[:8, 7] = [6, 12, 3, 6 * 2.0 ** -125, 6.1 * 2.0 ** -125, 2.0 ** -149, 0, 1.5 * 2.0 ** 100]
+    assert ref.quantise4(x)[1][:, 0].tolist() == [ref.scale_byte4(a) for a in np.abs(x).max(1)]
     assert ref.scale_byte4(0.0) == 2 and ref.scale_byte4(6.1) == 128 and ref.scale_byte4(3.0) == 126
     assert ref.scale_byte4(float(np.float32(3.4028234e38))) == 253
 
