@@ -279,6 +279,56 @@ bd_status bd_attend_scores(const bd_kv* kv, const void* q, int32_t q_type, const
                            const int32_t* lengths, int64_t B, float scale, const bd_scores* scores, uint16_t* out,
                            float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention of several new tokens per sequence over the cache: a whole prompt,
+ * a chunk of one behind what the cache holds of it, or a few proposed tokens.
+ * Their rows have been written to the cache by then.
+ *
+ *   out[t, i] = sum_j softmax_j(s_j) v_j,   first[t] <= j < last[t]
+ *
+ * with s_j the (formed) score of query row (t, i) and key j of its sequence.
+ *
+ *   q           T tokens of num_q_heads rows of head_dim bf16 values, 16-byte
+ *               aligned, strides as in bd_attend.
+ *   starts      [B + 1] int32, rising: sequence b's new tokens are the query
+ *               tokens starts[b] .. starts[b + 1] - 1, and the last ones of
+ *               its lengths[b] tokens: query token t stands at position
+ *               p = lengths[b] - starts[b + 1] + t.  Numbers outside 0 .. T
+ *               count as 0 and T, a falling one as no tokens.  Rows of out and
+ *               lse of tokens outside [starts[0], starts[B]) stay as they
+ *               were.  What falls is the caller's mistake: tokens that several
+ *               sequences have then get the result of any, or none.
+ *   lengths     [B] int32: tokens in the cache, the new ones among them.  0 or
+ *               less: zeros, and -infinity in lse.  Over max_pages * page_size:
+ *               rows of NaN.
+ *   scores      NULL: scale * q . k.  first: default the start; last: default
+ *               p + 1, which is the causal mask; with both a row sees any one
+ *               range of its sequence: a window (first = p - w + 1), its
+ *               document (first = the document's start), a prefix that sees
+ *               itself in both directions (last = the prefix's end).  Numbers
+ *               past the sequence's ends count as these.  A row that sees
+ *               nothing gets zeros, and -infinity in lse.
+ *   page_table, max_pages, scale, out [T, num_q_heads, head_dim], lse
+ *   [T, num_q_heads], workspace: as in bd_attend, with
+ *   bd_attend_prompt_workspace_bytes(...) bytes.  Only pages that hold tokens
+ *   that some row sees, or that lie between two such, are looked up; a page
+ *   outside [0, num_pages) makes NaN of the rows that see it.
+ * T * num_q_heads <= 2^29, B * num_heads <= 2^22.  T == 0 or B == 0 is a no-op.
+ * What a row does not see does not matter to it, NaN included.
+ * Scores, sums and outputs are fp32 until they are stored; the softmax weights
+ * are rounded to bf16 once, for the product with the values.  Fixed order: the
+ * same inputs and batch give bitwise the same outputs.
+ * Returns BD_OK, BD_ERR_NULL, _SHAPE, _ALIGN, _MODE, _WORKSPACE, _HIP,
+ * _DEVICE.
+ * ------------------------------------------------------------------------- */
+size_t bd_attend_prompt_workspace_bytes(int64_t T, int64_t B, int64_t num_q_heads, int64_t num_heads,
+                                        int64_t head_dim, int64_t page_size, int64_t max_pages);
+bd_status bd_attend_prompt(const bd_kv* kv, const uint16_t* q, const int64_t* q_strides, int32_t num_q_heads,
+                           int64_t T, const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                           const int32_t* lengths, const int32_t* starts, int64_t B, float scale,
+                           const bd_scores* scores, uint16_t* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,7 @@ from .bitdelta import (  # noqa: F401
     library,
 )
 from .cache import Busy, bd_cache  # noqa: F401
+from .prompt import bd_attend_prompt  # noqa: F401
 from .rotary import bd_rotary, bd_rotary_angles  # noqa: F401
 from .step import (  # noqa: F401
     bd_attend,

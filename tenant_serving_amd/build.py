@@ -19,7 +19,8 @@ INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 SOURCES = ["api.cpp", "cache.cpp", "compress.hip", "decode.hip", "shot.hip", "slice.hip", "gemv.hip", "quad.hip", "band.hip", "skinny.hip", "rowstream.hip", "prefill.hip",
            "grouped.hip", "gdec.hip", "step_api.cpp", "norm.hip", "rotary.hip", "kv.hip", "attend.hip",
            "attend_bf16.hip", "attend_e4m3.hip", "attend_e2m1.hip", "attend_bf16_formed.hip", "attend_e4m3_formed.hip",
-           "attend_e2m1_formed.hip"]
+           "attend_e2m1_formed.hip", "prompt.hip", "prompt_bf16.hip", "prompt_e4m3.hip", "prompt_e2m1.hip",
+           "prompt_bf16_formed.hip", "prompt_e4m3_formed.hip", "prompt_e2m1_formed.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -61,6 +61,14 @@ bool attend_shape(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size
     return rows <= int64_t(1) << 23 && (units + 4) * rows <= int64_t(1) << 30;
 }
 
+// The same of a prompt's: rows and workgroups below 2^31 and 2^23.
+bool prompt_shape(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, int64_t max_pages) {
+    if (T < 1 || B < 1 || H < 1 || H > 65535 || Hq < H || Hq > 65535 || Hq % H != 0) return false;
+    if (D < 16 || D > 256 || D % 16 != 0 || page_size < 8 || page_size > 4096 || page_size % 8 != 0) return false;
+    if (max_pages < 1 || max_pages > bd::kAttendMaxTokens / page_size) return false;
+    return T <= (int64_t(1) << 29) / Hq && B <= (int64_t(1) << 22) / H;
+}
+
 }  // namespace
 
 extern "C" {
@@ -186,6 +194,43 @@ bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_
                     void* workspace, size_t workspace_bytes, void* stream) {
     return bd_attend_scores(kv, q, q_type, q_strides, num_q_heads, page_table, table_stride, max_pages, lengths, B,
                             scale, nullptr, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t bd_attend_prompt_workspace_bytes(int64_t T, int64_t B, int64_t num_q_heads, int64_t num_heads,
+                                        int64_t head_dim, int64_t page_size, int64_t max_pages) {
+    if (!prompt_shape(T, B, num_q_heads, num_heads, head_dim, page_size, max_pages)) return 0;
+    return bd::prompt_workspace_bytes(T, B, num_q_heads, num_heads, head_dim, page_size * max_pages);
+}
+
+bd_status bd_attend_prompt(const bd_kv* kv, const uint16_t* q, const int64_t* q_strides, int32_t num_q_heads,
+                           int64_t T, const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+                           const int32_t* lengths, const int32_t* starts, int64_t B, float scale,
+                           const bd_scores* scores, uint16_t* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    bd_status st = check_kv(kv);
+    if (st != BD_OK) return st;
+    const bool some = B > 0 && T > 0;
+    if (!q_strides || (some && (!q || !page_table || !lengths || !starts || !out))) return BD_ERR_NULL;
+    const bd_scores form = scores ? *scores : bd_scores{};
+    if (B < 0 || T < 0 || table_stride < 0 || !(std::fabs(scale) <= kMaxScale) || !cap_ok(form.cap) ||
+        !prompt_shape(T > 0 ? T : 1, B > 0 ? B : 1, num_q_heads, kv->num_heads, kv->head_dim, kv->page_size, max_pages))
+        return BD_ERR_SHAPE;
+    if ((st = check_strides(q_strides, BD_BF16)) != BD_OK) return st;
+    for (const void* x : {static_cast<const void*>(page_table), static_cast<const void*>(lengths),
+                          static_cast<const void*>(starts), static_cast<const void*>(lse),
+                          static_cast<const void*>(form.slopes), static_cast<const void*>(form.first),
+                          static_cast<const void*>(form.last)})
+        if (!aligned(x, 4)) return BD_ERR_ALIGN;
+    if (!aligned(q, 16) || !aligned(out, 16)) return BD_ERR_ALIGN;
+    if (!some) return BD_OK;
+    const size_t need = bd::prompt_workspace_bytes(T, B, num_q_heads, kv->num_heads, kv->head_dim,
+                                                   kv->page_size * max_pages);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return BD_ERR_WORKSPACE;
+    if ((st = bd::check_current_device(nullptr)) != BD_OK) return st;
+    const bd::PromptArgs a{*kv, q, {q_strides[0], q_strides[1]}, page_table, lengths, starts, out, lse,
+                           need > 0 ? static_cast<float*>(workspace) : nullptr, table_stride, (int32_t)max_pages,
+                           (int32_t)B, (int32_t)T, num_q_heads, scale, form.cap, form.slopes, form.first, form.last};
+    return finish(bd::launch_prompt(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

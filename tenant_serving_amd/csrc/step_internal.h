@@ -90,6 +90,28 @@ struct AttendArgs {
 };
 hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream);
 
+// prompt.hip
+size_t prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t capacity);
+struct PromptArgs {
+    bd_kv kv;
+    const uint16_t* q;
+    Strides2 qs;
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* starts;
+    uint16_t* out;
+    float* lse;   // may be null
+    float* part;  // workspace, may be null where nothing is split
+    int64_t table_stride;
+    int32_t max_pages, B, T, Hq;
+    float scale;
+    float cap;             // 0: none
+    const float* slopes;   // may be null
+    const int32_t* first;  // may be null
+    const int32_t* last;   // may be null
+};
+hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream);
+
 // Scores capped: cap tanh(x / cap).  tanh y = 1 - 2 / (1 + e^(2 y)) loses what is
 // small against 1, so where all of the wave's |y| are below 1/4 its Taylor series
 // up to y^9 takes their place (the next term is below 2^-26 of the result), which

@@ -60,11 +60,14 @@ def declare(lib):
     lib.bd_kv_read.argtypes = [p, p, i64, p, p, p]
     lib.bd_attend.argtypes = [p, p, i32, p, i32, p, i64, i64, p, i64, f, p, p, p, sz, p]
     lib.bd_attend_scores.argtypes = [p, p, i32, p, i32, p, i64, i64, p, i64, f, p, p, p, p, sz, p]
+    lib.bd_attend_prompt.argtypes = [p, p, p, i32, i64, p, i64, i64, p, p, i64, f, p, p, p, p, sz, p]
     lib.bd_rotary.argtypes = [p, i32, i32, i32, i32, i32, i32, p, p, f, i64, p]
-    for n in ("rms_norm", "rotary", "kv_write", "kv_read", "attend", "attend_scores"):
+    for n in ("rms_norm", "rotary", "kv_write", "kv_read", "attend", "attend_scores", "attend_prompt"):
         getattr(lib, "bd_" + n).restype = ctypes.c_int
     lib.bd_attend_workspace_bytes.argtypes = [i64] * 6
     lib.bd_attend_workspace_bytes.restype = sz
+    lib.bd_attend_prompt_workspace_bytes.argtypes = [i64] * 7
+    lib.bd_attend_prompt_workspace_bytes.restype = sz
     return lib
 
 

@@ -103,3 +103,36 @@ def score_error(dim, reach, cap=0.0, slope_reach=0.0):
     off by 2^-21 where its argument is past a quarter, and by less of its result below), the distance's product and sum."""
     u = 2.0 ** -24
     return (dim + 8) * u * reach + (2.0 ** -19 * min(reach, cap) if cap else 0.0) + 3 * u * slope_reach
+
+
+def attend_prompt(q, k_rows, v_rows, scale, first, last, position, cap=0.0, slopes=None):
+    """New tokens of one sequence: q [n, Hq, D], rows [len, H, D] (float64), per token its range of keys and its position
+    -> (out [n, Hq, D], lse [n, Hq], largest sum of |q k| scale, and the weights' mean of |v| and root mean square share of
+    it: sum p |v| / sum p and sqrt(sum (p v)^2) / sum p, both [n, Hq, D])."""
+    n, hq, d = q.shape
+    out, lse = np.zeros(q.shape), np.full((n, hq), -np.inf)
+    mean, share, reach = np.zeros(q.shape), np.zeros(q.shape), 0.0
+    group = hq // k_rows.shape[1]
+    for t in range(n):
+        lo, hi = max(0, int(first[t])), min(len(k_rows), int(last[t]))
+        if lo >= hi:
+            continue
+        for h in range(k_rows.shape[1]):
+            at = slice(h * group, h * group + group)
+            k, v = k_rows[lo:hi, h], v_rows[lo:hi, h]
+            slope = None if slopes is None else slopes[at]
+            s, a = scores(q[t, at], np.broadcast_to(k, (group, *k.shape)), scale, cap, slope, int(position[t]) - lo)
+            reach = max(reach, a)
+            with np.errstate(all="ignore"):
+                top = s.max(1, keepdims=True)
+                p = np.exp(s - top)
+                total = p.sum(1, keepdims=True)
+                lse[t, at] = (top + np.log(total))[:, 0]
+                p = p / total
+                if np.isfinite(v).all():
+                    out[t, at], mean[t, at], share[t, at] = p @ v, p @ np.abs(v), np.sqrt(p ** 2 @ v ** 2)
+                else:
+                    pv = p[:, :, None] * v
+                    out[t, at], fine = pv.sum(1), np.where(np.isfinite(pv), pv, 0.0)
+                    mean[t, at], share[t, at] = np.abs(fine).sum(1), np.sqrt((fine ** 2).sum(1))
+    return out, lse, reach, mean, share
