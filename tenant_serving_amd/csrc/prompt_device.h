@@ -150,6 +150,12 @@ __device__ __forceinline__ Range range_of(const Args& p, const Tile& t, int len,
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
+// 16 bytes for every lane, written to LDS from `to` on, lane after lane.
+__device__ __forceinline__ void load_to_lds(const char* from, char* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
 // 16 bytes of bf16 values from eight held ones.
 template <int kHeld>
 struct Piece;
@@ -157,9 +163,7 @@ template <>
 struct Piece<BD_BF16> {
     uint4 w;
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const char* row, int piece, const uint8_t*) {
-        w = *reinterpret_cast<const uint4*>(row + piece * 16);
-    }
+    __device__ __forceinline__ void load(const char* at, const uint8_t*) { w = *reinterpret_cast<const uint4*>(at); }
     __device__ __forceinline__ uint4 value() const { return w; }
 };
 template <>
@@ -167,8 +171,8 @@ struct Piece<BD_E4M3> {
     uint2 w;
     int byte;
     __device__ __forceinline__ void zero() { w = make_uint2(0, 0), byte = 127; }
-    __device__ __forceinline__ void load(const char* row, int piece, const uint8_t* scale) {
-        w = *reinterpret_cast<const uint2*>(row + piece * 8);
+    __device__ __forceinline__ void load(const char* at, const uint8_t* scale) {
+        w = *reinterpret_cast<const uint2*>(at);
         byte = *scale;
     }
     __device__ __forceinline__ uint4 value() const {
@@ -182,8 +186,8 @@ struct Piece<BD_E2M1> {
     uint32_t w;
     int byte;
     __device__ __forceinline__ void zero() { w = 0, byte = 127; }
-    __device__ __forceinline__ void load(const char* row, int piece, const uint8_t* scale) {
-        w = *reinterpret_cast<const uint32_t*>(row + piece * 4);
+    __device__ __forceinline__ void load(const char* at, const uint8_t* scale) {
+        w = *reinterpret_cast<const uint32_t*>(at);
         byte = *scale;
     }
     __device__ __forceinline__ uint4 value() const { return e2m1x8_to_bf16(w, scale_of(byte)); }
@@ -195,36 +199,29 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
     return bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w);
 }
 
-// How a key's row lies in LDS: kStride bytes, 16-byte piece i of a key at place
-// i ^ key_swap(row) (its low bits only), 64-byte piece u of a value at u ^ value_swap(row).
-template <int kW>
-struct Lds {
-    static constexpr int kStride = kW * 2;
-    static constexpr int kKeyBits = kW == 96 ? 3 : kW % 128 == 0 ? 15 : 7;
-    static constexpr int kValueBits = kW == 96 ? 0 : kW % 128 == 0 ? 3 : 1;
-    static constexpr int kPieces = kW / 8;
-    __device__ static __forceinline__ int key_swap(int row) {
-        return kW == 96 ? (row >> 2) & 3 : kW % 128 == 0 ? row & 15 : (row >> 1) & 7;
-    }
-    __device__ static __forceinline__ int value_swap(int row) {
-        return kW == 96 ? 0 : kW % 128 == 0 ? row & 3 : (row >> 1) & 1;
-    }
-    __device__ static __forceinline__ int key_at(int row, int piece) { return row * kStride + (piece ^ key_swap(row)) * 16; }
-    __device__ static __forceinline__ int value_at(int row, int piece) {
-        return row * kStride + (((piece >> 2) ^ value_swap(row)) * 4 + (piece & 3)) * 16;
-    }
-};
+// How a tile lies in LDS: blocks of 8 keys by 64 columns, 128 bytes to a key, a
+// key group's blocks one after another.  The 16-byte piece i of a key's part is
+// at place i ^ key_swap(row), of a value's at i ^ value_swap(row): the 16 keys
+// that a read of keys touches at once lie in different banks then, and so do the
+// 4 values by 32 columns of a transposing read.  A block is what one wave loads
+// at once, lane l its bytes 16 l .. 16 l + 15.
+__device__ __forceinline__ int key_swap(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int value_swap(int row) { return (row >> 1 & 1) * 4; }
 
-template <int kW, int kHeld, bool kForm>
+// kDma: bf16 rows of full width go to LDS by loads that write there.
+template <int kW, int kHeld, bool kForm, bool kDma>
 __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(const Args p) {
-    typedef Lds<kW> L;
     constexpr int kKeys = keys_of(kW), KT = kKeys / 32, KS = kW / 16, DT = kW / 32;
-    constexpr int kBuf = kKeys * L::kStride;               // bytes of a buffer of keys, or of values
-    constexpr int kEach = kKeys * L::kPieces / kThreads;   // pieces of a thread, of keys and of values each
-    static_assert(kKeys * L::kPieces % kThreads == 0, "whole pieces for every thread");
-    __shared__ __attribute__((aligned(16))) char smem[4 * kBuf];
+    constexpr int NI = (kW + 63) / 64;             // blocks of a key group
+    constexpr int kGroup = NI * 1024;              // bytes of one
+    constexpr int kBuf = kKeys / 8 * kGroup;       // bytes of a buffer of keys, or of values
+    constexpr int G = kKeys / 8 / kWaves;          // key groups that a wave stages
+    static_assert(G * kWaves * 8 == kKeys, "whole groups for every wave");
+    // two variables, so that the loads into one are not waited for where the other is read
+    __shared__ __attribute__((aligned(1024))) char smem0[2 * kBuf], smem1[2 * kBuf];
     __shared__ int sr[4][kWaves];
-    __shared__ __attribute__((aligned(16))) uint32_t sbad[3][4];  // keys with values not finite; keys of bad pages
+    // of the tile in work and the two after it: whether there are any, keys with values not finite, keys of bad pages
+    __shared__ uint32_t sbad[3][5];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
@@ -260,7 +257,7 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
     }
     w_lo = uni(w_lo), w_hi = uni(w_hi), e_lo = uni(e_lo), e_hi = uni(e_hi);
     if (lane == 0) sr[0][wave] = w_lo, sr[1][wave] = w_hi, sr[2][wave] = e_lo, sr[3][wave] = e_hi;
-    if (tid < 12) (&sbad[0][0])[tid] = 0;
+    if (tid < 15) (&sbad[0][0])[tid] = 0;
     __syncthreads();
     int k_lo = sr[0][0], k_hi = sr[1][0], g_lo = sr[2][0], g_hi = sr[3][0];
 #pragma unroll
@@ -289,58 +286,114 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
         }
     }
 
-    // staging: the thread's pieces of a tile, the same of keys and of values
-    Piece<kHeld> kp[kEach], vp[kEach];
-    int page[kEach];      // of the tile after the one in flight
-    uint32_t lost = 0;    // pieces of bad pages
+    // Staging.  A wave takes G groups of 8 keys; lane l loads piece l % 8 (as
+    // the swap has it) of key l / 8, in every block.  Groups before the first
+    // key and behind the last are taken for these keys' groups, so that any
+    // address is one of the sequence; what lies outside is masked as keys are
+    // and cleared as values are.
+    const int r8 = lane >> 3, c8 = lane & 7;
+    const uint64_t token_bytes = (uint64_t)p.token16 * 16;
+    constexpr int kPiece = kHeld == BD_BF16 ? 16 : kHeld == BD_E4M3 ? 8 : 4;  // bytes of eight held values
+    int k_piece[G];
+    uint64_t k_off[G], v_off;
+    const int v_piece = c8 ^ value_swap(r8);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        k_piece[g] = c8 ^ key_swap((wave * G + g) * 8 + r8);
+        k_off[g] = r8 * token_bytes + k_piece[g] * kPiece;
+    }
+    v_off = r8 * token_bytes + v_piece * kPiece;
+    Piece<kHeld> kp[kDma ? 1 : G][kDma ? 1 : NI], vp[kDma ? 1 : G][kDma ? 1 : NI];
+    int page[G];        // of the tile after the one in flight, still on their way
+    uint32_t lost = 0;  // groups in flight whose page is a bad one
     const int32_t* table = p.a.table + tile.b * p.a.table_stride;
-    const auto row_of = [&](int i) { return (tid + kThreads * i) / L::kPieces; };
-    const auto piece_of = [&](int i) { return (tid + kThreads * i) % L::kPieces; };
+    const int first8 = k_lo >> 3, last8 = (k_hi - 1) >> 3;
+    const auto group8 = [&](int t, int g) {
+        const int g8 = (base >> 3) + t * (kKeys / 8) + wave * G + g;
+        return g8 < first8 ? first8 : g8 > last8 ? last8 : g8;
+    };
     const auto index_of = [&](int g8) {  // exact: g8 < 2^21, pg8 <= 2^9
-        return __umulhi((uint32_t)g8, (uint32_t)p.magic) + (p.pg8 == 1 ? (uint32_t)g8 : 0u);
+        return (int)(((uint64_t)(uint32_t)g8 * (uint32_t)p.magic) >> 32) + (p.pg8 == 1 ? g8 : 0);
     };
     const auto look_up = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int j = base + t * kKeys + row_of(i);
-            page[i] = j >= k_lo && j < k_hi ? table[index_of(j >> 3)] : 0;
-        }
+        for (int g = 0; g < G; ++g) page[g] = table[index_of(group8(t, g))];
     };
-    const auto load = [&](int t) {
+    const auto load = [&](int t, char* smem) {
         lost = 0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int j = base + t * kKeys + row_of(i), piece = piece_of(i);
-            kp[i].zero();
-            vp[i].zero();
-            if (j >= k_lo && j < k_hi && piece * 8 < p.dim) {
-                if ((uint32_t)page[i] >= p.pages) {
-                    lost |= 1u << i;
-                } else {
-                    const uint32_t at = (uint32_t)j - index_of(j >> 3) * (uint32_t)(p.pg8 * 8);
-                    const uint64_t to = ((uint64_t)(uint32_t)page[i] * p.page16 + (uint64_t)at * p.token16 +
-                                         (uint64_t)(uint32_t)head * p.head16) * 16;
-                    uint64_t sc = (uint64_t)(uint32_t)page[i] * p.page_scales + ((uint32_t)head * p.head_scales + at);
-                    if (kHeld == BD_E2M1) sc += (uint32_t)(piece / 4) * (uint32_t)(p.pg8 * 8);
-                    kp[i].load(static_cast<const char*>(p.a.kv.k) + to, piece, p.a.kv.k_scales + sc);
-                    vp[i].load(static_cast<const char*>(p.a.kv.v) + to, piece, p.a.kv.v_scales + sc);
+        for (int g = 0; g < G; ++g) {
+            const int g8 = group8(t, g), at = (g8 - index_of(g8) * p.pg8) * 8;
+            uint32_t pg = (uint32_t)uni(page[g]);
+            if (pg >= p.pages) {
+                lost |= 1u << g;
+                pg = 0;
+            }
+            const uint64_t to = ((uint64_t)pg * p.page16 + (uint64_t)(uint32_t)at * p.token16 +
+                                 (uint64_t)(uint32_t)head * p.head16) * 16;
+            const char* k = static_cast<const char*>(p.a.kv.k) + to;
+            const char* v = static_cast<const char*>(p.a.kv.v) + to;
+            if constexpr (kDma) {
+                char* ks = smem + (wave * G + g) * kGroup;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    load_to_lds(k + k_off[g] + i * 128, ks + i * 1024);
+                    load_to_lds(v + v_off + i * 128, ks + kBuf + i * 1024);
+                }
+            } else {
+                const uint64_t sc = (uint64_t)pg * p.page_scales + ((uint32_t)head * p.head_scales + (uint32_t)at);
+                const uint8_t* k_sc = p.a.kv.k_scales + sc + r8;
+                const uint8_t* v_sc = p.a.kv.v_scales + sc + r8;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    kp[g][i].zero();
+                    vp[g][i].zero();
+                    const int k_at = i * 8 + k_piece[g], v_at = i * 8 + v_piece;
+                    const int group = kHeld == BD_E2M1 ? p.pg8 * 8 : 0;  // scale bytes of a group of columns
+                    if (k_at * 8 < p.dim) kp[g][i].load(k + k_off[g] + i * 8 * kPiece, k_sc + k_at / 4 * group);
+                    if (v_at * 8 < p.dim) vp[g][i].load(v + v_off + i * 8 * kPiece, v_sc + v_at / 4 * group);
                 }
             }
         }
     };
-    const auto stage = [&](int t, int buf, int turn) {
+    // The tile in flight, when it has come: into LDS, and where some row sees
+    // part of it only, what is outside the keys cleared and values that are not
+    // finite marked.
+    const auto stage = [&](int t, char* smem, int turn) {
         const int j0 = base + t * kKeys;
         const bool edge = j0 < g_lo || j0 + kKeys > g_hi;
-        char* ks = smem + buf * 2 * kBuf;
-        char* vs = ks + kBuf;
+        char* ks = smem + wave * (G * kGroup) + lane * 16;
+        if constexpr (kDma) {
+            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        } else {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int r = row_of(i), piece = piece_of(i);
-            const uint4 v = vp[i].value();
-            *reinterpret_cast<uint4*>(ks + L::key_at(r, piece)) = kp[i].value();
-            *reinterpret_cast<uint4*>(vs + L::value_at(r, piece)) = v;
-            if (edge && not_finite(v)) atomicOr(&sbad[turn][r >> 5], 1u << (r & 31));
-            if (lost >> i & 1) atomicOr(&sbad[turn][2 + (r >> 5)], 1u << (r & 31));
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    *reinterpret_cast<uint4*>(ks + g * kGroup + i * 1024) = kp[g][i].value();
+                    *reinterpret_cast<uint4*>(ks + kBuf + g * kGroup + i * 1024) = vp[g][i].value();
+                }
+        }
+        if (edge || lost) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int r = (wave * G + g) * 8 + r8, j = j0 + r;
+                const bool in = j >= k_lo && j < k_hi, gone = lost >> g & 1;
+                uint32_t* bad = sbad[turn];
+                bool odd = false;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    uint4* v = reinterpret_cast<uint4*>(ks + kBuf + g * kGroup + i * 1024);
+                    if (!in || gone)
+                        *v = make_uint4(0, 0, 0, 0);
+                    else
+                        odd |= not_finite(*v);
+                }
+                if (in && (odd || gone)) {
+                    atomicOr(&bad[(gone ? 3 : 1) + (r >> 5)], 1u << (r & 31));
+                    bad[0] = 1;
+                }
+            }
         }
     };
 
@@ -349,38 +402,44 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
     for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
-    float m = kNegInf, mm = 0.0f, l = 0.0f;  // mm: m, or 0 while m is -infinity
+    // The weights are 2^(c s - mc), mc = c m rounded: one operation before the
+    // exponential.  What the rounding adds to all of them, c m - mc, is exact in
+    // fp32 (`rest`) and taken out where the sums change their maximum or end.
+    // Where mc is so large that this could pass fp32's range (`careful`), the
+    // difference to m comes first.
+    float m = kNegInf, l = 0.0f, mc = 0.0f, rest_c = 0.0f;
+    bool careful = false;
     const float c = p.c, times = kForm ? __builtin_fabsf(p.a.scale) : 1.0f;
 
     // where the lane reads keys and values; what a step of the products adds is the same for all lanes
     const int key = (col & 16) + (col >> 2 & 1) * 8 + (col >> 3 & 1) * 4 + (col & 3);
-    const int k_base = L::key_at(key, half);
+    const int k_base = (key >> 3) * kGroup + (key & 7) * 128 + (half ^ key_swap(key)) * 16;
     const int l16 = lane & 15;
-    const int v_row = half * 8 + (l16 >> 2);
-    const int v_base = v_row * L::kStride + L::value_swap(v_row) * 64 + (lane >> 4 & 1) * 32 + (l16 & 3) * 8;
+    const int v_row = l16 >> 2;
+    const int v_base = half * kGroup + v_row * 128 + value_swap(v_row) * 16 + (lane >> 4 & 1) * 32 + (l16 & 3) * 8;
 
     if (t_from < t_to) {
         look_up(t_from);
-        load(t_from);
+        load(t_from, smem0);
         look_up(t_from + 1);
-        stage(t_from, 0, 0);
+        stage(t_from, smem0, 0);
     }
     __syncthreads();
 
-    int buf = 0, turn = 0;
-    for (int t = t_from; t < t_to; ++t) {
+    int turn = 0;
+    // One key tile, in `smem`, while the next one comes into `other`.
+    const auto work = [&](int t, char* smem, char* other) {
         const bool more = t + 1 < t_to;
         if (more) {
-            load(t + 1);
+            load(t + 1, other);
             look_up(t + 2);
         }
         const int j0 = base + t * kKeys;
         const bool here = j0 < w_hi && j0 + kKeys > w_lo;  // this wave has rows that see some of it
-        const uint4 bad = *reinterpret_cast<const uint4*>(sbad[turn]);
-        const uint32_t bad_v0 = uni(bad.x), bad_v1 = uni(bad.y), no0 = uni(bad.z), no1 = uni(bad.w);
+        const uint32_t marked = uni(sbad[turn][0]);
         const int next_turn = turn == 2 ? 0 : turn + 1;
-        if (tid < 4) sbad[next_turn == 2 ? 0 : next_turn + 1][tid] = 0;
-        const char* ks = smem + buf * 2 * kBuf;
+        if (tid < 5) sbad[next_turn == 2 ? 0 : next_turn + 1][tid] = 0;
+        const char* ks = smem;
         const char* vs = ks + kBuf;
         uint4 pw[KT * 2];  // weights, 8 consecutive keys each
         if (here) {
@@ -392,8 +451,7 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
                 for (int r = 0; r < 16; ++r) s[r] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
-                    const int at = (k_base ^ ((2 * i & L::kKeyBits) * 16)) + (2 * i & ~L::kKeyBits) * 16 + kt * 32 * L::kStride;
-                    const uint4 a = *reinterpret_cast<const uint4*>(ks + at);
+                    const uint4 a = *reinterpret_cast<const uint4*>(ks + (k_base ^ (i % 4 * 32)) + i / 4 * 1024 + kt * 4 * kGroup);
                     s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(q[i]), s, 0, 0, 0);
                 }
 #pragma unroll
@@ -413,15 +471,17 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
                         sc[i] = __builtin_fmaf(-slope, __builtin_fabsf((float)(far - (i / 8 * 16 + i % 8))), sc[i]);
                 }
             }
-            if (j0 < e_lo || j0 + kKeys > e_hi || (no0 | no1) != 0) {
+            if (marked) {
+                const uint32_t no0 = sbad[turn][3] >> 8 * half, no1 = sbad[turn][4] >> 8 * half;
+#pragma unroll
+                for (int i = 0; i < KT * 16; ++i)
+                    if ((i < 16 ? no0 : no1) >> (i % 16 / 8 * 16 + i % 8) & 1) sc[i] = __builtin_nanf("");
+            }
+            if (j0 < e_lo || j0 + kKeys > e_hi) {
                 const int from = j0 + 8 * half - range.lo, n = range.hi - range.lo;
 #pragma unroll
-                for (int i = 0; i < KT * 16; ++i) {
-                    const int add = i / 8 * 16 + i % 8;
-                    const uint32_t no = add < 32 ? no0 : no1;
-                    if (no >> (add % 32 + 8 * half) & 1) sc[i] = __builtin_nanf("");
-                    sc[i] = (uint32_t)(from + add) < (uint32_t)n ? sc[i] : kNegInf;
-                }
+                for (int i = 0; i < KT * 16; ++i)
+                    sc[i] = (uint32_t)(from + i / 8 * 16 + i % 8) < (uint32_t)n ? sc[i] : kNegInf;
             }
             float mx = sc[0];
 #pragma unroll
@@ -430,30 +490,38 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
                 mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
                 const float up = fmaxf(m, mx);
                 const float to = up == kNegInf ? 0.0f : up;
-                const float f = __builtin_amdgcn_exp2f((m - to) * c);
+                mc = to * c;
+                careful = __ballot(!(__builtin_fabsf(mc) < 16777216.0f)) != 0;
+                const float was = rest_c;
+                rest_c = careful ? 0.0f : __builtin_fmaf(to, c, -mc);
+                const float f = __builtin_amdgcn_exp2f((m - to) * c + (rest_c - was));
                 m = up;
-                mm = to;
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < DT; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) o[i][r] *= f;
             }
+            if (careful) {
+                const float mm = m == kNegInf ? 0.0f : m;
+#pragma unroll
+                for (int i = 0; i < KT * 16; ++i) sc[i] = __builtin_amdgcn_exp2f((sc[i] - mm) * c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < KT * 16; ++i) sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], c, -mc));
+            }
 #pragma unroll
             for (int i = 0; i < KT * 2; ++i) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    sc[8 * i + r] = __builtin_amdgcn_exp2f((sc[8 * i + r] - mm) * c);
-                    l += sc[8 * i + r];
-                }
+                for (int r = 0; r < 8; ++r) l += sc[8 * i + r];
                 pw[i] = narrow_bf16x8(sc + 8 * i);
             }
         }
-        if ((bad_v0 | bad_v1) != 0) {
+        if (marked && (sbad[turn][1] | sbad[turn][2]) != 0) {
             // keys with values that are not finite: what they add to the rows that see them, one key at a time, then
             // their values are cleared
             for (int half_of = 0; half_of < KT; ++half_of) {
-                for (uint32_t left = half_of ? bad_v1 : bad_v0; left != 0; left &= left - 1) {
+                for (uint32_t left = uni(sbad[turn][1 + half_of]); left != 0; left &= left - 1) {
                     const int r = half_of * 32 + __ffs((int)left) - 1;
                     if (!here) continue;
                     uint32_t w = 0;
@@ -466,13 +534,13 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
                     float weight = __uint_as_float(r & 1 ? w & 0xffff0000u : w << 16);
                     weight = __shfl(weight, col + 32 * (r >> 3 & 1), 64);
                     const bool seen = (uint32_t)(j0 + r - range.lo) < (uint32_t)(range.hi - range.lo);
-                    const char* v_at = vs + r * L::kStride + half * 8;
-                    const int swap = L::value_swap(r);
+                    const char* v_at = vs + (r >> 3) * kGroup + (r & 7) * 128 + half * 8;
+                    const int swap = value_swap(r) * 16;
 #pragma unroll
                     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(v_at + (dt ^ swap) * 64 + x * 16);
+                            const uint2 v = *reinterpret_cast<const uint2*>(v_at + dt / 2 * 1024 + (dt % 2 * 64 ^ swap) + x * 16);
                             const float f[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
                                                 __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
 #pragma unroll
@@ -484,10 +552,10 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
                 }
             }
             __syncthreads();
-            for (int i = tid; i < kKeys * L::kPieces; i += kThreads) {
-                const int r = i / L::kPieces;
-                if ((r < 32 ? bad_v0 : bad_v1) >> (r & 31) & 1)
-                    *reinterpret_cast<uint4*>(smem + buf * 2 * kBuf + kBuf + i * 16) = make_uint4(0, 0, 0, 0);
+            for (int i = tid; i < kKeys * NI * 8; i += kThreads) {
+                const int r = i / (NI * 64) * 8 + i / 8 % 8;  // 64 pieces to a block
+                if (sbad[turn][1 + (r >> 5)] >> (r & 31) & 1)
+                    *reinterpret_cast<uint4*>(smem + kBuf + i * 16) = make_uint4(0, 0, 0, 0);
             }
             __syncthreads();
         }
@@ -496,27 +564,32 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
             for (int i = 0; i < KT * 2; ++i)
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt) {
-                    const int at = (v_base ^ ((dt & L::kValueBits) * 64)) + (dt & ~L::kValueBits) * 64 + i * 16 * L::kStride;
-                    const s16x4_t a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vs + at));
-                    const s16x4_t a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vs + at + 4 * L::kStride));
+                    const char* at = vs + (v_base ^ (dt % 2 * 64)) + dt / 2 * 1024 + i * 2 * kGroup;
+                    const s16x4_t a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+                    const s16x4_t a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 512));
                     const uint2 b0 = __builtin_bit_cast(uint2, a0), b1 = __builtin_bit_cast(uint2, a1);
                     o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(make_uint4(b0.x, b0.y, b1.x, b1.y)),
                                                                     as_bf16x8(pw[i]), o[dt], 0, 0, 0);
                 }
         }
-        if (more) stage(t + 1, buf ^ 1, next_turn);
+        if (more) stage(t + 1, other, next_turn);
         __syncthreads();
-        buf ^= 1;
         turn = next_turn;
+    };
+    for (int t = t_from; t < t_to; t += 2) {
+        work(t, smem0, smem1);
+        if (t + 1 >= t_to) break;
+        work(t + 1, smem1, smem0);
     }
 
     l += __shfl_xor(l, 32, 64);
+    const float fix = __builtin_amdgcn_exp2f(-rest_c);
     if (!mine) return;
     const int64_t at = (int64_t)(tile.start + token) * p.a.Hq + qhead;
     if (p.splits > 1) {
         float* part = place(p, from_end, head, split);
         const int r = wave * 32 + col;
-        if (half == 0) part[2 * r] = m, part[2 * r + 1] = l;
+        if (half == 0) part[2 * r] = m, part[2 * r + 1] = l * fix;
         float* to = part + 2 * kRows + r * p.dim + half * 4;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
@@ -524,7 +597,7 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
             for (int x = 0; x < 4; ++x)
                 if (dt * 32 + x * 8 + half * 4 < p.dim)
                     *reinterpret_cast<float4*>(to + dt * 32 + x * 8) =
-                        make_float4(o[dt][4 * x], o[dt][4 * x + 1], o[dt][4 * x + 2], o[dt][4 * x + 3]);
+                        make_float4(o[dt][4 * x] * fix, o[dt][4 * x + 1] * fix, o[dt][4 * x + 2] * fix, o[dt][4 * x + 3] * fix);
         return;
     }
     float inv = sees ? 1.0f / l : 0.0f;
@@ -539,20 +612,30 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
                     make_uint2(pack_bf16x2(o[dt][4 * x] * inv, o[dt][4 * x + 1] * inv),
                                pack_bf16x2(o[dt][4 * x + 2] * inv, o[dt][4 * x + 3] * inv));
     if (p.a.lse && half == 0) {
-        const float v = __builtin_fmaf(m, p.unit, __builtin_amdgcn_logf(l) * 0.69314718055994531f);
+        const float v = __builtin_fmaf(m, p.unit, __builtin_amdgcn_logf(l * fix) * 0.69314718055994531f);
         p.a.lse[at] = given > p.capacity ? __builtin_nanf("") : sees ? v : kNegInf;
     }
 }
 
+template <int kW, int kHeld, bool kForm>
+void go_width(const Args& p, unsigned groups, hipStream_t s) {
+    const dim3 grid(groups), block(kThreads);
+    if constexpr (kHeld == BD_BF16 && kW % 64 == 0) {  // whole blocks only
+        if (p.dim == kW) {
+            hipLaunchKernelGGL((prompt_kernel<kW, kHeld, kForm, true>), grid, block, 0, s, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((prompt_kernel<kW, kHeld, kForm, false>), grid, block, 0, s, p);
+}
 template <int kHeld, bool kForm>
 void go(const Args& p, unsigned groups, hipStream_t s) {
-    const dim3 grid(groups), block(kThreads);
     switch (width_of(p.dim)) {
-        case 64: hipLaunchKernelGGL((prompt_kernel<64, kHeld, kForm>), grid, block, 0, s, p); break;
-        case 96: hipLaunchKernelGGL((prompt_kernel<96, kHeld, kForm>), grid, block, 0, s, p); break;
-        case 128: hipLaunchKernelGGL((prompt_kernel<128, kHeld, kForm>), grid, block, 0, s, p); break;
-        case 192: hipLaunchKernelGGL((prompt_kernel<192, kHeld, kForm>), grid, block, 0, s, p); break;
-        default: hipLaunchKernelGGL((prompt_kernel<256, kHeld, kForm>), grid, block, 0, s, p);
+        case 64: go_width<64, kHeld, kForm>(p, groups, s); break;
+        case 96: go_width<96, kHeld, kForm>(p, groups, s); break;
+        case 128: go_width<128, kHeld, kForm>(p, groups, s); break;
+        case 192: go_width<192, kHeld, kForm>(p, groups, s); break;
+        default: go_width<256, kHeld, kForm>(p, groups, s);
     }
 }
 
