@@ -153,12 +153,13 @@ hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
     const auto unit16 = [&](int64_t stride) { return (uint32_t)(stride * (held == BD_BF16 ? 2 : 1) / 16); };
     const uint32_t head_scales = (uint32_t)(a.kv.page_size * (held == BD_E2M1 ? D / kGroup4 : 1));
     const float scale = __builtin_fabsf(a.scale);
+    const Form form = form_of(a.scale, a.cap);
     Args p{a, shape_of(a.B, a.Hq, a.kv.num_heads, D, a.kv.page_size, a.max_pages,
                      per_cu(width_of(D, held), q_fp32, held)),
            (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride), unit16(a.kv.token_stride),
            a.kv.num_heads * head_scales, head_scales,
-           formed ? 1.4426950408889634f : __builtin_fmaxf(scale * 1.4426950408889634f, kLeastC),
-           formed ? 1.0f : scale, a.scale < 0.0f ? 0x80008000u : 0u};
+           __builtin_fmaxf((formed ? form.unit : scale) * 1.4426950408889634f, kLeastC),
+           formed ? form.unit : scale, form.times, a.scale < 0.0f ? 0x80008000u : 0u};
     if (workspace_of(p.s) > attend_workspace_bytes(a.B, a.Hq, a.kv.num_heads, D, a.kv.page_size, a.max_pages))
         return hipErrorInvalidValue;  // what is laid out here is what the caller was told to bring
     if (held == BD_E2M1)

@@ -40,7 +40,7 @@
 // units a row stays in one piece instead, and nothing is joined (see is_whole).
 // Formed scores (kForm) are worked out between the products, on the lane's 8
 // scores: cap tanh(scale q.k / cap) less the head's slope times the distance.
-// The maximum is kept as such a score then, and c is log2(e).  Tokens before a
+// They and the maximum are kept in units of the cap then.  Tokens before a
 // sequence's first are none of its units'; those of the first group of 8 that
 // come before it are masked as those behind the end are.
 // fp32 queries' third term costs up to 4% (31 sequences of 4000 tokens, 32 heads
@@ -105,9 +105,9 @@ struct Args {
     uint32_t pages;                         // of the cache
     uint32_t page16, head16, token16;       // its strides in units of 16 bytes
     uint32_t page_scales, head_scales;      // scale bytes of a page, of a head of it
-    float c;                                // what the maximum's units take to be exponents of 2: |scale| log2(e), no
-                                            // smaller than kLeastC, or log2(e) for formed scores
-    float unit;                             // what they take to be scores: |scale|, or 1
+    // what the maximum's units take to be exponents of 2, no smaller than kLeastC, and to be scores
+    float c, unit;
+    float times;                            // what a product takes to be a formed score
     uint32_t flip;                          // the queries' sign bits where scale is negative
 };
 
@@ -337,12 +337,15 @@ __device__ __forceinline__ uint32_t e2m1_pair(uint32_t w, float scale, int byte)
 
 __device__ __forceinline__ void flip(uint4& v, uint32_t mask) { v.x ^= mask, v.y ^= mask, v.z ^= mask, v.w ^= mask; }
 
-// The scores of 8 consecutive tokens from their products: `times` makes scores of
-// them, `far` is the first one's distance to the new token.
+// The scores of 8 consecutive tokens from their products, `far` the first one's
+// distance to the new token.
 __device__ __forceinline__ void form_scores(const Args& p, float* sc, float times, float slope, int far) {
+    if (p.a.cap > 0.0f) {
+        cap_scores<8>(sc, times);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sc[j] *= times;
-    if (p.a.cap > 0.0f) cap_scores<8>(sc, p.a.cap);
+        for (int j = 0; j < 8; ++j) sc[j] *= times;
+    }
     if (p.a.slopes) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sc[j] = __builtin_fmaf(-slope, (float)(far - j), sc[j]);
@@ -636,8 +639,8 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
 
         f32x4_t acc[DV];
         float m, mm, l;  // mm: m, or 0 while m is -infinity
-        float c = p.c, times = kForm ? __builtin_fabsf(p.a.scale) : 1.0f;  // a product's factor to be a score
-        const float bias = slope;
+        float c = p.c, times = kForm ? p.times : 1.0f;
+        const float bias = kForm ? slope / p.unit : 0.0f;
         int pass = 0;  // 1: again, see below
         bool lost = false;
 

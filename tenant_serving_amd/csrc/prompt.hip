@@ -13,20 +13,21 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
     const int head = blockIdx.x % p.heads, from_end = blockIdx.x / p.heads;
     const Tile tile = tile_at(p, from_end);
     if (tile.none) return;
-    const int given = uni(p.a.lengths[tile.b]);
+    const int given = tile.given;
     const int len = given > p.capacity || given < 0 ? 0 : given;
     const int lanes = p.dim / 4;
-    const int rows = tile.n * p.group - tile.row < kRows ? tile.n * p.group - tile.row : kRows;
+    const int rows = tile.n * p.group - tile.row < p.rows ? tile.n * p.group - tile.row : p.rows;
     const int items = rows * lanes;
     for (int i = (int)(blockIdx.y * 256 + threadIdx.x); i < items; i += (int)gridDim.y * 256) {
         const int r = i / lanes, d = (i - r * lanes) * 4;
         const int token = (tile.row + r) / p.group, qhead = head * p.group + (tile.row + r) - token * p.group;
         float M = kNegInf, L = 0.0f;
         float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 4
         for (int s = 0; s < p.splits; ++s) {
             const float* part = place(p, from_end, head, s);
             const float m = part[2 * r], l = part[2 * r + 1];
-            const float4 x = *reinterpret_cast<const float4*>(part + 2 * kRows + r * p.dim + d);
+            const float4 x = *reinterpret_cast<const float4*>(part + 2 * p.rows + r * p.dim + d);
             // a part whose scores are all -infinity, or that saw no keys, has sum and output 0 (or NaN)
             const float to = fmaxf(M, m);
             const float f = M == kNegInf ? 1.0f : __builtin_amdgcn_exp2f((M - to) * p.c);
@@ -50,15 +51,17 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
 }
 
 // Tiles at most: whole ones of all rows, and one that is not for each sequence.
-int64_t tiles_at_most(int64_t T, int64_t B, int64_t group) { return T * group / kRows + B; }
+int64_t tiles_at_most(int64_t T, int64_t B, int64_t group, int rows) { return T * group / rows + B; }
+int rows_of(int64_t D) { return 32 * waves_of(width_of((int)D)); }
 
 // Workgroups that share a tile's keys: as many as make two workgroups for each
-// CU, while each has 256 keys of a full table.
-constexpr int64_t kWanted = 512, kLeastKeys = 256;
-int64_t splits_of(int64_t tiles, int64_t heads, int64_t capacity) {
-    const int64_t groups = tiles * heads;
-    int64_t n = (kWanted + groups - 1) / groups;
-    const int64_t most = capacity / kLeastKeys;
+// CU, while each has 256 keys of a full table, or 1024 where one workgroup per CU
+// is there already (us with 256 / 512 / 1024: 3 sequences of 5 tokens behind 1000
+// 21 / 32 / 31, 64 tokens behind 2048 25 / 29 / 40; 512 tokens 29 / 23 / 23).
+int64_t splits_of(int64_t tiles, int64_t heads, int64_t capacity, int rows) {
+    const int64_t groups = tiles * heads, wanted = 256;
+    int64_t n = (wanted + groups - 1) / groups;
+    const int64_t most = capacity / (groups < 256 ? 256 : 1024);
     n = n < most ? n : most;
     return n < 1 ? 1 : n;
 }
@@ -66,8 +69,9 @@ int64_t splits_of(int64_t tiles, int64_t heads, int64_t capacity) {
 }  // namespace
 
 size_t prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t capacity) {
-    const int64_t tiles = tiles_at_most(T, B, Hq / H), splits = splits_of(tiles, H, capacity);
-    return splits == 1 ? 0 : (size_t)(tiles * H * splits * kRows * (D + 2)) * sizeof(float);
+    const int rows = rows_of(D);
+    const int64_t tiles = tiles_at_most(T, B, Hq / H, rows), splits = splits_of(tiles, H, capacity, rows);
+    return splits == 1 ? 0 : (size_t)(tiles * H * splits * rows * (D + 2)) * sizeof(float);
 }
 
 hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream) {
@@ -76,14 +80,16 @@ hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream) {
     const auto unit16 = [&](int64_t stride) { return (uint32_t)(stride * (held == BD_BF16 ? 2 : 1) / 16); };
     const uint32_t head_scales = (uint32_t)(a.kv.page_size * (held == BD_E2M1 ? D / kGroup4 : 1));
     const float scale = __builtin_fabsf(a.scale);
+    const Form form = form_of(a.scale, a.cap);
     const int pg8 = a.kv.page_size / 8;
-    const int64_t tiles = tiles_at_most(a.T, a.B, a.Hq / H);
-    const Args p{a, D, H, a.Hq / H, pg8, pg8 == 1 ? 0 : (int32_t)(uint32_t)((uint64_t(1) << 32) / pg8 + 1),
-                 a.kv.page_size * a.max_pages, (int32_t)splits_of(tiles, H, (int64_t)a.kv.page_size * a.max_pages),
+    const int rows = rows_of(D);
+    const int64_t tiles = tiles_at_most(a.T, a.B, a.Hq / H, rows);
+    const Args p{a, D, H, a.Hq / H, rows, pg8, pg8 == 1 ? 0 : (int32_t)(uint32_t)((uint64_t(1) << 32) / pg8 + 1),
+                 a.kv.page_size * a.max_pages, (int32_t)splits_of(tiles, H, (int64_t)a.kv.page_size * a.max_pages, rows),
                  (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride),
                  unit16(a.kv.token_stride), H * head_scales, head_scales,
-                 formed ? 1.4426950408889634f : __builtin_fmaxf(scale * 1.4426950408889634f, kLeastC),
-                 formed ? 1.0f : scale, a.scale < 0.0f ? 0x80008000u : 0u};
+                 __builtin_fmaxf((formed ? form.unit : scale) * 1.4426950408889634f, kLeastC),
+                 formed ? form.unit : scale, form.times, a.scale < 0.0f ? 0x80008000u : 0u};
     const unsigned groups = (unsigned)(tiles * H * p.splits);
     if (held == BD_E2M1)
         formed ? go_e2m1_formed(p, groups, stream) : go_e2m1(p, groups, stream);
@@ -95,7 +101,7 @@ hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream) {
     if (e != hipSuccess || p.splits == 1) return e;
     // the rows of a tile over as many workgroups as make about four for each CU
     int64_t y = 4 * 256 / (tiles * H);
-    const int64_t most = (int64_t)kRows * D / 4 / 256;
+    const int64_t most = (int64_t)rows * D / 4 / 256;
     y = y < 1 ? 1 : y > most ? most : y;
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)(tiles * H), (unsigned)y), dim3(256), 0, stream, p);
     return hipGetLastError();

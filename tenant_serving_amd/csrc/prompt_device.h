@@ -40,43 +40,48 @@
 // workgroups, whose fp32 partial results a second kernel adds in order.
 #pragma once
 
+#include <type_traits>
+
 #include "step_internal.h"
 
 namespace bd {
 namespace prompt {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * 64;
-constexpr int kRows = kWaves * 32;  // of a tile
 constexpr float kLazy = 10.0f;      // log2: how large a weight may be before the maximum moves
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLeastC = 0x1p-149f;  // times it -infinity stays what it is
 
 // A kernel's width: head_dim rounded up to 64, 96, 128, 192 or 256.
 constexpr int width_of(int dim) { return dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256; }
-// Keys of a tile: two buffers of keys and values in half a CU's LDS.
+// Keys of a tile.
 constexpr int keys_of(int width) { return width <= 128 ? 64 : 32; }
+
+// Waves of a workgroup: 8, or 4 where two to a SIMD would not have the registers.
+constexpr int waves_of(int width) { return width <= 192 ? 8 : 4; }
 
 struct Args {
     PromptArgs a;
     int32_t dim, heads, group;
+    int32_t rows;                      // of a tile: 32 for each wave of a workgroup
     int32_t pg8, magic;                // groups of 8 tokens in a page
     int32_t capacity;                  // tokens a table row holds
     int32_t splits;
     uint32_t pages;                    // of the cache
     uint32_t page16, head16, token16;  // its strides in units of 16 bytes
     uint32_t page_scales, head_scales; // scale bytes of a page, of a head of it
-    float c;                           // what the maximum's units take to be exponents of 2
-    float unit;                        // what they take to be scores
+    // what the maximum's units take to be exponents of 2, no smaller than kLeastC, and to be scores
+    float c, unit;
+    float times;                       // what a product takes to be a formed score
     uint32_t flip;                     // the queries' sign bits where scale is negative
 };
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// A tile: its sequence, the sequence's new tokens, and its first row among
-// theirs.  Tiles are numbered over the batch, each sequence's in order.
+// A tile: its sequence, the sequence's new tokens and length as given, and its
+// first row among theirs.  Tiles are numbered over the batch, each sequence's in
+// order.
 struct Tile {
-    int b, start, n;  // sequence, its first new token in the batch, new tokens
+    int b, start, n, given;  // sequence, its first new token in the batch, new tokens, length
     int row;
     bool none;
 };
@@ -87,14 +92,16 @@ __device__ __forceinline__ void tokens_of(const Args& p, int b, int* start, int*
     *start = s0;
     *n = s1 - s0;
 }
-__device__ __forceinline__ int tiles_of(const Args& p, int n) { return (n * p.group + kRows - 1) / kRows; }
-// The tile that comes `from_end`-th from the end; each wave works it out.
+__device__ __forceinline__ int tiles_of(const Args& p, int n) { return (n * p.group + p.rows - 1) / p.rows; }
+// The tile that comes `from_end`-th from the end; each wave works it out, lane l
+// for `per` sequences from l per on.
 __device__ __forceinline__ Tile tile_at(const Args& p, int from_end) {
     const int lane = threadIdx.x & 63;
     const int per = (p.a.B + 63) / 64, b0 = lane * per;
-    int sum = 0, start, n;
+    int sum = 0, start = 0, n = 0, given = 0;
     for (int i = 0; i < per; ++i)
         if (b0 + i < p.a.B) {
+            given = p.a.lengths[b0 + i];
             tokens_of(p, b0 + i, &start, &n);
             sum += tiles_of(p, n);
         }
@@ -104,32 +111,40 @@ __device__ __forceinline__ Tile tile_at(const Args& p, int from_end) {
         const int o = __shfl_up(inc, off, 64);
         if (lane >= off) inc += o;
     }
-    const int total = uni(__shfl(inc, 63, 64));
-    Tile t{0, 0, 0, 0, from_end >= total};
+    const int total = __builtin_amdgcn_readlane(inc, 63);
+    Tile t{0, 0, 0, 0, 0, from_end >= total};
     if (t.none) return t;
     int at = total - 1 - from_end;
     // the first lane whose sequences end past it
-    const int l = __ffsll((unsigned long long)__ballot(inc > at)) - 1;
-    at -= uni(__shfl(inc - sum, l, 64));
+    const int l = uni(__ffsll((unsigned long long)__ballot(inc > at)) - 1);
+    at -= __builtin_amdgcn_readlane(inc - sum, l);
     t.b = l * per;
-    for (;;) {
-        tokens_of(p, t.b, &start, &n);
-        const int tiles = tiles_of(p, uni(n));
-        if (at < tiles || t.b + 1 >= p.a.B) break;
-        at -= tiles;
-        ++t.b;
+    if (per == 1) {
+        start = __builtin_amdgcn_readlane(start, l);
+        n = __builtin_amdgcn_readlane(n, l);
+        given = __builtin_amdgcn_readlane(given, l);
+    } else {
+        for (;;) {
+            tokens_of(p, t.b, &start, &n);
+            const int tiles = tiles_of(p, uni(n));
+            if (at < tiles || t.b + 1 >= p.a.B) break;
+            at -= tiles;
+            ++t.b;
+        }
+        given = p.a.lengths[t.b];
     }
     t.b = uni(t.b);
     t.start = uni(start);
     t.n = uni(n);
-    t.row = uni(at) * kRows;
+    t.given = uni(given);
+    t.row = uni(at) * p.rows;
     return t;
 }
 
-// Partial results of a split: per tile and head, `splits` places of kRows rows'
+// Partial results of a split: per tile and head, `splits` places of its rows'
 // (maximum, sum) and unnormalised outputs.
 __device__ __forceinline__ float* place(const Args& p, int tile, int head, int split) {
-    return p.a.part + (((int64_t)tile * p.heads + head) * p.splits + split) * (kRows * (p.dim + 2));
+    return p.a.part + (((int64_t)tile * p.heads + head) * p.splits + split) * (p.rows * (p.dim + 2));
 }
 
 // A row's range of keys, in its sequence of `len` tokens, and its position.
@@ -147,13 +162,36 @@ __device__ __forceinline__ Range range_of(const Args& p, const Tile& t, int len,
     return r;
 }
 
+// The largest of 32 neighbouring lanes' numbers, in all of them.
+template <int kCtrl>
+__device__ __forceinline__ int max_dpp(int x) {
+    const int o = __builtin_amdgcn_update_dpp(x, x, kCtrl, 0xf, 0xf, false);
+    return o > x ? o : x;
+}
+__device__ __forceinline__ int max_of_half(int x) {
+    x = max_dpp<0xb1>(x);   // quads: lane ^ 1
+    x = max_dpp<0x4e>(x);   // lane ^ 2
+    x = max_dpp<0x141>(x);  // mirrored within 8
+    x = max_dpp<0x140>(x);  // mirrored within 16
+    const int o = __shfl_xor(x, 16, 64);
+    return o > x ? o : x;
+}
+
+// Keys [lo, hi) that some of a set of rows see, of which [all_lo, all_hi) are
+// seen by all of them.
+struct Keys {
+    int lo, hi, all_lo, all_hi;
+};
+constexpr int kFar = 0x7fffffff;
+
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
 
-// 16 bytes for every lane, written to LDS from `to` on, lane after lane.
-__device__ __forceinline__ void load_to_lds(const char* from, char* to) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+// 16 bytes for every lane, from `off` bytes behind a uniform address, written to
+// LDS from `to` on, lane after lane.  (A buffer load: the compiler counts the
+// LDS reads behind a global one of this kind as if they came in any order.)
+__device__ __forceinline__ void load_to_lds(rsrc_t from, uint32_t off, uint32_t more, char* to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, off, more, 0, 0);
 }
 
 // 16 bytes of bf16 values from eight held ones.
@@ -208,20 +246,45 @@ __device__ __forceinline__ bool not_finite(uint4 v) {
 __device__ __forceinline__ int key_swap(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int value_swap(int row) { return (row >> 1 & 1) * 4; }
 
-// kDma: bf16 rows of full width go to LDS by loads that write there.
-template <int kW, int kHeld, bool kForm, bool kDma>
-__global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(const Args p) {
+// Four of a held row's values from column d on, in fp32; `sc` is the row's scale
+// byte, or that of its first group, `group` bytes before the next one's.
+template <int kHeld>
+__device__ __forceinline__ void four_of(const char* row, const uint8_t* sc, int group, int d, float* f) {
+    uint2 w;
+    if constexpr (kHeld == BD_BF16) {
+        w = *reinterpret_cast<const uint2*>(row + d * 2);
+    } else if constexpr (kHeld == BD_E4M3) {
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(row + d);
+        w = make_uint2(e4m3x2_to_bf16<false>(c, scale_of(*sc)), e4m3x2_to_bf16<true>(c, scale_of(*sc)));
+    } else {
+        const uint32_t c = *reinterpret_cast<const uint16_t*>(row + d / 2);
+        const float scale = scale_of(sc[d / kGroup4 * group]);
+        w = make_uint2(e2m1x2_to_bf16<0>(c, scale), e2m1x2_to_bf16<1>(c, scale));
+    }
+    f[0] = __uint_as_float(w.x << 16), f[1] = __uint_as_float(w.x & 0xffff0000u);
+    f[2] = __uint_as_float(w.y << 16), f[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+
+// kFull: head_dim is kW and 8 tokens' rows lie within 2^31 bytes; bf16 rows of
+// whole blocks go to LDS by loads that write there then.
+// kWaves: 4, or 8 that take turns.
+template <int kW, int kHeld, bool kForm, bool kFull, int kWaves>
+__global__ __launch_bounds__(kWaves * 64, kWaves == 8 || kW <= 192 ? 2 : 1) void prompt_kernel(const Args p) {
+    constexpr bool kTurns = kWaves == 8, kDma = kFull && kHeld == BD_BF16 && kW % 64 == 0;
     constexpr int kKeys = keys_of(kW), KT = kKeys / 32, KS = kW / 16, DT = kW / 32;
-    constexpr int NI = (kW + 63) / 64;             // blocks of a key group
-    constexpr int kGroup = NI * 1024;              // bytes of one
-    constexpr int kBuf = kKeys / 8 * kGroup;       // bytes of a buffer of keys, or of values
-    constexpr int G = kKeys / 8 / kWaves;          // key groups that a wave stages
-    static_assert(G * kWaves * 8 == kKeys, "whole groups for every wave");
-    // two variables, so that the loads into one are not waited for where the other is read
-    __shared__ __attribute__((aligned(1024))) char smem0[2 * kBuf], smem1[2 * kBuf];
-    __shared__ int sr[4][kWaves];
-    // of the tile in work and the two after it: whether there are any, keys with values not finite, keys of bad pages
-    __shared__ uint32_t sbad[3][5];
+    constexpr int NI = (kW + 63) / 64;        // blocks of a key group
+    constexpr int kGroup = NI * 1024;         // bytes of one
+    constexpr int kGroups = kKeys / 8;        // of a tile
+    constexpr int kBuf = kGroups * kGroup;    // bytes of a buffer of keys, or of values
+    // A wave stages G groups of keys and as many of values, or where there are
+    // fewer groups than waves either.
+    constexpr int G = kGroups >= kWaves ? kGroups / kWaves : 1;
+    constexpr bool kEither = kGroups < kWaves;
+    static_assert(kEither ? 2 * kGroups == kWaves : G * kWaves == kGroups, "whole groups for every wave");
+    // variables of their own, so that loads into one are not waited for where another is read
+    __shared__ __attribute__((aligned(1024))) char keys0[kBuf], keys1[kBuf], values0[kBuf], values1[kBuf];
+    __shared__ Keys sr[kWaves];
+    __shared__ int any_odd;  // some key's values were not finite, see below
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
@@ -229,170 +292,188 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
     const int split = rest % p.splits, from_end = rest / p.splits;
     const Tile tile = tile_at(p, from_end);
     if (tile.none) return;
-    const int given = uni(p.a.lengths[tile.b]);
+    const int given = tile.given;
     const int len = given > p.capacity || given < 0 ? 0 : given;
 
     // the lane's row
+    const int rows = tile.n * p.group;
     const int row = tile.row + wave * 32 + col;
-    const bool mine = row < tile.n * p.group;
+    const bool mine = row < rows;
     const int token = mine ? row / p.group : 0, qhead = head * p.group + (mine ? row - token * p.group : 0);
-    Range range{0, 0, 0};
-    if (mine) range = range_of(p, tile, len, token);
-    const float slope = kForm && p.a.slopes && mine ? p.a.slopes[qhead] : 0.0f;
 
-    // the wave's keys [w_lo, w_hi), of which [e_lo, e_hi) are seen by all its rows; then the workgroup's
-    const bool sees = range.hi > range.lo;
-    int w_lo = sees ? range.lo : 0x7fffffff, w_hi = range.hi;
-    int e_lo = range.lo, e_hi = mine ? range.hi : 0x7fffffff;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        int o = __shfl_xor(w_lo, off, 64);
-        w_lo = o < w_lo ? o : w_lo;
-        o = __shfl_xor(w_hi, off, 64);
-        w_hi = o > w_hi ? o : w_hi;
-        o = __shfl_xor(e_lo, off, 64);
-        e_lo = o > e_lo ? o : e_lo;
-        o = __shfl_xor(e_hi, off, 64);
-        e_hi = o < e_hi ? o : e_hi;
-    }
-    w_lo = uni(w_lo), w_hi = uni(w_hi), e_lo = uni(e_lo), e_hi = uni(e_hi);
-    if (lane == 0) sr[0][wave] = w_lo, sr[1][wave] = w_hi, sr[2][wave] = e_lo, sr[3][wave] = e_hi;
-    if (tid < 15) (&sbad[0][0])[tid] = 0;
-    __syncthreads();
-    int k_lo = sr[0][0], k_hi = sr[1][0], g_lo = sr[2][0], g_hi = sr[3][0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-        k_lo = sr[0][w] < k_lo ? sr[0][w] : k_lo;
-        k_hi = sr[1][w] > k_hi ? sr[1][w] : k_hi;
-        g_lo = sr[2][w] > g_lo ? sr[2][w] : g_lo;
-        g_hi = sr[3][w] < g_hi ? sr[3][w] : g_hi;
-    }
-    k_lo = uni(k_lo), k_hi = uni(k_hi), g_lo = uni(g_lo), g_hi = uni(g_hi);
-
-    // this split's key tiles
-    const int base = k_lo & -kKeys;
-    const int tiles = k_hi > k_lo ? (k_hi - base + kKeys - 1) / kKeys : 0;
-    const int t_from = (int)((int64_t)tiles * split / p.splits), t_to = (int)((int64_t)tiles * (split + 1) / p.splits);
-
-    // queries: B operand, column col, values 16 s + 8 half ..
+    // queries: B operand, column col, values 16 s + 8 half .. (lanes without a row take the first one's, whose results
+    // are not stored)
     uint4 q[KS];
+    const uint16_t* q_row = p.a.q + (tile.start + token) * p.a.qs.token + qhead * p.a.qs.head;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-        q[s] = make_uint4(0, 0, 0, 0);
         const int d = s * 16 + half * 8;
-        if (mine && d < p.dim) {
-            q[s] = *reinterpret_cast<const uint4*>(p.a.q + (tile.start + token) * p.a.qs.token + qhead * p.a.qs.head + d);
-            q[s].x ^= p.flip, q[s].y ^= p.flip, q[s].z ^= p.flip, q[s].w ^= p.flip;
+        q[s] = *reinterpret_cast<const uint4*>(q_row + (d < p.dim ? d : 0));
+    }
+    const float slope = kForm && p.a.slopes ? p.a.slopes[qhead] / p.unit : 0.0f;
+    Range range{0, 0, 0};
+    if (mine) range = range_of(p, tile, len, token);
+    const bool sees = range.hi > range.lo;
+    if (tid == 0) any_odd = 0;
+
+    // the wave's keys and the workgroup's
+    Keys own, all;
+    if (!p.a.first && !p.a.last) {
+        // each row's end rises with its number, and all start at 0
+        const auto end_of = [&](int r) {
+            const int e = len - tile.n + r / p.group + 1;
+            return e < 0 ? 0 : e > len ? len : e;
+        };
+        const auto keys_of_rows = [&](int r0, int n) {
+            if (r0 >= rows) return Keys{kFar, 0, 0, kFar};
+            const int hi = end_of(r0 + n < rows ? r0 + n - 1 : rows - 1);
+            return Keys{hi > 0 ? 0 : kFar, hi, 0, end_of(r0)};
+        };
+        own = keys_of_rows(tile.row + wave * 32, 32);
+        all = keys_of_rows(tile.row, kWaves * 32);
+    } else {
+        own.lo = uni(-max_of_half(sees ? -range.lo : -kFar));
+        own.hi = uni(max_of_half(range.hi));
+        own.all_lo = uni(max_of_half(range.lo));
+        own.all_hi = uni(-max_of_half(mine ? -range.hi : -kFar));
+        if (lane == 0) sr[wave] = own;
+        __syncthreads();
+        all = sr[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) {
+            const Keys k = sr[w];
+            all.lo = k.lo < all.lo ? k.lo : all.lo;
+            all.hi = k.hi > all.hi ? k.hi : all.hi;
+            all.all_lo = k.all_lo > all.all_lo ? k.all_lo : all.all_lo;
+            all.all_hi = k.all_hi < all.all_hi ? k.all_hi : all.all_hi;
         }
+        all = Keys{uni(all.lo), uni(all.hi), uni(all.all_lo), uni(all.all_hi)};
     }
 
-    // Staging.  A wave takes G groups of 8 keys; lane l loads piece l % 8 (as
-    // the swap has it) of key l / 8, in every block.  Groups before the first
-    // key and behind the last are taken for these keys' groups, so that any
-    // address is one of the sequence; what lies outside is masked as keys are
-    // and cleared as values are.
+    // this split's key tiles, numbered from 0: n of them, the first from key j_from on
+    const int base = all.lo & -kKeys;
+    const int tiles = all.hi > all.lo ? (all.hi - base + kKeys - 1) / kKeys : 0;
+    const int t_from = (int)((int64_t)tiles * split / p.splits), t_to = (int)((int64_t)tiles * (split + 1) / p.splits);
+    const int n = t_to - t_from, j_from = base + t_from * kKeys;
+    // a tile that some row of the workgroup does not see all of
+    const auto edge = [&](int t) { return j_from + t * kKeys < all.all_lo || j_from + t * kKeys + kKeys > all.all_hi; };
+
+    // Staging.  Lane l loads piece l % 8 (as the swap has it) of key l / 8 of its
+    // wave's groups, in every block.  Groups before the first key and behind the
+    // last are taken for these keys' groups, so that any address is one of the
+    // sequence; what lies outside is masked as keys are and cleared as values are.
     const int r8 = lane >> 3, c8 = lane & 7;
+    const int group0 = kEither ? wave % kGroups : wave * G;
+    const bool keys_mine = !kEither || wave < kGroups, values_mine = !kEither || wave >= kGroups;
     const uint64_t token_bytes = (uint64_t)p.token16 * 16;
     constexpr int kPiece = kHeld == BD_BF16 ? 16 : kHeld == BD_E4M3 ? 8 : 4;  // bytes of eight held values
     int k_piece[G];
-    uint64_t k_off[G], v_off;
+    uint64_t k_off[G];
     const int v_piece = c8 ^ value_swap(r8);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        k_piece[g] = c8 ^ key_swap((wave * G + g) * 8 + r8);
+        k_piece[g] = c8 ^ key_swap((group0 + g) * 8 + r8);
         k_off[g] = r8 * token_bytes + k_piece[g] * kPiece;
     }
-    v_off = r8 * token_bytes + v_piece * kPiece;
-    Piece<kHeld> kp[kDma ? 1 : G][kDma ? 1 : NI], vp[kDma ? 1 : G][kDma ? 1 : NI];
-    int page[G];        // of the tile after the one in flight, still on their way
-    uint32_t lost = 0;  // groups in flight whose page is a bad one
+    const uint64_t v_off = r8 * token_bytes + v_piece * kPiece;
     const int32_t* table = p.a.table + tile.b * p.a.table_stride;
-    const int first8 = k_lo >> 3, last8 = (k_hi - 1) >> 3;
-    const auto group8 = [&](int t, int g) {
-        const int g8 = (base >> 3) + t * (kKeys / 8) + wave * G + g;
+    const int first8 = all.lo >> 3, last8 = (all.hi - 1) >> 3;
+    const auto group8 = [&](int t, int g) __attribute__((always_inline)) {
+        const int g8 = ((j_from + t * kKeys) >> 3) + g;
         return g8 < first8 ? first8 : g8 > last8 ? last8 : g8;
     };
-    const auto index_of = [&](int g8) {  // exact: g8 < 2^21, pg8 <= 2^9
+    const auto index_of = [&](int g8) __attribute__((always_inline)) {  // exact: g8 < 2^21, pg8 <= 2^9
         return (int)(((uint64_t)(uint32_t)g8 * (uint32_t)p.magic) >> 32) + (p.pg8 == 1 ? g8 : 0);
     };
-    const auto look_up = [&](int t) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) page[g] = table[index_of(group8(t, g))];
+    // Where a wave's group of a tile lies: byte and scale byte of its first
+    // token; page 0 stands in for a bad page.  A lane works it out for one tile,
+    // 64 tiles at a time.
+    struct Spot {
+        uint64_t to, sc;
+        bool bad;
     };
-    const auto load = [&](int t, char* smem) {
-        lost = 0;
+    Spot spots[G];
+    uint64_t bad_tiles[G];
+    const auto look_up = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            const int g8 = group8(t, g), at = (g8 - index_of(g8) * p.pg8) * 8;
-            uint32_t pg = (uint32_t)uni(page[g]);
-            if (pg >= p.pages) {
-                lost |= 1u << g;
-                pg = 0;
-            }
-            const uint64_t to = ((uint64_t)pg * p.page16 + (uint64_t)(uint32_t)at * p.token16 +
-                                 (uint64_t)(uint32_t)head * p.head16) * 16;
-            const char* k = static_cast<const char*>(p.a.kv.k) + to;
-            const char* v = static_cast<const char*>(p.a.kv.v) + to;
+            const int g8 = group8(t + lane, group0 + g), idx = index_of(g8), at = (g8 - idx * p.pg8) * 8;
+            uint32_t pg = (uint32_t)table[idx];
+            bad_tiles[g] = __ballot(pg >= p.pages);
+            if (pg >= p.pages) pg = 0;
+            spots[g].to = ((uint64_t)pg * p.page16 + (uint64_t)(uint32_t)at * p.token16 + (uint64_t)(uint32_t)head * p.head16) * 16;
+            spots[g].sc = (uint64_t)pg * p.page_scales + ((uint32_t)head * p.head_scales + (uint32_t)at);
+        }
+    };
+    const auto lane64 = [](uint64_t v, int l) __attribute__((always_inline)) {
+        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), l) << 32 |
+               (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, l);
+    };
+    const auto spot_of = [&](int t, int g) __attribute__((always_inline)) {
+        const int l = t & 63;
+        return Spot{lane64(spots[g].to, l), kHeld == BD_BF16 ? 0 : lane64(spots[g].sc, l), (bad_tiles[g] >> l & 1) != 0};
+    };
+    Piece<kHeld> kp[kDma ? 1 : G][kDma ? 1 : NI], vp[kDma ? 1 : G][kDma ? 1 : NI];
+    const int scale_group = kHeld == BD_E2M1 ? p.pg8 * 8 : 0;  // scale bytes from a group of columns to the next
+    const auto load = [&](const void* array, const uint8_t* scales, const Spot* x, const uint64_t* off, int same,
+                          const int* piece, auto& pieces, char* to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const char* group_at = static_cast<const char*>(array) + x[g].to;
+            char* group_to = to + (group0 + g) * kGroup;
             if constexpr (kDma) {
-                char* ks = smem + (wave * G + g) * kGroup;
+                const rsrc_t whole = make_rsrc(group_at, 0xffffffffu);
+                const uint32_t lane_off = (uint32_t)off[g * same];
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    load_to_lds(k + k_off[g] + i * 128, ks + i * 1024);
-                    load_to_lds(v + v_off + i * 128, ks + kBuf + i * 1024);
-                }
+                for (int i = 0; i < NI; ++i) load_to_lds(whole, lane_off, i * 128, group_to + i * 1024);
             } else {
-                const uint64_t sc = (uint64_t)pg * p.page_scales + ((uint32_t)head * p.head_scales + (uint32_t)at);
-                const uint8_t* k_sc = p.a.kv.k_scales + sc + r8;
-                const uint8_t* v_sc = p.a.kv.v_scales + sc + r8;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    kp[g][i].zero();
-                    vp[g][i].zero();
-                    const int k_at = i * 8 + k_piece[g], v_at = i * 8 + v_piece;
-                    const int group = kHeld == BD_E2M1 ? p.pg8 * 8 : 0;  // scale bytes of a group of columns
-                    if (k_at * 8 < p.dim) kp[g][i].load(k + k_off[g] + i * 8 * kPiece, k_sc + k_at / 4 * group);
-                    if (v_at * 8 < p.dim) vp[g][i].load(v + v_off + i * 8 * kPiece, v_sc + v_at / 4 * group);
+                    const int c = i * 8 + piece[g * same];
+                    if (!(kFull && kW % 64 == 0)) pieces[g][i].zero();
+                    if ((kFull && kW % 64 == 0) || c * 8 < p.dim)
+                        pieces[g][i].load(group_at + off[g * same] + i * 8 * kPiece, scales + x[g].sc + r8 + c / 4 * scale_group);
                 }
             }
         }
     };
-    // The tile in flight, when it has come: into LDS, and where some row sees
-    // part of it only, what is outside the keys cleared and values that are not
-    // finite marked.
-    const auto stage = [&](int t, char* smem, int turn) {
-        const int j0 = base + t * kKeys;
-        const bool edge = j0 < g_lo || j0 + kKeys > g_hi;
-        char* ks = smem + wave * (G * kGroup) + lane * 16;
-        if constexpr (kDma) {
-            __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
-        } else {
+    const auto store = [&](auto& pieces, char* to) __attribute__((always_inline)) {
+        if constexpr (!kDma) {
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    *reinterpret_cast<uint4*>(ks + g * kGroup + i * 1024) = kp[g][i].value();
-                    *reinterpret_cast<uint4*>(ks + kBuf + g * kGroup + i * 1024) = vp[g][i].value();
-                }
+                for (int i = 0; i < NI; ++i)
+                    *reinterpret_cast<uint4*>(to + (group0 + g) * kGroup + i * 1024 + lane * 16) = pieces[g][i].value();
         }
-        if (edge || lost) {
+    };
+    // Keys that have come for a bad page: NaN, as the scores of those that see them.
+    const auto spoil = [&](const Spot* x, char* keys) __attribute__((always_inline)) {
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int r = (wave * G + g) * 8 + r8, j = j0 + r;
-                const bool in = j >= k_lo && j < k_hi, gone = lost >> g & 1;
-                uint32_t* bad = sbad[turn];
-                bool odd = false;
+        for (int g = 0; g < G; ++g)
+            if (x[g].bad) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    uint4* v = reinterpret_cast<uint4*>(ks + kBuf + g * kGroup + i * 1024);
-                    if (!in || gone)
-                        *v = make_uint4(0, 0, 0, 0);
-                    else
-                        odd |= not_finite(*v);
-                }
-                if (in && (odd || gone)) {
-                    atomicOr(&bad[(gone ? 3 : 1) + (r >> 5)], 1u << (r & 31));
-                    bad[0] = 1;
-                }
+                for (int i = 0; i < NI; ++i)
+                    *reinterpret_cast<uint4*>(keys + (group0 + g) * kGroup + i * 1024 + lane * 16) =
+                        make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+            }
+    };
+    // Values of tile t that have come, where some row does not see all of it or
+    // a page is bad: what is outside the keys is cleared, and so are keys whose
+    // values are not finite, which are made up for at the end.
+    const auto clean = [&](int t, const Spot* x, char* values) __attribute__((always_inline)) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int r = (group0 + g) * 8 + r8, j = j_from + t * kKeys + r;
+            uint4* at = reinterpret_cast<uint4*>(values + (group0 + g) * kGroup + lane * 16);
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) odd |= not_finite(at[i * 64]);
+            const uint64_t rows_odd = __ballot(odd) >> (lane & 56) & 0xff;  // of the key's eight lanes
+            const bool out = j < all.lo || j >= all.hi || x[g].bad;
+            if (out || rows_odd) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) at[i * 64] = make_uint4(0, 0, 0, 0);
+                if (!out) any_odd = 1;
             }
         }
     };
@@ -404,12 +485,12 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
         for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
     // The weights are 2^(c s - mc), mc = c m rounded: one operation before the
     // exponential.  What the rounding adds to all of them, c m - mc, is exact in
-    // fp32 (`rest`) and taken out where the sums change their maximum or end.
+    // fp32 (`rest_c`) and taken out where the sums change their maximum or end.
     // Where mc is so large that this could pass fp32's range (`careful`), the
     // difference to m comes first.
     float m = kNegInf, l = 0.0f, mc = 0.0f, rest_c = 0.0f;
     bool careful = false;
-    const float c = p.c, times = kForm ? __builtin_fabsf(p.a.scale) : 1.0f;
+    const float c = p.c;
 
     // where the lane reads keys and values; what a step of the products adds is the same for all lanes
     const int key = (col & 16) + (col >> 2 & 1) * 8 + (col >> 3 & 1) * 4 + (col & 3);
@@ -418,168 +499,276 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
     const int v_row = l16 >> 2;
     const int v_base = half * kGroup + v_row * 128 + value_swap(v_row) * 16 + (lane >> 4 & 1) * 32 + (l16 & 3) * 8;
 
-    if (t_from < t_to) {
-        look_up(t_from);
-        load(t_from, smem0);
-        look_up(t_from + 1);
-        stage(t_from, smem0, 0);
+    f32x16_t s[KT];     // scores of the tile in work
+    uint4 pw[KT * 2];   // its weights, 8 consecutive keys each
+#pragma unroll
+    for (int i = 0; i < KT * 2; ++i) pw[i] = make_uint4(0, 0, 0, 0);
+
+    // The matrix products' turn: the sums of the tile before and the scores of
+    // this one, in a row of steps of one product each, whose A operands are read
+    // kAhead steps before.
+    constexpr int kSums = KT * 2 * DT, kScores = KT * KS, kAhead = 6;
+    const auto value_at = [&](const char* values, int step) __attribute__((always_inline)) {
+        const int i = step / DT, dt = step % DT;
+        const char* at = values + (v_base ^ (dt % 2 * 64)) + dt / 2 * 1024 + i * 2 * kGroup;
+        const uint2 a0 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
+        const uint2 a1 = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 512)));
+        return make_uint4(a0.x, a0.y, a1.x, a1.y);
+    };
+    const auto key_at = [&](const char* keys, int step) __attribute__((always_inline)) {
+        const int kt = step / KS, i = step % KS;
+        return *reinterpret_cast<const uint4*>(keys + (k_base ^ (i % 4 * 32)) + i / 4 * 1024 + kt * 4 * kGroup);
+    };
+    const auto products = [&](auto scores, const char* keys, const char* values) __attribute__((always_inline)) {
+        constexpr int kFrom = 0, kTo = decltype(scores)::value ? kSums + kScores : kSums;
+        if (kTurns) __builtin_amdgcn_s_setprio(1);
+        const auto fetch = [&](int step) __attribute__((always_inline)) {
+            return step < kSums ? value_at(values, step) : key_at(keys, step - kSums);
+        };
+        uint4 a[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) a[i] = fetch(kFrom + i);
+#pragma unroll
+        for (int step = kFrom; step < kTo; ++step) {
+            const bf16x8_t x = as_bf16x8(a[(step - kFrom) % kAhead]);
+            if (step < kSums) {
+                o[step % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(pw[step / DT]), o[step % DT], 0, 0, 0);
+            } else {
+                const int kt = (step - kSums) / KS, i = (step - kSums) % KS;
+                if (i == 0) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[kt][r] = 0.0f;
+                }
+                s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(q[i]), s[kt], 0, 0, 0);
+            }
+            if (step + kAhead < kTo) a[(step - kFrom) % kAhead] = fetch(step + kAhead);
+        }
+        // in just this order
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) kFrom + i < kSums ? __builtin_amdgcn_sched_group_barrier(0x100, 2, 0) : __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+        for (int step = kFrom; step < kTo; ++step) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (step + kAhead < kTo) step + kAhead < kSums ? __builtin_amdgcn_sched_group_barrier(0x100, 2, 0) : __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        if (kTurns) __builtin_amdgcn_s_setprio(0);
+    };
+
+    // The weights of tile t from its scores.
+    const auto weights = [&](int t) __attribute__((always_inline)) {
+        const int j0 = j_from + t * kKeys;
+        float sc[KT * 16];
+#pragma unroll
+        for (int i = 0; i < KT * 16; ++i) sc[i] = s[i / 16][i % 16];
+        if constexpr (kForm) {
+            if (p.a.cap > 0.0f) {
+#pragma unroll
+                for (int i = 0; i < KT * 2; ++i) cap_scores<8>(sc + 8 * i, p.times);
+            } else {
+#pragma unroll
+                for (int i = 0; i < KT * 16; ++i) sc[i] *= p.times;
+            }
+            if (p.a.slopes) {
+                const float far = (float)(range.pos - j0 - 8 * half);
+#pragma unroll
+                for (int i = 0; i < KT * 16; ++i)
+                    sc[i] = __builtin_fmaf(-slope, __builtin_fabsf(far - (float)(i / 8 * 16 + i % 8)), sc[i]);
+            }
+        }
+        if (j0 < own.all_lo) {
+            const int lo = range.lo - j0 - 8 * half;
+#pragma unroll
+            for (int i = 0; i < KT * 16; ++i) sc[i] = i / 8 * 16 + i % 8 < lo ? kNegInf : sc[i];
+        }
+        if (j0 + kKeys > own.all_hi) {
+            const int hi = range.hi - j0 - 8 * half;
+#pragma unroll
+            for (int i = 0; i < KT * 16; ++i) sc[i] = i / 8 * 16 + i % 8 < hi ? sc[i] : kNegInf;
+        }
+        float mx = sc[0];
+#pragma unroll
+        for (int i = 1; i < KT * 16; ++i) mx = fmaxf(mx, sc[i]);
+        if (__ballot((mx - m) * c > kLazy)) {
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            const float up = fmaxf(m, mx);
+            const float to = up == kNegInf ? 0.0f : up;
+            mc = to * c;
+            careful = __ballot(!(__builtin_fabsf(mc) < 16777216.0f)) != 0;
+            const float was = rest_c;
+            rest_c = careful ? 0.0f : __builtin_fmaf(to, c, -mc);
+            const float f = __builtin_amdgcn_exp2f((m - to) * c + (rest_c - was));
+            m = up;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[i][r] *= f;
+        }
+        if (careful) {
+            const float mm = m == kNegInf ? 0.0f : m;
+#pragma unroll
+            for (int i = 0; i < KT * 16; ++i) sc[i] = __builtin_amdgcn_exp2f((sc[i] - mm) * c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KT * 16; ++i) sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], c, -mc));
+        }
+#pragma unroll
+        for (int i = 0; i < KT * 2; ++i) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) l += sc[8 * i + r];
+            pw[i] = narrow_bf16x8(sc + 8 * i);
+        }
+    };
+
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        q[i].x ^= p.flip, q[i].y ^= p.flip, q[i].z ^= p.flip, q[i].w ^= p.flip;
+        if (i * 16 + half * 8 >= p.dim) q[i] = make_uint4(0, 0, 0, 0);
+    }
+    // round 0 has no tile before it: its weights and values are zeros
+    for (int i = tid * 16; i < kBuf; i += kWaves * 1024) *reinterpret_cast<uint4*>(values1 + i) = make_uint4(0, 0, 0, 0);
+    __syncthreads();  // the mark is clear
+
+    // Round t: the sums of tile t - 1 and the scores of tile t (products), then
+    // its weights, while the keys of tile t + 1 and the values of tile t come.
+    // With 8 waves the second four are half a round behind, so that of the two
+    // waves of a SIMD one has products and the other weights to work on; their
+    // share of the staging is not, so it starts and ends half a round earlier
+    // in theirs.
+    const bool late = kTurns && wave >= kWaves / 2;
+    Spot next[G], now[G];
+    if (n > 0) {
+        look_up(0);
+#pragma unroll
+        for (int g = 0; g < G; ++g) next[g] = spot_of(0, g);
+        if (keys_mine) {
+            load(p.a.kv.k, p.a.kv.k_scales, next, k_off, 1, k_piece, kp, keys0);
+            if constexpr (kDma) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+            store(kp, keys0);
+            spoil(next, keys0);
+        }
     }
     __syncthreads();
 
-    int turn = 0;
-    // One key tile, in `smem`, while the next one comes into `other`.
-    const auto work = [&](int t, char* smem, char* other) {
-        const bool more = t + 1 < t_to;
-        if (more) {
-            load(t + 1, other);
-            look_up(t + 2);
+    const auto begin = [&](int t, char* keys_to, char* values_to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) now[g] = next[g];
+        if (t + 1 < n) {
+            if (((t + 1) & 63) == 0) look_up(t + 1);
+#pragma unroll
+            for (int g = 0; g < G; ++g) next[g] = spot_of(t + 1, g);
+            if (keys_mine) load(p.a.kv.k, p.a.kv.k_scales, next, k_off, 1, k_piece, kp, keys_to);
         }
-        const int j0 = base + t * kKeys;
-        const bool here = j0 < w_hi && j0 + kKeys > w_lo;  // this wave has rows that see some of it
-        const uint32_t marked = uni(sbad[turn][0]);
-        const int next_turn = turn == 2 ? 0 : turn + 1;
-        if (tid < 5) sbad[next_turn == 2 ? 0 : next_turn + 1][tid] = 0;
-        const char* ks = smem;
-        const char* vs = ks + kBuf;
-        uint4 pw[KT * 2];  // weights, 8 consecutive keys each
-        if (here) {
-            float sc[KT * 16];
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                f32x16_t s;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const uint4 a = *reinterpret_cast<const uint4*>(ks + (k_base ^ (i % 4 * 32)) + i / 4 * 1024 + kt * 4 * kGroup);
-                    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(q[i]), s, 0, 0, 0);
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) sc[kt * 16 + r] = s[r];
-            }
-            if constexpr (kForm) {
-#pragma unroll
-                for (int i = 0; i < KT * 16; ++i) sc[i] *= times;
-                if (p.a.cap > 0.0f) {
-#pragma unroll
-                    for (int i = 0; i < KT * 2; ++i) cap_scores<8>(sc + 8 * i, p.a.cap);
-                }
-                if (p.a.slopes) {
-                    const int far = range.pos - j0 - 8 * half;
-#pragma unroll
-                    for (int i = 0; i < KT * 16; ++i)
-                        sc[i] = __builtin_fmaf(-slope, __builtin_fabsf((float)(far - (i / 8 * 16 + i % 8))), sc[i]);
-                }
-            }
-            if (marked) {
-                const uint32_t no0 = sbad[turn][3] >> 8 * half, no1 = sbad[turn][4] >> 8 * half;
-#pragma unroll
-                for (int i = 0; i < KT * 16; ++i)
-                    if ((i < 16 ? no0 : no1) >> (i % 16 / 8 * 16 + i % 8) & 1) sc[i] = __builtin_nanf("");
-            }
-            if (j0 < e_lo || j0 + kKeys > e_hi) {
-                const int from = j0 + 8 * half - range.lo, n = range.hi - range.lo;
-#pragma unroll
-                for (int i = 0; i < KT * 16; ++i)
-                    sc[i] = (uint32_t)(from + i / 8 * 16 + i % 8) < (uint32_t)n ? sc[i] : kNegInf;
-            }
-            float mx = sc[0];
-#pragma unroll
-            for (int i = 1; i < KT * 16; ++i) mx = fmaxf(mx, sc[i]);
-            if (__ballot((mx - m) * c > kLazy)) {
-                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                const float up = fmaxf(m, mx);
-                const float to = up == kNegInf ? 0.0f : up;
-                mc = to * c;
-                careful = __ballot(!(__builtin_fabsf(mc) < 16777216.0f)) != 0;
-                const float was = rest_c;
-                rest_c = careful ? 0.0f : __builtin_fmaf(to, c, -mc);
-                const float f = __builtin_amdgcn_exp2f((m - to) * c + (rest_c - was));
-                m = up;
-                l *= f;
-#pragma unroll
-                for (int i = 0; i < DT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) o[i][r] *= f;
-            }
-            if (careful) {
-                const float mm = m == kNegInf ? 0.0f : m;
-#pragma unroll
-                for (int i = 0; i < KT * 16; ++i) sc[i] = __builtin_amdgcn_exp2f((sc[i] - mm) * c);
-            } else {
-#pragma unroll
-                for (int i = 0; i < KT * 16; ++i) sc[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], c, -mc));
-            }
-#pragma unroll
-            for (int i = 0; i < KT * 2; ++i) {
-#pragma unroll
-                for (int r = 0; r < 8; ++r) l += sc[8 * i + r];
-                pw[i] = narrow_bf16x8(sc + 8 * i);
-            }
-        }
-        if (marked && (sbad[turn][1] | sbad[turn][2]) != 0) {
-            // keys with values that are not finite: what they add to the rows that see them, one key at a time, then
-            // their values are cleared
-            for (int half_of = 0; half_of < KT; ++half_of) {
-                for (uint32_t left = uni(sbad[turn][1 + half_of]); left != 0; left &= left - 1) {
-                    const int r = half_of * 32 + __ffs((int)left) - 1;
-                    if (!here) continue;
-                    uint32_t w = 0;
-#pragma unroll
-                    for (int i = 0; i < KT * 8; ++i) {
-                        const uint4& x = pw[i / 4];
-                        const uint32_t y = i % 4 == 0 ? x.x : i % 4 == 1 ? x.y : i % 4 == 2 ? x.z : x.w;
-                        w = i == (r >> 4) * 4 + (r & 7) / 2 ? y : w;
-                    }
-                    float weight = __uint_as_float(r & 1 ? w & 0xffff0000u : w << 16);
-                    weight = __shfl(weight, col + 32 * (r >> 3 & 1), 64);
-                    const bool seen = (uint32_t)(j0 + r - range.lo) < (uint32_t)(range.hi - range.lo);
-                    const char* v_at = vs + (r >> 3) * kGroup + (r & 7) * 128 + half * 8;
-                    const int swap = value_swap(r) * 16;
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(v_at + dt / 2 * 1024 + (dt % 2 * 64 ^ swap) + x * 16);
-                            const float f[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                                                __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float y = o[dt][4 * x + e];
-                                o[dt][4 * x + e] = seen ? __builtin_fmaf(weight, f[e], y) : y;
-                            }
-                        }
-                }
-            }
-            __syncthreads();
-            for (int i = tid; i < kKeys * NI * 8; i += kThreads) {
-                const int r = i / (NI * 64) * 8 + i / 8 % 8;  // 64 pieces to a block
-                if (sbad[turn][1 + (r >> 5)] >> (r & 31) & 1)
-                    *reinterpret_cast<uint4*>(smem + kBuf + i * 16) = make_uint4(0, 0, 0, 0);
-            }
-            __syncthreads();
-        }
-        if (here) {
-#pragma unroll
-            for (int i = 0; i < KT * 2; ++i)
-#pragma unroll
-                for (int dt = 0; dt < DT; ++dt) {
-                    const char* at = vs + (v_base ^ (dt % 2 * 64)) + dt / 2 * 1024 + i * 2 * kGroup;
-                    const s16x4_t a0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-                    const s16x4_t a1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 512));
-                    const uint2 b0 = __builtin_bit_cast(uint2, a0), b1 = __builtin_bit_cast(uint2, a1);
-                    o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(make_uint4(b0.x, b0.y, b1.x, b1.y)),
-                                                                    as_bf16x8(pw[i]), o[dt], 0, 0, 0);
-                }
-        }
-        if (more) stage(t + 1, other, next_turn);
-        __syncthreads();
-        turn = next_turn;
+        if (t < n && values_mine) load(p.a.kv.v, p.a.kv.v_scales, now, &v_off, 0, &v_piece, vp, values_to);
     };
-    for (int t = t_from; t < t_to; t += 2) {
-        work(t, smem0, smem1);
-        if (t + 1 >= t_to) break;
-        work(t + 1, smem1, smem0);
+    const auto end = [&](int t, char* keys_to, char* values_to) __attribute__((always_inline)) {
+        if constexpr (kDma) __builtin_amdgcn_s_waitcnt(0x0f70);
+        if (t + 1 < n && keys_mine) {
+            store(kp, keys_to);
+            spoil(next, keys_to);
+        }
+        if (t < n && values_mine) {
+            store(vp, values_to);
+            bool bad = edge(t);
+#pragma unroll
+            for (int g = 0; g < G; ++g) bad |= now[g].bad;
+            if (bad) clean(t, now, values_to);
+        }
+    };
+    // Where waves meet, those that have just staged wait for their loads and
+    // writes first; the others' loads stay on their way, which a plain barrier
+    // would wait for too.
+    const auto meet = [&](bool staged) __attribute__((always_inline)) {
+        asm volatile("" ::: "memory");
+        if (staged) __builtin_amdgcn_s_waitcnt(0);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    // keys0 and values0 have the even tiles.  A wave none of whose rows sees a
+    // key only stages.
+    const bool idle = own.hi == 0;
+    const auto round = [&](int t, char* keys, char* keys_to, char* values, char* values_to) __attribute__((always_inline)) {
+        if (!late) begin(t, keys_to, values_to);
+        if (!idle) products(std::true_type{}, keys, values);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kTurns) {
+            if (late) end(t, keys_to, values_to);
+            meet(late);
+            if (late) begin(t + 1, keys, values);
+        }
+        if (!idle) weights(t);
+        __builtin_amdgcn_sched_barrier(0);
+        if (!late) end(t, keys_to, values_to);
+        if (!late || t + 1 < n) meet(!late);
+    };
+    if (n > 0) {
+        if (late) {
+            begin(0, keys1, values0);
+            meet(false);
+        }
+        int t = 0;
+        for (;;) {
+            round(t, keys0, keys1, values1, values0);
+            if (++t >= n) break;
+            round(t, keys1, keys0, values0, values1);
+            if (++t >= n) break;
+        }
+        // the last tile's sums, whose values have been there since the last round's staging
+        if (!idle) products(std::false_type{}, nullptr, n & 1 ? values0 : values1);
+    }
+
+    // Keys that were cleared above: what they add to the rows that see them, from
+    // the cache itself, one key after another and 32 columns at a time.
+    if (uni(any_odd)) {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+#pragma nounroll
+            for (int at = 0; at < n * kKeys; ++at) {
+                const int t = at / kKeys, j = j_from + at;
+                if (!edge(t) || j < all.lo || j >= all.hi) continue;
+                const int idx = index_of(j >> 3), place = j - idx * p.pg8 * 8;
+                const uint32_t pg = (uint32_t)uni(table[idx]);
+                if (pg >= p.pages) continue;
+                const uint64_t to = ((uint64_t)pg * p.page16 + (uint64_t)(uint32_t)place * p.token16 +
+                                     (uint64_t)(uint32_t)head * p.head16) * 16;
+                const uint64_t sc = (uint64_t)pg * p.page_scales + ((uint32_t)head * p.head_scales + (uint32_t)place);
+                const char* k = static_cast<const char*>(p.a.kv.k) + to;
+                const char* v = static_cast<const char*>(p.a.kv.v) + to;
+                float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (lane * 4 < p.dim) four_of<kHeld>(v, p.a.kv.v_scales + sc, scale_group, lane * 4, f);
+                if (!__ballot((f[0] * 0.0f + f[1] * 0.0f) + (f[2] * 0.0f + f[3] * 0.0f) != 0.0f)) continue;
+                float x = 0.0f;
+#pragma nounroll
+                for (int d = half * 4; d < p.dim; d += 8) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(q_row + d);
+                    four_of<kHeld>(k, p.a.kv.k_scales + sc, scale_group, d, f);
+                    x = __builtin_fmaf(f[0], __uint_as_float((w.x ^ p.flip) << 16), x);
+                    x = __builtin_fmaf(f[1], __uint_as_float((w.x ^ p.flip) & 0xffff0000u), x);
+                    x = __builtin_fmaf(f[2], __uint_as_float((w.y ^ p.flip) << 16), x);
+                    x = __builtin_fmaf(f[3], __uint_as_float((w.y ^ p.flip) & 0xffff0000u), x);
+                }
+                x += __shfl_xor(x, 32, 64);
+                if constexpr (kForm) {
+                    if (p.a.cap > 0.0f)
+                        cap_scores<1>(&x, p.times);
+                    else
+                        x *= p.times;
+                    x = __builtin_fmaf(-slope, __builtin_fabsf((float)(range.pos - j)), x);
+                }
+                const float w = __builtin_amdgcn_exp2f(careful ? (x - (m == kNegInf ? 0.0f : m)) * c : __builtin_fmaf(x, c, -mc));
+                const bool seen = j >= range.lo && j < range.hi;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int d = dt * 32 + b * 8 + half * 4;
+                    if (d < p.dim) four_of<kHeld>(v, p.a.kv.v_scales + sc, scale_group, d, f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = o[dt][4 * b + e];
+                        o[dt][4 * b + e] = seen ? __builtin_fmaf(w, f[e], y) : y;
+                    }
+                }
+            }
+        }
     }
 
     l += __shfl_xor(l, 32, 64);
@@ -590,7 +779,7 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
         float* part = place(p, from_end, head, split);
         const int r = wave * 32 + col;
         if (half == 0) part[2 * r] = m, part[2 * r + 1] = l * fix;
-        float* to = part + 2 * kRows + r * p.dim + half * 4;
+        float* to = part + 2 * p.rows + r * p.dim + half * 4;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -619,14 +808,12 @@ __global__ __launch_bounds__(kThreads, kW <= 192 ? 2 : 1) void prompt_kernel(con
 
 template <int kW, int kHeld, bool kForm>
 void go_width(const Args& p, unsigned groups, hipStream_t s) {
-    const dim3 grid(groups), block(kThreads);
-    if constexpr (kHeld == BD_BF16 && kW % 64 == 0) {  // whole blocks only
-        if (p.dim == kW) {
-            hipLaunchKernelGGL((prompt_kernel<kW, kHeld, kForm, true>), grid, block, 0, s, p);
-            return;
-        }
-    }
-    hipLaunchKernelGGL((prompt_kernel<kW, kHeld, kForm, false>), grid, block, 0, s, p);
+    constexpr int kWaves = waves_of(kW);
+    const dim3 grid(groups), block(kWaves * 64);
+    if (p.dim == kW && p.token16 < (1u << 24))
+        hipLaunchKernelGGL((prompt_kernel<kW, kHeld, kForm, true, kWaves>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((prompt_kernel<kW, kHeld, kForm, false, kWaves>), grid, block, 0, s, p);
 }
 template <int kHeld, bool kForm>
 void go(const Args& p, unsigned groups, hipStream_t s) {

@@ -112,37 +112,47 @@ struct PromptArgs {
 };
 hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream);
 
-// Scores capped: cap tanh(x / cap).  tanh y = 1 - 2 / (1 + e^(2 y)) loses what is
-// small against 1, so where all of the wave's |y| are below 1/4 its Taylor series
-// up to y^9 takes their place (the next term is below 2^-26 of the result), which
-// needs neither exponential nor reciprocal and is the usual case: scores are small
-// against a cap.  Where some are larger, each lane takes what suits it.
+// Capped scores in units of their cap: x = tanh(times x), times = scale / cap.
+// tanh y = 1 - 2 / (1 + e^(2 y)) loses what is small against 1, and costs two
+// quarter-rate operations.  Where |y| <= 1/2 it is y + y^3 g(y^2), g of degree 3
+// fitted to the least relative error of the whole (2^-25.7); that is the usual
+// case, as scores are small against a cap, and the only one where all of a
+// wave's scores are.  Where some are larger each lane takes what suits it.
 template <int kN>
-__device__ __forceinline__ void cap_scores(float* x, float cap) {
-    const float inv = 1.0f / cap;
+__device__ __forceinline__ void cap_scores(float* x, float times) {
     float big = 0.0f;
-    float y[kN], small[kN];
+    float small[kN];
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
-        y[j] = x[j] * inv;
-        big = fmaxf(big, __builtin_fabsf(y[j]));
-        const float q = y[j] * y[j];
-        float a = __builtin_fmaf(q, 2.1869489e-02f, -5.3968254e-02f);
-        a = __builtin_fmaf(a, q, 1.3333333e-01f);
-        a = __builtin_fmaf(a, q, -3.3333333e-01f);
-        small[j] = __builtin_fmaf(a * q, y[j], y[j]);
+        const float y = x[j] = x[j] * times;
+        big = fmaxf(big, __builtin_fabsf(y));
+        const float q = y * y;
+        float g = __builtin_fmaf(q, 0.017257417f, -0.05305313f);
+        g = __builtin_fmaf(g, q, 0.13325989f);
+        g = __builtin_fmaf(g, q, -0.3333315f);
+        small[j] = __builtin_fmaf(g, q * y, y);
     }
-    if (__ballot(big > 0.25f)) {
+    if (__ballot(!(big <= 0.5f))) {
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-            const float e = __builtin_amdgcn_exp2f(y[j] * 2.8853900817779268f);  // 2 log2(e)
+            const float e = __builtin_amdgcn_exp2f(x[j] * 2.8853900817779268f);  // 2 log2(e)
             const float t = __builtin_fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + e), 1.0f);
-            x[j] = cap * (__builtin_fabsf(y[j]) <= 0.25f ? small[j] : t);
+            x[j] = __builtin_fabsf(x[j]) <= 0.5f ? small[j] : t;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < kN; ++j) x[j] = cap * small[j];
+        for (int j = 0; j < kN; ++j) x[j] = small[j];
     }
+}
+// What formed scores are kept in: units of the cap, or of 1 without one.  `times`
+// makes them of products (of the queries with scale's sign).
+struct Form {
+    float unit, times;
+};
+inline Form form_of(float scale, float cap) {
+    const float size = scale < 0.0f ? -scale : scale, unit = cap > 0.0f ? cap : 1.0f;
+    // an infinite product times a scale other than 0 stays infinite
+    return Form{unit, size > 0.0f && size / unit == 0.0f ? 0x1p-149f : size / unit};
 }
 
 // ---------------------------------------------------------------------------
