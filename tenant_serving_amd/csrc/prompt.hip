@@ -52,14 +52,15 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
 
 // Tiles at most: whole ones of all rows, and one that is not for each sequence.
 int64_t tiles_at_most(int64_t T, int64_t B, int64_t group, int rows) { return T * group / rows + B; }
-int rows_of(int64_t D) { return 32 * waves_of(width_of((int)D)); }
+int rows_of(int64_t D, int held) { return 32 * waves_of(width_of((int)D), held); }
 
-// Workgroups that share a tile's keys: as many as make two workgroups for each
-// CU, while each has 256 keys of a full table, or 1024 where one workgroup per CU
-// is there already (us with 256 / 512 / 1024: 3 sequences of 5 tokens behind 1000
-// 21 / 32 / 31, 64 tokens behind 2048 25 / 29 / 40; 512 tokens 29 / 23 / 23).
-int64_t splits_of(int64_t tiles, int64_t heads, int64_t capacity, int rows) {
-    const int64_t groups = tiles * heads, wanted = 256;
+// Workgroups that share a tile's keys: as many as make two of 4 waves for each
+// CU, or one of 8 or of 256 columns, while each has 256 keys of a full table, or
+// 1024 where one workgroup per CU is there already (us with 256 / 512 / 1024,
+// bf16: 3 sequences of 5 tokens behind 1000 21 / 32 / 31, 64 tokens behind 2048
+// 25 / 29 / 40; 512 tokens 29 / 23 / 23).
+int64_t splits_of(int64_t tiles, int64_t heads, int64_t capacity, int64_t D, int rows) {
+    const int64_t groups = tiles * heads, wanted = rows == 128 && D <= 192 ? 512 : 256;
     int64_t n = (wanted + groups - 1) / groups;
     const int64_t most = capacity / (groups < 256 ? 256 : 1024);
     n = n < most ? n : most;
@@ -68,10 +69,16 @@ int64_t splits_of(int64_t tiles, int64_t heads, int64_t capacity, int rows) {
 
 }  // namespace
 
+// Enough for every type of cache.
 size_t prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t capacity) {
-    const int rows = rows_of(D);
-    const int64_t tiles = tiles_at_most(T, B, Hq / H, rows), splits = splits_of(tiles, H, capacity, rows);
-    return splits == 1 ? 0 : (size_t)(tiles * H * splits * rows * (D + 2)) * sizeof(float);
+    size_t bytes = 0;
+    for (const int held : {BD_BF16, BD_E4M3}) {
+        const int rows = rows_of(D, held);
+        const int64_t tiles = tiles_at_most(T, B, Hq / H, rows), splits = splits_of(tiles, H, capacity, D, rows);
+        const size_t n = splits == 1 ? 0 : (size_t)(tiles * H * splits * rows * (D + 2)) * sizeof(float);
+        bytes = n > bytes ? n : bytes;
+    }
+    return bytes;
 }
 
 hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream) {
@@ -82,10 +89,10 @@ hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream) {
     const float scale = __builtin_fabsf(a.scale);
     const Form form = form_of(a.scale, a.cap);
     const int pg8 = a.kv.page_size / 8;
-    const int rows = rows_of(D);
+    const int rows = rows_of(D, held);
     const int64_t tiles = tiles_at_most(a.T, a.B, a.Hq / H, rows);
     const Args p{a, D, H, a.Hq / H, rows, pg8, pg8 == 1 ? 0 : (int32_t)(uint32_t)((uint64_t(1) << 32) / pg8 + 1),
-                 a.kv.page_size * a.max_pages, (int32_t)splits_of(tiles, H, (int64_t)a.kv.page_size * a.max_pages, rows),
+                 a.kv.page_size * a.max_pages, (int32_t)splits_of(tiles, H, (int64_t)a.kv.page_size * a.max_pages, D, rows),
                  (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride),
                  unit16(a.kv.token_stride), H * head_scales, head_scales,
                  __builtin_fmaxf((formed ? form.unit : scale) * 1.4426950408889634f, kLeastC),

@@ -5,13 +5,17 @@
 //
 // with s_j = q.k_j and c = scale log2(e), or formed scores and c = log2(e), and
 // m a running maximum of s_j.  Bound by the matrix units, where the prompt is
-// long, and by the exponentials between the two products.
+// long, and by the exponentials between the two products: a tile's products take
+// a wave 32 cycles for each of KT (KS + 2 DT) instructions, 1024 at 128 columns,
+// and its weights about 1400, which the other waves' products hide for the most
+// part.  8192 tokens, 64 query heads of 128 columns over 8, bf16, causal: 1055 us,
+// 1040 TFLOP/s of what is not masked (a large product of matrices reaches 1170).
 //
 // Layout.  The rows of a tile are (token, query head) pairs of one sequence and
 // one key-value head, tokens first: the heads that share keys and values share a
 // tile's loads.  A wave takes 32 rows, a workgroup kWaves * 32, and goes over the
-// keys kKeys at a time, which it stages in LDS as bf16, codes converted on the
-// way, two buffers in turn.
+// keys kKeys at a time, which it stages in LDS as bf16, two buffers in turn:
+// bf16 rows by loads that write there, codes by way of registers, converted.
 //   scores  S^T [keys, rows] = K Q^T by v_mfma_f32_32x32x16_bf16, queries in
 //           registers.  The A operand's row m is key 16 (m / 16) + 8 (m / 4 % 2)
 //           + 4 (m / 8 % 2) + m % 4, which leaves a lane with the scores of 8
@@ -32,9 +36,9 @@
 // of a key tile nothing is masked.  Elsewhere a row's scores outside its range
 // are -infinity, whatever the keys hold.  Values there must not reach it either,
 // and 0 times infinity or NaN would: so tiles that some row of the workgroup sees
-// in part are looked through for values that are not finite as they are staged,
-// and the keys that hold some are taken apart from the product, by a sum that
-// leaves out the rows that do not see them.
+// in part are looked through for values that are not finite as they are staged.
+// Such a key's values are cleared, and added at the end to the rows that see it,
+// from the cache itself.
 //
 // Split.  Where the rows are few a tile's keys are shared out over several
 // workgroups, whose fp32 partial results a second kernel adds in order.
@@ -56,8 +60,16 @@ constexpr int width_of(int dim) { return dim <= 64 ? 64 : dim <= 96 ? 96 : dim <
 // Keys of a tile.
 constexpr int keys_of(int width) { return width <= 128 ? 64 : 32; }
 
-// Waves of a workgroup: 8, or 4 where two to a SIMD would not have the registers.
-constexpr int waves_of(int width) { return width <= 192 ? 8 : 4; }
+// Waves of a workgroup: 8 that take turns where codes are converted on the way,
+// since a tile of 256 rows has half the conversions for each of them, else two
+// workgroups of 4 to a CU, which drift into turns by themselves (a whole prompt
+// of 8192 tokens, 64 query heads of 128 columns over 8, with 4 and with 8: bf16
+// 1054 and 1081 us, e4m3 1248 and 1158, 4-bit codes capped 1836 and 1717; 64
+// columns 724 and 788, with e4m3 codes 779 and 782; 192 columns 1460 and 1557,
+// with codes 1647 and 1561; a chunk of 512 tokens on 32768 4-bit ones 656 and
+// 574; 15 tokens on 48000 bf16 ones 48 and 63).  At 256 columns a workgroup of 4
+// takes a CU's registers.
+constexpr int waves_of(int width, int held) { return held == BD_BF16 || width == 64 || width == 256 ? 4 : 8; }
 
 struct Args {
     PromptArgs a;
@@ -808,7 +820,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 8 || kW <= 192 ? 2 : 1) void
 
 template <int kW, int kHeld, bool kForm>
 void go_width(const Args& p, unsigned groups, hipStream_t s) {
-    constexpr int kWaves = waves_of(kW);
+    constexpr int kWaves = waves_of(kW, kHeld);
     const dim3 grid(groups), block(kWaves * 64);
     if (p.dim == kW && p.token16 < (1u << 24))
         hipLaunchKernelGGL((prompt_kernel<kW, kHeld, kForm, true, kWaves>), grid, block, 0, s, p);
