@@ -62,9 +62,11 @@ constexpr int kUnit = kWaves * kTile;      // tokens of a unit
 // are the better ones: 80 in bf16 to 128 (lanes of 8 columns, not 4 and 2; 64
 // sequences of up to 2048, 32 heads, 148 there, 181 at 96), 144 to 176 in e4m3
 // to 256 (of 16 columns, not 8 and 4; 176: 177 there, 206 at 192).
-// e2m1 rows, which are a multiple of 32 wide, go to the next width.
+// e2m1 rows, which are a multiple of 32 wide, go to the next width, but for 96,
+// which goes to 128 (lanes of 8 columns, not 4 and 2, whose loads of 2 bytes and 1
+// took 293 us where 128 takes 128).
 constexpr int width_of(int dim, int held) {
-    return dim <= 64 ? 64 : dim == 96 || (dim < 96 && held == BD_E4M3) ? 96 : dim <= 128 ? 128 :
+    return dim <= 64 ? 64 : (dim == 96 && held != BD_E2M1) || (dim < 96 && held == BD_E4M3) ? 96 : dim <= 128 ? 128 :
            dim == 192 || (dim < 192 && held != BD_E4M3) ? 192 : 256;
 }
 // Workgroups at most: what 256 CUs hold of them by their registers and LDS, so
@@ -73,10 +75,13 @@ constexpr int width_of(int dim, int held) {
 // 768 of them for 512 places, 64 of 8192 tokens in e4m3 173 -> 230 us) and at
 // 192 (31 of up to 1013 tokens, 32 heads, e4m3: one 61.2, two 48.4).  At 256
 // the registers of two spill but for e4m3 with bf16 queries (in bf16, 8 of 8192
-// tokens, two would take 86 -> 107).
+// tokens, two would take 86 -> 107).  Of 4-bit codes with bf16 queries three up
+// to 128, whose loads in flight are small (64 sequences of up to 16381 tokens, 64
+// heads of 128 over 8, 132 -> 123 us, with a cap 141 -> 134; one of 131071 35.0 ->
+// 35.4).
 constexpr int kCUs = 256;
 constexpr int per_cu(int width, bool split_q, int held) {
-    return width <= 64 ? 3 : width <= 192 || (held != BD_BF16 && !split_q) ? 2 : 1;
+    return width <= 64 || (width <= 128 && held == BD_E2M1 && !split_q) ? 3 : width <= 192 || (held != BD_BF16 && !split_q) ? 2 : 1;
 }
 // What a row costs beside its units, in units.  Without it the workgroups that
 // get many short rows come last: 64 sequences of up to 16381 tokens in e4m3
@@ -374,16 +379,25 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
     constexpr int VD = (DV * kBits + 31) / 32;  // dwords of a value row per lane
     constexpr int VB1 = DV1 * kBits / 8, VB2 = DV2 * kBits / 8;
     constexpr int kPad = kDC + 4;
-    // Two of each, used in turn by the rows: one barrier a row.  Past head_dim
-    // 128 one, where a CU then holds two workgroups instead of one; at 256, and
-    // for fp32 queries, with the queries in LDS instead of registers.
-    constexpr bool kOneTurn = kDC > 128 && per_cu(kDC, kSplitQ, kHeld) == 2;
-    constexpr bool kTight = kOneTurn && (kDC == 256 || kSplitQ);
+    // Two of each, used in turn by the rows: one barrier a row.  One where a CU
+    // then holds a workgroup more: past head_dim 128 two instead of one (at 256,
+    // and for fp32 queries, with the queries in LDS instead of registers), at 128
+    // three instead of two.
+    constexpr bool kOneTurn = kDC > 64 && per_cu(kDC, kSplitQ, kHeld) > (kDC > 128 ? 1 : 2);
+    constexpr bool kTight = kOneTurn && kDC > 128 && (kDC == 256 || kSplitQ);
     constexpr int QT = kSplitQ ? 3 : 1;
     constexpr int kTurns = kOneTurn ? 1 : 2;
     __shared__ float so[kTurns][kWaves][16][kPad];
     __shared__ float sm[kTurns][kWaves][16], sl[kTurns][kWaves][16];
     __shared__ uint4 sq[kTight ? QT : 1][kTight ? NS : 1][64];
+    // What a masked token's values are is settled after the weights where that
+    // lets the values come later: e2m1 without formed scores 136 -> 129 us, with
+    // a cap 149 -> 152 (64 sequences of up to 16381 tokens, 64 heads of 128 over 8).
+    constexpr bool kLate = kE2m1 && !kForm;
+    // Whether a tile's next loads are sent in any case, see below: where there are
+    // scales to wait for, or more than 128 columns (in bf16 at 256 768 -> 731 us,
+    // but 31 sequences of 1024 tokens of 128 32 -> 33).
+    constexpr bool kAlways = kHeld != BD_BF16 || kDC > 128;
     constexpr int NR = kTight ? (NS + kWaves - 1) / kWaves : NS;  // k-steps whose queries a wave loads
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
@@ -445,14 +459,21 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
     Piece now = piece_at(b0, seq0, row0, into > 0 ? into : 0, at);
     bool first_piece = true;
 
-    // A tile's loads, in flight while the tile before it is worked on: the
-    // page numbers a tile earlier, the keys as soon as the scores are done
-    // with the registers, the values after the sums.  A row's first tile and
-    // its queries are loaded while the row before it is summed up.
+    // A tile's loads, in flight while the tile before it is worked on: the keys
+    // as soon as the scores are done with the registers, the values after the
+    // sums, the page numbers just before the keys of the tile before.  So none is
+    // waited for by way of another that was sent later.  Behind a piece's last
+    // tile page 0 is loaded, whose lines all waves share (kAlways): without a
+    // branch the compiler knows what is on its way at a tile's start, and does
+    // not wait for all of it.  Scale bytes are made scales where they are used.
+    // (64 sequences of up to 16381 tokens, 64 heads of 128 over 8, e2m1: 155 ->
+    // 129 us; 16 of up to 8191, 32 heads of 64, e4m3, a bias by distance: 72 -> 63.)
+    // A row's first tile and its queries are loaded while the row before it is
+    // summed up.
     Dwords<4> kk[2][KL];  // of the odd one, two
     Dwords<VD> vv[8];
     constexpr int KG = kE2m1 ? KL : 1, VG = kE2m1 && DV2 > 0 ? 2 : 1;  // scales of a lane's part of a row
-    float ks[2][KG];
+    uint32_t ks[2][KG];
     uint2 vs[VG];
     float slope = 0.0f;  // of the lane's head
     Raw8<kSplitQ> raw[NR];
@@ -476,8 +497,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
         return Groups{look_up(p.s, table, group_of(x, t, i16 >> 2)), look_up(p.s, table, group_of(x, t, g))};
     };
     const uint64_t token_bytes = (uint64_t)p.token16 * 16;
-    const auto load_keys = [&](const Piece& x, Group at_page) {
-        const Where wh = locate(p, at_page, x.head);
+    const auto load_keys = [&](const Where& wh) {
         bad |= wh.bad;
         // one address, stepped by uniform strides, so that no per-row address
         // stays in registers
@@ -502,7 +522,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                     }
                     // the lane's columns of a load lie in one group
                     const int group = kFull || d < p.s.dim ? d / kGroup4 : 0;
-                    ks[h][s] = scale_of(p.a.kv.k_scales[wh.sc + (uint32_t)group * (uint32_t)p.s.page_size + (i16 & 3) + 4 * h]);
+                    ks[h][s] = p.a.kv.k_scales[wh.sc + (uint32_t)group * (uint32_t)p.s.page_size + (i16 & 3) + 4 * h];
                     continue;
                 }
                 const char* k = static_cast<const char*>(p.a.kv.k) + at + s * 64;
@@ -516,11 +536,10 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                 }
             }
             at += 4 * token_bytes;
-            if (kE4m3) ks[h][0] = scale_of(p.a.kv.k_scales[wh.sc + (i16 & 3) + 4 * h]);
+            if (kE4m3) ks[h][0] = p.a.kv.k_scales[wh.sc + (i16 & 3) + 4 * h];
         }
     };
-    const auto load_values = [&](const Piece& x, Group at_page) {
-        const Where wh = locate(p, at_page, x.head);
+    const auto load_values = [&](const Where& wh) {
         bad |= wh.bad;
         // lanes behind head_dim hold some other columns, which are not used
         uint64_t at = opaque(wh.at + (kFull || i16 * DV1 < p.s.dim ? i16 * VB1 : 0));
@@ -586,19 +605,29 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
 #pragma unroll
         for (int j = 0; j < 8; ++j) clear(vv[j]);
 #pragma unroll
-        for (int i = 0; i < KG; ++i) ks[0][i] = ks[1][i] = 0.0f;
+        for (int i = 0; i < KG; ++i) ks[0][i] = ks[1][i] = 0;
 #pragma unroll
         for (int i = 0; i < VG; ++i) vs[i] = make_uint2(0, 0);
     };
 
     Groups pages{};  // of the tile after the one in flight
+    // The page numbers of the tile at t and the keys of the one before it, or of
+    // page 0; its values are at what comes back.
+    const auto load_next = [&](const Piece& x, int t, bool more) {
+        const Where k = locate(p, more ? pages.k : Group{0, 0}, x.head);
+        const Where v = locate(p, more ? pages.v : Group{0, 0}, x.head);
+        __builtin_amdgcn_sched_barrier(0);  // no copies of numbers that are on their way
+        pages = load_pages(x, t);           // past the end: the last group's page
+        __builtin_amdgcn_sched_barrier(0);
+        load_keys(k);
+        __builtin_amdgcn_sched_barrier(0);
+        return v;
+    };
     drop();
     load_queries(now);
     if (now.t0 < now.stop) {
         pages = load_pages(now, now.t0);
-        load_keys(now, pages.k);
-        load_values(now, pages.v);
-        pages = load_pages(now, now.t0 + kUnit);  // past the end: the last group's page
+        load_values(load_next(now, now.t0 + kUnit, true));
     }
 
     for (int turn = 0;; turn ^= kTurns - 1) {
@@ -661,11 +690,12 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                     uint4 kb;
                     if constexpr (kE4m3) {
                         const uint32_t c0 = kk[h][s / 2].d[2 * (s & 1)], c1 = kk[h][s / 2].d[2 * (s & 1) + 1];
-                        kb = make_uint4(e4m3x2_to_bf16<false>(c0, ks[h][0]), e4m3x2_to_bf16<true>(c0, ks[h][0]),
-                                        e4m3x2_to_bf16<false>(c1, ks[h][0]), e4m3x2_to_bf16<true>(c1, ks[h][0]));
+                        const float scale = scale_of(ks[h][0]);
+                        kb = make_uint4(e4m3x2_to_bf16<false>(c0, scale), e4m3x2_to_bf16<true>(c0, scale),
+                                        e4m3x2_to_bf16<false>(c1, scale), e4m3x2_to_bf16<true>(c1, scale));
                     } else if constexpr (kE2m1) {
                         const int l = s < NS / 4 * 4 ? s / 4 : s < NS / 4 * 4 + k_steps(NS / 4) ? NS / 4 : NS / 4 + 1;
-                        kb = e2m1x8_to_bf16(kk[h][l].d[s - k_first(l)], ks[h][l]);
+                        kb = e2m1x8_to_bf16(kk[h][l].d[s - k_first(l)], scale_of(ks[h][l]));
                     } else {
                         const Dwords<4>& r = kk[h][s];
                         kb = make_uint4(r.d[0], r.d[1], r.d[2], r.d[3]);
@@ -684,24 +714,28 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
 #pragma unroll
                 for (int r = 0; r < 4; ++r) sc[4 * h + r] = x[r];
             }
-            if (more) load_keys(now, pages.k);
+            Where values_at{};
+            if (kAlways || more) values_at = load_next(now, t + 2 * kUnit, more);
             if constexpr (kForm) form_scores(p, sc, times, bias, len - 1 - (t + 8 * g));
             const bool tail = t + kTile > tokens || (kForm && t < first);
+            const auto clear_value = [&](int j, bool out) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < VD; ++i) vv[j].d[i] = out ? 0u : vv[j].d[i];
+                if constexpr (kHeld != BD_BF16) {  // any byte may stand there: 2^0
+#pragma unroll
+                    for (int i = 0; i < VG; ++i) {
+                        uint32_t& sw = j < 4 ? vs[i].x : vs[i].y;
+                        const uint32_t field = 0xffu << (8 * (j & 3));
+                        sw = out ? (sw & ~field) | (127u << (8 * (j & 3))) : sw;
+                    }
+                }
+            };
             if (tail) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const bool out = t + 8 * g + j >= tokens || (kForm && t + 8 * g + j < first);
                     sc[j] = out ? kNegInf : sc[j];
-#pragma unroll
-                    for (int i = 0; i < VD; ++i) vv[j].d[i] = out ? 0u : vv[j].d[i];
-                    if constexpr (kHeld != BD_BF16) {  // any byte may stand there: 2^0
-#pragma unroll
-                        for (int i = 0; i < VG; ++i) {
-                            uint32_t& sw = j < 4 ? vs[i].x : vs[i].y;
-                            const uint32_t field = 0xffu << (8 * (j & 3));
-                            sw = out ? (sw & ~field) | (127u << (8 * (j & 3))) : sw;
-                        }
-                    }
+                    if constexpr (!kLate) clear_value(j, out);
                 }
             }
 
@@ -733,6 +767,11 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
             for (int j = 0; j < 8; ++j) back[j] = pr[j] - back[j];
             uint4 pl = narrow_bf16x8(back);
             if (pass) pl = ph;
+
+            if (kLate && tail) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) clear_value(j, t + 8 * g + j >= tokens);
+            }
 
             // value rows as bf16 pairs of columns, then pairs of tokens
             float vscale[VG][8];
@@ -769,10 +808,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                 }
                 if (kTight) __builtin_amdgcn_sched_barrier(0);  // or the pairs of all columns wait in registers
             }
-            if (more) {
-                load_values(now, pages.v);
-                pages = load_pages(now, t + 2 * kUnit);
-            }
+            if (kAlways || more) load_values(values_at);
         }
 
         // Further terms break on infinities: they are of either sign or zero,
@@ -806,9 +842,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                 }
                 pass = 1;
                 pages = load_pages(now, t0);
-                load_keys(now, pages.k);
-                load_values(now, pages.v);
-                pages = load_pages(now, t0 + kUnit);
+                load_values(load_next(now, t0 + kUnit, true));
                 goto again;
             }
         } else {
@@ -831,9 +865,8 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
         bad = false;
         if (!last) load_queries(next);
         if (!last && next.t0 < next.stop) {
-            load_keys(next, next_pages.k);
-            load_values(next, next_pages.v);
-            pages = load_pages(next, next.t0 + kUnit);
+            pages = next_pages;
+            load_values(load_next(next, next.t0 + kUnit, true));
         } else {  // nothing is kept in these registers from here
             drop();
         }
@@ -919,8 +952,7 @@ void go_queries(const Args& p, bool q_fp32, hipStream_t s) {
 // width_of goes elsewhere.
 template <int kDC, int kHeld, bool kForm>
 void go_width(const Args& p, bool q_fp32, hipStream_t s) {
-    constexpr bool kPart = !(kDC == 96 && kHeld != BD_E4M3) && !(kDC == 128 && kHeld == BD_E2M1) &&
-                           !(kDC == 192 && kHeld == BD_E4M3);
+    constexpr bool kPart = !(kDC == 96 && kHeld != BD_E4M3) && !(kDC == 192 && kHeld == BD_E4M3);
     if (p.s.dim == kDC)
         go_queries<kDC, true, kHeld, kForm>(p, q_fp32, s);
     else if constexpr (kPart)
@@ -930,7 +962,9 @@ template <int kHeld, bool kForm>
 void go_held(const Args& p, bool q_fp32, hipStream_t s) {
     switch (width_of(p.s.dim, kHeld)) {
         case 64: go_width<64, kHeld, kForm>(p, q_fp32, s); break;
-        case 96: go_width<96, kHeld, kForm>(p, q_fp32, s); break;
+        case 96:
+            if constexpr (kHeld != BD_E2M1) go_width<96, kHeld, kForm>(p, q_fp32, s);
+            break;
         case 128: go_width<128, kHeld, kForm>(p, q_fp32, s); break;
         case 192: go_width<192, kHeld, kForm>(p, q_fp32, s); break;
         default: go_width<256, kHeld, kForm>(p, q_fp32, s);
