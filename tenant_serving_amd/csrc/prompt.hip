@@ -54,17 +54,30 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
 int64_t tiles_at_most(int64_t T, int64_t B, int64_t group, int rows) { return T * group / rows + B; }
 int rows_of(int64_t D, int held) { return 32 * waves_of(width_of((int)D), held); }
 
-// Workgroups that share a tile's keys: as many as make two of 4 waves for each
-// CU, or one of 8 or of 256 columns, while each has 256 keys of a full table, or
-// 1024 where one workgroup per CU is there already (us with 256 / 512 / 1024,
-// bf16: 3 sequences of 5 tokens behind 1000 21 / 32 / 31, 64 tokens behind 2048
-// 25 / 29 / 40; 512 tokens 29 / 23 / 23).
-int64_t splits_of(int64_t tiles, int64_t heads, int64_t capacity, int64_t D, int rows) {
-    const int64_t groups = tiles * heads, wanted = rows == 128 && D <= 192 ? 512 : 256;
-    int64_t n = (wanted + groups - 1) / groups;
-    const int64_t most = capacity / (groups < 256 ? 256 : 1024);
-    n = n < most ? n : most;
-    return n < 1 ? 1 : n;
+// Workgroups that share a tile's keys.  `places` of them run at a time: two of 4
+// waves on each CU, or one of 8 or of 256 columns.  A split costs what its keys
+// do, a start and an end of about 256 keys, and where there are several the
+// partial results (350 more, and 250 for the join's launch); what is least is
+// taken of 1 and the numbers that fill 1 to 4 rounds of places, while each has
+// 256 keys of a full table.  The sequences are taken to be alike, as the host
+// does not know them.  (us with 1 workgroup / those that fill a round / one more
+// for each tile, bf16, 64 heads of 128 over 8: 3 sequences of 5 tokens behind
+// 16000 - / 41 / 48, 32 of them 331 / 232 / -; 300 tokens behind 8192 - / 101 /
+// 128; 512 tokens of their own 23 / 29 / -.)
+int64_t splits_of(int64_t T, int64_t B, int64_t group, int64_t heads, int64_t capacity, int64_t D, int rows) {
+    if (T < 1 || B < 1) return 1;
+    const int64_t groups = B * (((T + B - 1) / B * group + rows - 1) / rows) * heads;
+    const int64_t places = rows == 128 && D <= 192 ? 512 : 256;
+    const int64_t most = capacity / 256;
+    int64_t best = 1, least = (groups + places - 1) / places * (capacity + 256);
+    for (int r = 1; r <= 4; ++r) {
+        int64_t n = r * places / groups;
+        n = n < most ? n : most;
+        if (n < 2) continue;
+        const int64_t cost = (groups * n + places - 1) / places * (capacity / n + 256 + 350) + 250;
+        if (cost < least) best = n, least = cost;
+    }
+    return best;
 }
 
 }  // namespace
@@ -74,7 +87,7 @@ size_t prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64
     size_t bytes = 0;
     for (const int held : {BD_BF16, BD_E4M3}) {
         const int rows = rows_of(D, held);
-        const int64_t tiles = tiles_at_most(T, B, Hq / H, rows), splits = splits_of(tiles, H, capacity, D, rows);
+        const int64_t tiles = tiles_at_most(T, B, Hq / H, rows), splits = splits_of(T, B, Hq / H, H, capacity, D, rows);
         const size_t n = splits == 1 ? 0 : (size_t)(tiles * H * splits * rows * (D + 2)) * sizeof(float);
         bytes = n > bytes ? n : bytes;
     }
@@ -92,7 +105,7 @@ hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream) {
     const int rows = rows_of(D, held);
     const int64_t tiles = tiles_at_most(a.T, a.B, a.Hq / H, rows);
     const Args p{a, D, H, a.Hq / H, rows, pg8, pg8 == 1 ? 0 : (int32_t)(uint32_t)((uint64_t(1) << 32) / pg8 + 1),
-                 a.kv.page_size * a.max_pages, (int32_t)splits_of(tiles, H, (int64_t)a.kv.page_size * a.max_pages, D, rows),
+                 a.kv.page_size * a.max_pages, (int32_t)splits_of(a.T, a.B, a.Hq / H, H, (int64_t)a.kv.page_size * a.max_pages, D, rows),
                  (uint32_t)a.kv.num_pages, unit16(a.kv.page_stride), unit16(a.kv.head_stride),
                  unit16(a.kv.token_stride), H * head_scales, head_scales,
                  __builtin_fmaxf((formed ? form.unit : scale) * 1.4426950408889634f, kLeastC),
