@@ -394,10 +394,13 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
     // lets the values come later: e2m1 without formed scores 136 -> 129 us, with
     // a cap 149 -> 152 (64 sequences of up to 16381 tokens, 64 heads of 128 over 8).
     constexpr bool kLate = kE2m1 && !kForm;
-    // Whether a tile's next loads are sent in any case, see below: where there are
-    // scales to wait for, or more than 128 columns (in bf16 at 256 768 -> 731 us,
-    // but 31 sequences of 1024 tokens of 128 32 -> 33).
-    constexpr bool kAlways = kHeld != BD_BF16 || kDC > 128;
+    // Whether a tile's next loads are sent in any case, see below.  Not where that
+    // is more than it gives: in bf16 up to 128 columns, where no scales are waited
+    // for (at 256 768 -> 731 us, but 31 sequences of 1024 tokens of 128 32 -> 33),
+    // and in e4m3 at 64 without formed scores (31 of up to 1013, 32 heads, 20.9 ->
+    // 21.9; with a bias by distance 16 of up to 8191 67.7 -> 65.2; at 128 64 of up
+    // to 16381 184 -> 182).
+    constexpr bool kAlways = kE2m1 || kDC > 128 || (kE4m3 && (kForm || kDC > 64));
     constexpr int NR = kTight ? (NS + kWaves - 1) / kWaves : NS;  // k-steps whose queries a wave loads
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
@@ -948,8 +951,8 @@ void go_queries(const Args& p, bool q_fp32, hipStream_t s) {
     else
         hipLaunchKernelGGL((attend_kernel<kDC, kFull, kHeld, false, kForm>), grid, block, 0, s, p);
 }
-// The kernels that some head_dim has: below 96 (bf16), 128 (e2m1) and 192 (e4m3)
-// width_of goes elsewhere.
+// The kernels that some head_dim has: below 96 (bf16) and 192 (e4m3) width_of goes
+// elsewhere, and e2m1 has none of 96.
 template <int kDC, int kHeld, bool kForm>
 void go_width(const Args& p, bool q_fp32, hipStream_t s) {
     constexpr bool kPart = !(kDC == 96 && kHeld != BD_E4M3) && !(kDC == 192 && kHeld == BD_E4M3);
