@@ -129,8 +129,8 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     return s;
 }
 
-size_t workspace_of(const Shape& s) {
-    return s.whole ? 0 : (size_t)s.crosses * sizeof(Cross) + (size_t)s.groups * 2 * 16 * (s.dim + 2) * sizeof(float);
+size_t workspace_of(const Shape& s, int32_t crosses) {
+    return s.whole ? 0 : (size_t)crosses * sizeof(Cross) + (size_t)s.groups * 2 * 16 * (s.dim + 2) * sizeof(float);
 }
 
 }  // namespace
@@ -144,7 +144,7 @@ size_t attend_workspace_bytes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64
             most = n > most ? n : most;
         }
     const Shape s = shape_of(B, Hq, H, D, page_size, max_pages, most);
-    return workspace_of(s);
+    return workspace_of(s, s.groups);  // the table never has more entries
 }
 
 hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
@@ -160,7 +160,7 @@ hipError_t launch_attend(const AttendArgs& a, bool q_fp32, hipStream_t stream) {
            a.kv.num_heads * head_scales, head_scales,
            __builtin_fmaxf((formed ? form.unit : scale) * 1.4426950408889634f, kLeastC),
            formed ? form.unit : scale, form.times, a.scale < 0.0f ? 0x80008000u : 0u};
-    if (workspace_of(p.s) > attend_workspace_bytes(a.B, a.Hq, a.kv.num_heads, D, a.kv.page_size, a.max_pages))
+    if (workspace_of(p.s, p.s.crosses) > attend_workspace_bytes(a.B, a.Hq, a.kv.num_heads, D, a.kv.page_size, a.max_pages))
         return hipErrorInvalidValue;  // what is laid out here is what the caller was told to bring
     if (held == BD_E2M1)
         formed ? go_e2m1_formed(p, q_fp32, stream) : go_e2m1(p, q_fp32, stream);
