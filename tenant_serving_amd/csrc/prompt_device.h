@@ -587,15 +587,19 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 8 || kW <= 192 ? 2 : 1) void
                     sc[i] = __builtin_fmaf(-slope, __builtin_fabsf(far - (float)(i / 8 * 16 + i % 8)), sc[i]);
             }
         }
-        if (j0 < own.all_lo) {
-            const int lo = range.lo - j0 - 8 * half;
+        if (j0 < own.all_lo || j0 + kKeys > own.all_hi) {
+            // a bit for each of the tile's keys that the row sees, then of the lane's own; two operations for each score
+            const int lo = range.lo - j0, hi = range.hi - j0;
+            const auto below = [](int n) __attribute__((always_inline)) {
+                return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+            };
+            const uint64_t seen = below(hi) & ~below(lo);
+            const uint32_t bits = __builtin_amdgcn_perm((uint32_t)(seen >> 32), (uint32_t)seen, half ? 0x07050301u : 0x06040200u);
 #pragma unroll
-            for (int i = 0; i < KT * 16; ++i) sc[i] = i / 8 * 16 + i % 8 < lo ? kNegInf : sc[i];
-        }
-        if (j0 + kKeys > own.all_hi) {
-            const int hi = range.hi - j0 - 8 * half;
-#pragma unroll
-            for (int i = 0; i < KT * 16; ++i) sc[i] = i / 8 * 16 + i % 8 < hi ? sc[i] : kNegInf;
+            for (int i = 0; i < KT * 16; ++i) {
+                const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)bits, i, 1);
+                sc[i] = __uint_as_float((__float_as_uint(sc[i]) & keep) | (0xff800000u & ~keep));
+            }
         }
         float mx = sc[0];
 #pragma unroll
