@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
 
 // Tiles at most: whole ones of all rows, and one that is not for each sequence.
 int64_t tiles_at_most(int64_t T, int64_t B, int64_t group, int rows) { return T * group / rows + B; }
-int rows_of(int64_t D, int held) { return 32 * waves_of(width_of((int)D), held); }
+int rows_of(int64_t D, int held, bool form) { return 32 * waves_of(width_of((int)D), held, form); }
 
 // Workgroups that share a tile's keys.  `places` of them run at a time: two of 4
 // waves on each CU, or one of 8 or of 256 columns.  A split costs what its keys
@@ -82,11 +82,11 @@ int64_t splits_of(int64_t T, int64_t B, int64_t group, int64_t heads, int64_t ca
 
 }  // namespace
 
-// Enough for every type of cache.
+// Enough for every type of cache, whose tiles have one number of rows or the other.
 size_t prompt_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t capacity) {
     size_t bytes = 0;
     for (const int held : {BD_BF16, BD_E4M3}) {
-        const int rows = rows_of(D, held);
+        const int rows = rows_of(D, held, false);
         const int64_t tiles = tiles_at_most(T, B, Hq / H, rows), splits = splits_of(T, B, Hq / H, H, capacity, D, rows);
         const size_t n = splits == 1 ? 0 : (size_t)(tiles * H * splits * rows * (D + 2)) * sizeof(float);
         bytes = n > bytes ? n : bytes;
@@ -102,7 +102,7 @@ hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream) {
     const float scale = __builtin_fabsf(a.scale);
     const Form form = form_of(a.scale, a.cap);
     const int pg8 = a.kv.page_size / 8;
-    const int rows = rows_of(D, held);
+    const int rows = rows_of(D, held, formed);
     const int64_t tiles = tiles_at_most(a.T, a.B, a.Hq / H, rows);
     const Args p{a, D, H, a.Hq / H, rows, pg8, pg8 == 1 ? 0 : (int32_t)(uint32_t)((uint64_t(1) << 32) / pg8 + 1),
                  a.kv.page_size * a.max_pages, (int32_t)splits_of(a.T, a.B, a.Hq / H, H, (int64_t)a.kv.page_size * a.max_pages, D, rows),

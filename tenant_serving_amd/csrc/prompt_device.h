@@ -67,9 +67,12 @@ constexpr int keys_of(int width) { return width <= 128 ? 64 : 32; }
 // 1054 and 1081 us, e4m3 1248 and 1158, 4-bit codes capped 1836 and 1717; 64
 // columns 724 and 788, with e4m3 codes 779 and 782; 192 columns 1460 and 1557,
 // with codes 1647 and 1561; a chunk of 512 tokens on 32768 4-bit ones 656 and
-// 574; 15 tokens on 48000 bf16 ones 48 and 63).  At 256 columns a workgroup of 4
-// takes a CU's registers.
-constexpr int waves_of(int width, int held) { return held == BD_BF16 || width == 64 || width == 256 ? 4 : 8; }
+// 574; 15 tokens on 48000 bf16 ones 48 and 63).  Formed scores at 192 columns spill
+// with 8 (capped, e4m3 1999 and 2132, 4-bit codes 2109 and 2454).  At 256 columns a
+// workgroup of 4 takes a CU's registers.
+constexpr int waves_of(int width, int held, bool form) {
+    return held == BD_BF16 || width == 64 || width == 256 || (width == 192 && form) ? 4 : 8;
+}
 
 struct Args {
     PromptArgs a;
@@ -824,7 +827,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 8 || kW <= 192 ? 2 : 1) void
 
 template <int kW, int kHeld, bool kForm>
 void go_width(const Args& p, unsigned groups, hipStream_t s) {
-    constexpr int kWaves = waves_of(kW, kHeld);
+    constexpr int kWaves = waves_of(kW, kHeld, kForm);
     const dim3 grid(groups), block(kWaves * 64);
     if (p.dim == kW && p.token16 < (1u << 24))
         hipLaunchKernelGGL((prompt_kernel<kW, kHeld, kForm, true, kWaves>), grid, block, 0, s, p);
