@@ -145,3 +145,38 @@ def test_graph_of_a_token():
         assert bool(replayed.isfinite().all())
         for name in ("k", "v", "k_scales", "v_scales"):
             assert torch.equal(*(getattr(kv, name).view(torch.uint8) for kv in held)), (i, name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [BF, torch.float8_e4m3fn, torch.float4_e2m1fn_x2])
+def test_nothing_to_do(kind):
+    """No tokens, no sequences, sequences without tokens, and a cache of one page with bad tables: zeros, or no rows."""
+    on = lambda *values: torch.tensor(values, dtype=torch.int32, device=DEV)
+    kv = bd.bd_kv_cache.empty(1, 2, 8, 64, kind, DEV)
+    angles = bd.bd_rotary_angles(64, device=DEV)
+    q, k = torch.ones((3, 4, 64), dtype=BF, device=DEV), torch.ones((3, 2, 64), dtype=BF, device=DEV)
+    none = on()
+    tq, tk = bd.bd_rotary(angles, q[:0], none, k[:0])
+    assert tq.shape == (0, 4, 64) and tk.shape == (0, 2, 64)
+    bd.bd_kv_write(kv, k[:0], k[:0], none)
+    assert bd.bd_kv_read(kv, none)[0].shape == (0, 2, 64)
+    table = torch.full((2, 5), -1, dtype=torch.int32, device=DEV)
+    assert bd.bd_attend(q[:0], kv, table[:0], none, cap=3.0).shape == (0, 4, 64)
+    assert bd.bd_attend_prompt(q[:0], kv, table, on(0, 0), on(0, 0, 0)).shape == (0, 4, 64)
+    out = torch.full((3, 4, 64), 5.0, dtype=BF, device=DEV)
+    assert bool((bd.bd_attend_prompt(q, kv, table[:0], none, on(0), out=out) == 5).all())
+    for lens in (on(0, 0), on(-3, 0)):
+        for kw in (dict(), dict(cap=3.0)):
+            assert bool((bd.bd_attend(q[:2], kv, table, lens, **kw) == 0).all())
+            out.fill_(5.0)
+            bd.bd_attend_prompt(q, kv, table, lens, on(0, 2, 2), out=out, **kw)
+            assert bool((out[:2] == 0).all()) and bool((out[2:] == 5).all())
+    # a window that has passed the sequence's end, and one key that everything sees
+    assert bool((bd.bd_attend(q[:2], kv, table, on(1, 40), first=on(1, 40)) == 0).all())
+    bd.bd_kv_write(kv, k[:1], k[:1], on(0))
+    table[0, 0] = 0
+    for n in (1, 2, 3):
+        first, last = torch.zeros(n, dtype=torch.int32, device=DEV), torch.ones(n, dtype=torch.int32, device=DEV)
+        got = bd.bd_attend_prompt(q[:n], kv, table[:1], on(n), on(0, n), first=first, last=last)
+        assert bool((got == 1).all())
+    assert bool((bd.bd_attend(q[:1], kv, table[:1], on(1)) == 1).all())
