@@ -109,7 +109,11 @@ __device__ __forceinline__ void tokens_of(const Args& p, int b, int* start, int*
 }
 __device__ __forceinline__ int tiles_of(const Args& p, int n) { return (n * p.group + p.rows - 1) / p.rows; }
 // The tile that comes `from_end`-th from the end; each wave works it out, lane l
-// for `per` sequences from l per on.
+// for `per` sequences from l per on.  Starts that rise give fewer than kTilesMost
+// tiles (2^29 / 128 rows and 2^22 sequences); where they fall several sequences
+// may claim the same tokens, and a lane's sum stops there, so that 64 of them fit
+// 32 bits and what is found is a tile of its sequence.
+constexpr int kTilesMost = 1 << 24;
 __device__ __forceinline__ Tile tile_at(const Args& p, int from_end) {
     const int lane = threadIdx.x & 63;
     const int per = (p.a.B + 63) / 64, b0 = lane * per;
@@ -119,6 +123,7 @@ __device__ __forceinline__ Tile tile_at(const Args& p, int from_end) {
             given = p.a.lengths[b0 + i];
             tokens_of(p, b0 + i, &start, &n);
             sum += tiles_of(p, n);
+            sum = sum < kTilesMost ? sum : kTilesMost;
         }
     int inc = sum;
 #pragma unroll
