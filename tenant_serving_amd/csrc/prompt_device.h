@@ -583,7 +583,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 8 || kW <= 192 ? 2 : 1) void
         if constexpr (kForm) {
             if (p.a.cap > 0.0f) {
 #pragma unroll
-                for (int i = 0; i < KT * 2; ++i) cap_scores<8, true>(sc + 8 * i, p.times);
+                for (int i = 0; i < KT * 2; ++i) cap_scores<8>(sc + 8 * i, p.times);
             } else {
 #pragma unroll
                 for (int i = 0; i < KT * 16; ++i) sc[i] *= p.times;
@@ -774,7 +774,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 8 || kW <= 192 ? 2 : 1) void
                 x += __shfl_xor(x, 32, 64);
                 if constexpr (kForm) {
                     if (p.a.cap > 0.0f)
-                        cap_scores<1, true>(&x, p.times);
+                        cap_scores<1>(&x, p.times);
                     else
                         x *= p.times;
                     x = __builtin_fmaf(-slope, __builtin_fabsf((float)(range.pos - j)), x);

@@ -118,11 +118,9 @@ hipError_t launch_prompt(const PromptArgs& a, hipStream_t stream);
 // fitted to the least relative error of the whole (2^-25.7); that is the usual
 // case, as scores are small against a cap, and the only one where all of a
 // wave's scores are.  Where some are larger each lane takes what suits it.
-// kShort: g of degree 2 (2^-20.5), where the weights are rounded to 2^-9 anyway:
-// a cap of 50 leaves 2^-16 in the exponent, and in lse, where the roundings of a
-// score's own sum of 128 products may come to more.  (A prompt of 8192 tokens,
-// 64 heads of 128 over 8, capped: e4m3 1678 -> 1610 us, bf16 1445 -> 1410.)
-template <int kN, bool kShort = false>
+// A shorter g would give lse, an fp32 result, an error that grows with the cap:
+// degree 2 (2^-20.5) that of 12 roundings of the score.
+template <int kN>
 __device__ __forceinline__ void cap_scores(float* x, float times) {
     float big = 0.0f;
     float small[kN];
@@ -131,15 +129,9 @@ __device__ __forceinline__ void cap_scores(float* x, float times) {
         const float y = x[j] = x[j] * times;
         big = fmaxf(big, __builtin_fabsf(y));
         const float q = y * y;
-        float g;
-        if constexpr (kShort) {
-            g = __builtin_fmaf(q, -0.044750601f, 0.13205358f);
-            g = __builtin_fmaf(g, q, -0.33328161f);
-        } else {
-            g = __builtin_fmaf(q, 0.017257417f, -0.05305313f);
-            g = __builtin_fmaf(g, q, 0.13325989f);
-            g = __builtin_fmaf(g, q, -0.3333315f);
-        }
+        float g = __builtin_fmaf(q, 0.017257417f, -0.05305313f);
+        g = __builtin_fmaf(g, q, 0.13325989f);
+        g = __builtin_fmaf(g, q, -0.3333315f);
         small[j] = __builtin_fmaf(g, q * y, y);
     }
     if (__ballot(!(big <= 0.5f))) {

@@ -89,3 +89,54 @@ def test_sequences_that_claim_the_same_tokens():
     near = ((out.double() - want).abs() <= tol).all(2)
     assert (near | left).all()
     assert near.any()
+
+
+def lone_scores(kind, cap, new, past, seed=31):
+    """A case whose scores are one exact product each, up to about twice the cap and of either sign: queries and keys are
+    zero but in one column."""
+    def fix(k, v):
+        x = k[..., 5].clone()
+        k.zero_()
+        k[..., 5] = x
+    c, q, table, lengths, starts, slots = plain.case(new, past, 2, 4, 64, 16, kind, seed=seed, fix=fix)
+    x = q[..., 5].clone()
+    q.zero_()
+    q[..., 5] = x
+    return c, q, table, lengths, starts, slots, cap / 2
+
+
+def check_lone(lse, q, keys, cap, scale):
+    """lse [n, heads] of rows that see one key each, keys [n, kv heads, dim]: it is the capped score.  Where the score before
+    the cap is at most half of it: two roundings of the factor and of its product with the score, a polynomial of relative
+    error 2^-25.7 whose last sum is rounded once and the roundings within it a third of one, a product with the cap and the
+    sum's logarithm of an exponential and its own (4 u).  Beyond, tanh x = 1 - 2 / (1 + e^(2 x)): off by 8 u, as the
+    exponential's argument is rounded, 2 x of its own size, which the slope of the whole at most halves, and the exponential,
+    the inverse and the sums take a step each."""
+    s = (q[..., 5] * keys[..., 5].repeat(q.shape[1] // keys.shape[1], 1)) * scale
+    want = cap * np.tanh(s / cap)
+    tol = np.where(np.abs(s) <= cap / 2 * (1 - 4 * U), 6 * U * np.abs(want), 8 * U * cap + 3 * U * np.abs(want)) + 4 * U
+    off = np.abs(lse - want) / tol
+    assert (off <= 1).all(), (cap, off.max(), (s / cap)[off > 1][:4])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [BF, plain.E4, plain.E2])
+@pytest.mark.parametrize("cap", [50.0, 1e4, 1e6, 2.0 ** 40])
+def test_capped_scores_are_those_of_fp32(kind, cap):
+    """Each token sees its own key only, so lse is its score: in a prompt, and as one new token of a sequence."""
+    new, past = [200, 33, 1], [3, 64, 700]
+    c, q, table, lengths, starts, slots, scale = lone_scores(kind, cap, new, past)
+    pos = np.concatenate([np.arange(p, p + n) for n, p in zip(new, past)])
+    first = torch.tensor(pos, dtype=torch.int32)
+    keys = np.concatenate([plain.rows64(c, 0, own[p:]) for own, p in zip(slots, past)])
+    values = np.concatenate([plain.rows64(c, 1, own[p:]) for own, p in zip(slots, past)])
+    out, lse = plain.run(c, q, table, lengths, starts, scale=scale, cap=cap, first=first)
+    q64, want = q.double().numpy(), values.repeat(4, 1)
+    check_lone(lse.cpu().double().numpy(), q64, keys, cap, scale)
+    assert (np.abs(out.cpu().double().numpy() - want) <= 2.0 ** -8 * 2 * np.abs(want)).all()     # its one weight is rounded too
+    lens = torch.tensor(pos + 1, dtype=torch.int32)
+    tables = torch.cat([table[b:b + 1].repeat(n, 1) for b, n in enumerate(new)])
+    for x in (q, q.float()):
+        out, lse = plain.formed.run(c, x, tables, lens, scale=scale, cap=cap, first=first)
+        check_lone(lse.cpu().double().numpy(), q64, keys, cap, scale)
+        assert np.array_equal(out.cpu().double().numpy(), want)
