@@ -256,7 +256,8 @@ bd_status bd_attend(const bd_kv* kv, const void* q, int32_t q_type, const int64_
  * and which tokens are attended to: first <= j < last.
  *
  *   cap      0, or 2^-60 .. 2^60: no score is larger than it in magnitude.
- *   slopes   [num_q_heads] fp32; finite.
+ *   slopes   [num_q_heads] fp32; finite.  A slope times a distance past fp32's range
+ *            (both over the cap, where there is one) counts as infinite.
  *   first    int32, one number for each query token (each sequence of
  *            bd_attend_scores): tokens before it are not attended to, and
  *            pages that hold only such are not looked up.  0 or less, or NULL:

@@ -672,7 +672,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
         f32x4_t acc[DV];
         float m, mm, l;  // mm: m, or 0 while m is -infinity
         float c = p.c, times = kForm ? p.times : 1.0f;
-        const float bias = kForm ? slope / p.unit : 0.0f;
+        const float bias = kForm ? slope_in(slope, p.unit) : 0.0f;
         int pass = 0;  // 1: again, see below
         bool lost = false;
 

@@ -330,7 +330,7 @@ __global__ __launch_bounds__(kWaves * 64, kWaves == 8 || kW <= 192 ? 2 : 1) void
         const int d = s * 16 + half * 8;
         q[s] = *reinterpret_cast<const uint4*>(q_row + (d < p.dim ? d : 0));
     }
-    const float slope = kForm && p.a.slopes ? p.a.slopes[qhead] / p.unit : 0.0f;
+    const float slope = kForm && p.a.slopes ? slope_in(p.a.slopes[qhead], p.unit) : 0.0f;
     Range range{0, 0, 0};
     if (mine) range = range_of(p, tile, len, token);
     const bool sees = range.hi > range.lo;

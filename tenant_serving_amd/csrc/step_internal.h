@@ -156,6 +156,11 @@ inline Form form_of(float scale, float cap) {
     // an infinite product times a scale other than 0 stays infinite
     return Form{unit, size > 0.0f && size / unit == 0.0f ? 0x1p-149f : size / unit};
 }
+// A slope in these units; finite, so that it takes nothing off at no distance.
+__device__ __forceinline__ float slope_in(float slope, float unit) {
+    const float b = slope / unit;
+    return __builtin_isinf(b) ? __builtin_copysignf(0x1.fffffep127f, b) : b;
+}
 
 // ---------------------------------------------------------------------------
 // e4m3 groups

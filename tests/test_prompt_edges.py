@@ -140,3 +140,23 @@ def test_capped_scores_are_those_of_fp32(kind, cap):
         out, lse = plain.formed.run(c, x, tables, lens, scale=scale, cap=cap, first=first)
         check_lone(lse.cpu().double().numpy(), q64, keys, cap, scale)
         assert np.array_equal(out.cpu().double().numpy(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [BF, plain.E2])
+def test_slopes_far_above_the_cap(kind):
+    """Slopes that over the cap leave fp32's range: at no distance they take nothing off, at any other everything."""
+    new, past = [70, 3], [3, 64]
+    c, q, table, lengths, starts, slots = plain.case(new, past, 2, 4, 64, 16, kind)
+    pos = np.concatenate([np.arange(p, p + n) for n, p in zip(new, past)])
+    values = np.concatenate([plain.rows64(c, 1, own[p:]) for own, p in zip(slots, past)]).repeat(4, 1)
+    tables = torch.cat([table[b:b + 1].repeat(n, 1) for b, n in enumerate(new)])
+    slopes = torch.full((8,), 2.0 ** 100)
+    for cap in (2.0 ** -60, 2.0 ** -30, 1.0, None):
+        kw = dict(slopes=slopes, cap=cap)
+        out, lse = plain.run(c, q, table, lengths, starts, **kw)
+        one, one_lse = plain.formed.run(c, q, tables, torch.tensor(pos + 1, dtype=torch.int32), **kw)
+        for o, l in ((out, lse), (one, one_lse)):
+            # a lone weight: exact, or rounded to bf16 as the result is
+            assert (np.abs(o.cpu().double().numpy() - values) <= 2.0 ** -8 * 2 * np.abs(values)).all()
+            assert l.isfinite().all() and (cap is None or (l.abs() <= cap + 4 * U).all())
