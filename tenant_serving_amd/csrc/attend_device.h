@@ -394,13 +394,20 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
     // lets the values come later: e2m1 without formed scores 136 -> 129 us, with
     // a cap 149 -> 152 (64 sequences of up to 16381 tokens, 64 heads of 128 over 8).
     constexpr bool kLate = kE2m1 && !kForm;
+    // Whether page numbers are sent before the keys of the tile before and scale
+    // bytes made scales where they are used, see below.  Not in e4m3 from 128 columns on
+    // without formed scores (31 sequences of up to 1013 tokens, 32 heads of 128 /
+    // 192 / 256, 37.1 -> 36.0 / 50.5 -> 48.7 / 64.7 -> 62.0 us; 64 of up to 16381, 64
+    // heads over 8, at 192 294 -> 290), but with fp32 queries of 256 (there 74.5 -> 80.2).
+    constexpr bool kPagesFirst = !kE4m3 || kForm || kDC < 128 || (kDC == 256 && kSplitQ);
     // Whether a tile's next loads are sent in any case, see below.  Not where that
     // is more than it gives: in bf16 up to 128 columns, where no scales are waited
-    // for (at 256 768 -> 731 us, but 31 sequences of 1024 tokens of 128 32 -> 33),
-    // and in e4m3 at 64 without formed scores (31 of up to 1013, 32 heads, 20.9 ->
-    // 21.9; with a bias by distance 16 of up to 8191 67.7 -> 65.2; at 128 64 of up
-    // to 16381 184 -> 182).
-    constexpr bool kAlways = kE2m1 || kDC > 128 || (kE4m3 && (kForm || kDC > 64));
+    // for (at 256 806 -> 774 us, but 31 sequences of 1024 tokens of 128 32 -> 33), and
+    // without formed scores at 192 (31 of up to 1013, 32 heads, 76.2 -> 80.1), and in
+    // e4m3 at 64 without formed scores (31 of up to 1013, 32 heads, 20.9 -> 21.9; with
+    // a bias by distance 16 of up to 8191 67.7 -> 65.2; at 96 64 of up to 16381 160 ->
+    // 157).
+    constexpr bool kAlways = kPagesFirst && (kE2m1 || kDC == 256 || (kForm && kDC > 128) || (kE4m3 && (kForm || kDC > 64)));
     constexpr int NR = kTight ? (NS + kWaves - 1) / kWaves : NS;  // k-steps whose queries a wave loads
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
@@ -464,11 +471,11 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
 
     // A tile's loads, in flight while the tile before it is worked on: the keys
     // as soon as the scores are done with the registers, the values after the
-    // sums, the page numbers just before the keys of the tile before.  So none is
-    // waited for by way of another that was sent later.  Behind a piece's last
-    // tile page 0 is loaded, whose lines all waves share (kAlways): without a
-    // branch the compiler knows what is on its way at a tile's start, and does
-    // not wait for all of it.  Scale bytes are made scales where they are used.
+    // sums, the page numbers just before the keys of the tile before, so that none is
+    // waited for by way of another that was sent later (kPagesFirst; else after the
+    // values).  Behind a piece's last tile page 0 is loaded, whose lines all waves
+    // share (kAlways): without a branch the compiler knows what is on its way at a
+    // tile's start, and does not wait for all of it.
     // (64 sequences of up to 16381 tokens, 64 heads of 128 over 8, e2m1: 155 ->
     // 129 us; 16 of up to 8191, 32 heads of 64, e4m3, a bias by distance: 72 -> 63.)
     // A row's first tile and its queries are loaded while the row before it is
@@ -539,7 +546,10 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                 }
             }
             at += 4 * token_bytes;
-            if (kE4m3) ks[h][0] = p.a.kv.k_scales[wh.sc + (i16 & 3) + 4 * h];
+            if (kE4m3) {
+                const uint32_t byte = p.a.kv.k_scales[wh.sc + (i16 & 3) + 4 * h];
+                ks[h][0] = kPagesFirst ? byte : __float_as_uint(scale_of(byte));
+            }
         }
     };
     const auto load_values = [&](const Where& wh) {
@@ -618,19 +628,33 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
     // page 0; its values are at what comes back.
     const auto load_next = [&](const Piece& x, int t, bool more) {
         const Where k = locate(p, more ? pages.k : Group{0, 0}, x.head);
-        const Where v = locate(p, more ? pages.v : Group{0, 0}, x.head);
-        __builtin_amdgcn_sched_barrier(0);  // no copies of numbers that are on their way
-        pages = load_pages(x, t);           // past the end: the last group's page
-        __builtin_amdgcn_sched_barrier(0);
-        load_keys(k);
-        __builtin_amdgcn_sched_barrier(0);
-        return v;
+        if constexpr (!kPagesFirst) {
+            load_keys(k);
+            return Where{};
+        } else {
+            const Where v = locate(p, more ? pages.v : Group{0, 0}, x.head);
+            __builtin_amdgcn_sched_barrier(0);  // no copies of numbers that are on their way
+            pages = load_pages(x, t);           // past the end: the last group's page
+            __builtin_amdgcn_sched_barrier(0);
+            load_keys(k);
+            __builtin_amdgcn_sched_barrier(0);
+            return v;
+        }
+    };
+    // That tile's values, and where they come first the page numbers of the next.
+    const auto load_rest = [&](const Piece& x, int t, const Where& v) {
+        if constexpr (!kPagesFirst) {
+            load_values(locate(p, pages.v, x.head));
+            pages = load_pages(x, t);
+        } else {
+            load_values(v);
+        }
     };
     drop();
     load_queries(now);
     if (now.t0 < now.stop) {
         pages = load_pages(now, now.t0);
-        load_values(load_next(now, now.t0 + kUnit, true));
+        load_rest(now, now.t0 + kUnit, load_next(now, now.t0 + kUnit, true));
     }
 
     for (int turn = 0;; turn ^= kTurns - 1) {
@@ -693,7 +717,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                     uint4 kb;
                     if constexpr (kE4m3) {
                         const uint32_t c0 = kk[h][s / 2].d[2 * (s & 1)], c1 = kk[h][s / 2].d[2 * (s & 1) + 1];
-                        const float scale = scale_of(ks[h][0]);
+                        const float scale = kPagesFirst ? scale_of(ks[h][0]) : __uint_as_float(ks[h][0]);
                         kb = make_uint4(e4m3x2_to_bf16<false>(c0, scale), e4m3x2_to_bf16<true>(c0, scale),
                                         e4m3x2_to_bf16<false>(c1, scale), e4m3x2_to_bf16<true>(c1, scale));
                     } else if constexpr (kE2m1) {
@@ -811,7 +835,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                 }
                 if (kTight) __builtin_amdgcn_sched_barrier(0);  // or the pairs of all columns wait in registers
             }
-            if (kAlways || more) load_values(values_at);
+            if (kAlways || more) load_rest(now, t + 2 * kUnit, values_at);
         }
 
         // Further terms break on infinities: they are of either sign or zero,
@@ -845,7 +869,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                 }
                 pass = 1;
                 pages = load_pages(now, t0);
-                load_values(load_next(now, t0 + kUnit, true));
+                load_rest(now, t0 + kUnit, load_next(now, t0 + kUnit, true));
                 goto again;
             }
         } else {
@@ -869,7 +893,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
         if (!last) load_queries(next);
         if (!last && next.t0 < next.stop) {
             pages = next_pages;
-            load_values(load_next(next, next.t0 + kUnit, true));
+            load_rest(next, next.t0 + kUnit, load_next(next, next.t0 + kUnit, true));
         } else {  // nothing is kept in these registers from here
             drop();
         }
