@@ -160,3 +160,19 @@ def test_slopes_far_above_the_cap(kind):
             # a lone weight: exact, or rounded to bf16 as the result is
             assert (np.abs(o.cpu().double().numpy() - values) <= 2.0 ** -8 * 2 * np.abs(values)).all()
             assert l.isfinite().all() and (cap is None or (l.abs() <= cap + 4 * U).all())
+
+
+# every width's kernels, whole and in part; formed scores of codes take four waves at 192 columns, eight at 96 and 128
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,dims", [(BF, (48, 80, 112, 192, 176, 224)), (plain.E4, (48, 80, 112, 192, 176, 224)),
+                                       (plain.E2, (32, 192, 224))])
+def test_formed_scores_of_every_width(kind, dims):
+    new, past = [1, 33, 0, 130, 7], [1100, 64, 3, 0, 400]
+    first, last = plain.ranges("both", new, past)
+    for dim, (heads, group) in zip(dims, ((2, 3), (1, 8), (1, 1), (2, 4), (1, 2), (3, 1))):
+        slopes = torch.exp2(-4 * torch.rand(heads * group, generator=plain.gen_of(1)))
+        for kw in (dict(cap=3.0), dict(slopes=slopes), dict(cap=50.0, slopes=slopes, first=first, last=last, scale=-0.7)):
+            print("prompt formed", kind, dim, sorted(kw), flush=True)
+            c, q, table, lengths, starts, slots = plain.case(new, past, heads, group, dim, 16, kind)
+            out, lse = plain.run(c, q, table, lengths, starts, **kw)
+            plain.check(c, q, starts, slots, out, lse, some=(0, 1, 5, 31, 32, 100, -1), **kw)
