@@ -176,3 +176,35 @@ def test_formed_scores_of_every_width(kind, dims):
             c, q, table, lengths, starts, slots = plain.case(new, past, heads, group, dim, 16, kind)
             out, lse = plain.run(c, q, table, lengths, starts, **kw)
             plain.check(c, q, starts, slots, out, lse, some=(0, 1, 5, 31, 32, 100, -1), **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,dim,kw", [(BF, 64, {}), (BF, 128, {}), (BF, 192, {}), (BF, 256, {}), (plain.E4, 96, {}), (plain.E4, 128, {}),
+                                         (plain.E4, 256, {}), (plain.E2, 64, {}), (plain.E2, 128, dict(cap=20.0)), (plain.E2, 192, {}),
+                                         (plain.E2, 192, dict(cap=20.0))])
+def test_more_than_two_rounds_of_page_numbers(kind, dim, kw):
+    """Workgroups that go over more than 128 tiles of keys, whose pages they look up 64 tiles at a time; also with pages
+    that are not there, in each round, which only some tokens see."""
+    keys, heads, group, n = (64 if dim <= 128 else 32), 2, 16, 2048
+    past = 129 * keys + 40
+    c, q, table, lengths, starts, slots = plain.case([n], [past], heads, group, dim, 16, kind)
+    # nothing is split, so that a workgroup's tiles are all of a row's
+    assert plain.prompt._prompt_bytes(n, 1, heads * group, heads, dim, 16, table.shape[1]) == 0 and past // keys > 128
+    some = (0, 1, 31, 32, 127, 128, 900, 2040, -1)
+    print("prompt rounds", kind, dim, kw, flush=True)
+    out, lse = plain.run(c, q, table, lengths, starts, **kw)
+    plain.check(c, q, starts, slots, out, lse, some=some, **kw)
+    bad = [70 * keys + 3, 63 * keys, 128 * keys + 17]      # tokens whose pages are not there
+    for i, j in enumerate(bad):
+        table[0, j // 16] = (10 ** 6, -1, 2 ** 31 - 1)[i]
+    sees = torch.arange(n) // 8 % 5
+    first, last = torch.zeros(n, dtype=torch.int32), torch.zeros(n, dtype=torch.int32)
+    ranges = [(0, 63 * keys), (63 * keys + 16, 70 * keys), (71 * keys, 128 * keys), (129 * keys, past), (0, past)]
+    for i, (a, b) in enumerate(ranges):
+        first[sees == i], last[sees == i] = a, b
+    out, lse = plain.run(c, q, table, lengths, starts, first=first, last=last, **kw)
+    nan = out.cpu().isnan().all(2).all(1)
+    assert torch.equal(nan, sees == 4) and torch.equal(out.cpu().isnan().any(2).any(1), nan)
+    assert torch.equal(lse.cpu().isnan().any(1), nan)
+    some = [t for t in (0, 8, 16, 24, 31, 40, 127, 800, 808, 2040) if sees[t] < 4]
+    plain.check(c, q, starts, slots, out, lse, first=first, last=last, some=some, **kw)
