@@ -208,3 +208,54 @@ def test_more_than_two_rounds_of_page_numbers(kind, dim, kw):
     assert torch.equal(lse.cpu().isnan().any(1), nan)
     some = [t for t in (0, 8, 16, 24, 31, 40, 127, 800, 808, 2040) if sees[t] < 4]
     plain.check(c, q, starts, slots, out, lse, first=first, last=last, some=some, **kw)
+
+
+def formed_bound(q, k, scale, cap):
+    """Capped scores [Hq, n] of q [Hq, D] and k [Hq, n, D] (float64), and how far one is off at most: the products' and
+    sums' roundings as far as the cap lets them through, and 8 u of the cap (see check_lone).  The kernels' sums of
+    infinite terms of one sign are exact."""
+    with np.errstate(all="ignore"):
+        prod = q[:, None, :] * k * scale
+        s, a = prod.sum(2), np.abs(prod).sum(2)
+        e = np.where(np.isfinite(a), (q.shape[1] + 8) * U * a, 0.0)
+        through = np.where(np.isfinite(a), cap * (np.tanh((np.abs(s) + e) / cap) - np.tanh((np.abs(s) - e) / cap)), 0.0)
+    return cap * np.tanh(s / cap), np.minimum(through, e).max() + 8 * U * cap
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_t", [BF, F32])
+@pytest.mark.parametrize("kind", [BF, plain.E4, plain.E2])
+def test_scores_far_past_the_cap(kind, q_t):
+    """Saturated scores, of finite and infinite keys, with bounds that a wrong one passes: a prompt's last tokens, and one
+    new token.  fp32 queries hold bf16 values, as where a sequence's keys are infinite only these enter, and weights as one
+    term like a prompt's."""
+    lens, new, alone = [40, 300, 3000], 3, 2.0 ** -8 if kind == BF and q_t == F32 else 2.0 ** -15
+
+    def fix(k, v):
+        # a key's values have one sign, so that no score is what is left of larger terms
+        k.copy_(k.abs() * torch.where(torch.arange(len(k)) % 3 == 0, 1, -1)[:, None, None])
+        if kind == BF:
+            k[3], k[350] = float("inf"), -float("inf")      # codes hold no infinities
+        k[45] *= 3e4
+        k[700] *= 3e4
+        k[2000, 1] *= -1e5
+    for cap, scale in ((8.0, 0.125), (100.0, 2.0 ** 60), (2.0 ** -20, -1.0), (30.0, -50.0)):
+        c, q, table, lengths, starts, slots = plain.case([new] * 3, [n - new for n in lens], 2, 2, 64, 16, kind, fix=fix)
+        q = q.abs() + 0.25          # all products of a wholly infinite key have one sign
+        print("capped", kind, q_t, cap, scale, flush=True)
+        out, lse = plain.run(c, q, table, lengths, starts, cap=cap, scale=scale)
+        one, one_lse = plain.formed.run(c, q[new - 1::new].to(q_t).contiguous(), table, lengths, cap=cap, scale=scale)
+        for b, own in enumerate(slots):
+            k, v = (plain.rows64(c, i, own).transpose(1, 0, 2).repeat(2, 0) for i in (0, 1))
+            for o, l, extra in ((out[b * new + new - 1], lse[b * new + new - 1], 2.0 ** -8), (one[b], one_lse[b], alone)):
+                s, ds = formed_bound(q[b * new + new - 1].double().numpy(), k, scale, cap)
+                p = np.exp(s - s.max(1, keepdims=True))
+                want = (p[:, None] @ v)[:, 0] / p.sum(1)[:, None]
+                mean = (p[:, None] @ np.abs(v))[:, 0] / p.sum(1)[:, None]
+                n = len(own)
+                tol = 2.0 ** -8 * np.abs(want) + extra * mean + 2 * np.abs(v).max() * (np.expm1(2 * ds) + (n + 64) * U)
+                assert tol.max() < 0.1 * np.abs(v).max(), tol.max()      # or the test says nothing
+                assert (np.abs(o.cpu().double().numpy() - want) <= tol).all(), (b, extra)
+                want_lse = s.max(1) + np.log(p.sum(1))
+                tl = ds + (n + 64) * U + 4 * U * np.abs(want_lse)
+                assert tl.max() < 0.01 * max(1.0, cap) and (np.abs(l.cpu().double().numpy() - want_lse) <= tl).all(), (b, extra)
