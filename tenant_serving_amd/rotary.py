@@ -8,12 +8,15 @@ from __future__ import annotations
 
 import ctypes
 import math
+from fractions import Fraction
 
 import torch
 
 from . import step
 from .bitdelta import _check
 from .step import _IN, _Pair, _any_on_rows, _index, _overlap, _plain, _rows, _same_gpu, _span, _tensor, _typed
+
+_TURN = Fraction("6.283185307179586476925286766559005768394338798750211641949889")  # 2 pi
 
 
 class bd_rotary_angles:
@@ -45,8 +48,9 @@ class bd_rotary_angles:
             frequencies = [float(x) for x in (frequencies.tolist() if isinstance(frequencies, torch.Tensor) else frequencies)]
         if len(frequencies) != turned // 2 or not all(abs(x) <= 2.0 ** 20 for x in frequencies):
             raise ValueError("frequencies must be %d numbers of at most 2^20 (got %s)" % (turned // 2, frequencies))
-        # the low 64 bits, as the signed number that int64 holds
-        steps = [round(math.ldexp(x / (2.0 * math.pi), 64)) & (1 << 64) - 1 for x in frequencies]
+        # the low 64 bits, as the signed number that int64 holds; a float64's quotient would be off by 2^-56 of a turn,
+        # which the farthest position makes 2^-25
+        steps = [round(Fraction(x) / _TURN * 2 ** 64) & (1 << 64) - 1 for x in frequencies]
         self.steps = torch.tensor([x - (x >> 63 << 64) for x in steps], dtype=torch.int64, device=device)
         self.turned, self.interleaved, self.gain = turned, bool(interleaved), float(gain)
         self.frequencies = frequencies
