@@ -107,7 +107,9 @@ bd_status bd_rms_norm(const void* x, int32_t x_type, const void* residual, void*
  *   steps       [turned / 2] uint64, 8-byte aligned: the part of a turn that a
  *               position adds, as a fraction of 2^64.  Its product with a
  *               position wraps as the angle does, so that no position is too
- *               far: a pair's angle is exact to 2^-32 of a turn (1.5e-9).
+ *               far: a pair's phase is kept to 2^-32 of a turn, and what it is
+ *               past the nearest quarter turn is rounded to fp32, which leaves
+ *               the angle 1.5e-7 of a radian off at most.
  *   gain        finite (1 but where a scaled context asks for another).
  * Products and sums are fp32, results rounded once.  T <= 2^31 - 1; T == 0 is
  * a no-op.

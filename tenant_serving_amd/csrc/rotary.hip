@@ -9,7 +9,8 @@
 // The angle in whole numbers: s_i is the part of a turn that one position adds
 // as a fraction of 2^64, and the low 64 bits of p s_i are the angle without its
 // whole turns, however far p is.  Their upper 32 bits less the nearest quarter
-// turn leave at most pi / 4, where the series of sine and cosine end soon.
+// turn leave at most pi / 4, where the series of sine and cosine end soon; in fp32
+// that is off by three roundings, 1.4e-7, which the results' own are as large as.
 #include "step_internal.h"
 
 namespace bd {
