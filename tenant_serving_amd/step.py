@@ -633,7 +633,8 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     scale = kv.head_dim ** -0.5 if scale is None else float(scale)
     if not abs(scale) <= 2.0 ** 60:
         raise ValueError("scale must be at most 2^60 (got %r)" % scale)
-    formed, limit = cap is not None or slopes is not None or first is not None, _cap(cap)
+    formed = cap is not None or slopes is not None or first is not None
+    limit = _cap(cap) if formed else 0.0
     q0 = q.data_ptr()
     if not (type(page_table) is torch.Tensor and page_table.dim() == 2
             and page_table.dtype is _INT and page_table.shape[0] == B and page_table.is_contiguous()
@@ -652,23 +653,22 @@ def bd_attend(q: torch.Tensor, kv: bd_kv_cache, page_table: torch.Tensor, length
     lib = _declared or _library()
     pages = page_table.shape[1]
     nbytes = _attend_bytes(B, heads, kv.num_heads, kv.head_dim, kv.page_size, pages)
-    scores = None
-    if formed:
-        scores = ctypes.byref(_Scores(limit, _at(slopes), _at(first), None))
     if out is None:
         if kind == BD_BF16 and q.is_contiguous():
             out = torch.empty_like(q)
         else:
             out = torch.empty((B, heads, kv.head_dim), dtype=torch.bfloat16, device=kv.device)
     ws = _workspace(nbytes, kv.device)
-    args = (out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None,
-            nbytes, _stream_of(dev))
     if formed:
+        scores = _Scores(limit, _at(slopes), _at(first), None)
         st = lib.bd_attend_scores(kv._ref, q0, kind, qs, heads, page_table.data_ptr(),
-                                  page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, scores, *args)
+                                  page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale,
+                                  ctypes.byref(scores), out.data_ptr(), _at(lse), _at(ws), nbytes, _stream_of(dev))
     else:
         st = lib.bd_attend(kv._ref, q0, kind, qs, heads, page_table.data_ptr(),
-                           page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, *args)
+                           page_table.stride(0) if B > 1 else 0, pages, lengths.data_ptr(), B, scale, out.data_ptr(),
+                           lse.data_ptr() if lse is not None else None, ws.data_ptr() if ws is not None else None, nbytes,
+                           _stream_of(dev))
     if st:
         _check(lib, "bd_attend", st)
     return out
