@@ -396,19 +396,22 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
     // a cap 149 -> 152 (64 sequences of up to 16381 tokens, 64 heads of 128 over 8).
     constexpr bool kLate = kE2m1 && !kForm;
     // Whether page numbers are sent before the keys of the tile before and scale
-    // bytes made scales where they are used, see below.  Not in e4m3 from 128 columns on
-    // without formed scores (31 sequences of up to 1013 tokens, 32 heads of 128 /
-    // 192 / 256, 37.1 -> 36.0 / 50.5 -> 48.7 / 64.7 -> 62.0 us; 64 of up to 16381, 64
-    // heads over 8, at 192 294 -> 290), but with fp32 queries of 256 (there 74.5 -> 80.2).
-    constexpr bool kPagesFirst = !kE4m3 || kForm || kDC < 128 || (kDC == 256 && kSplitQ);
+    // bytes made scales where they are used, see below.  Without formed scores only
+    // where that gives something.  Not in e4m3 from 128 columns on (31 sequences of up
+    // to 1013 tokens, 32 heads of 128 / 192 / 256, 37.1 -> 36.0 / 50.5 -> 48.7 / 64.7
+    // -> 62.0 us; 64 of up to 16381, 64 heads over 8, at 192 294 -> 290), but with fp32
+    // queries of 256 (there 80.2 -> 74.5).  In bf16 at 160 to 192 and 256 (32 of up to
+    // 8192, 32 heads over 8, 168 -> 165.5 and 228 -> 216), not below or between (16 of
+    // up to 300, 64 heads of 64 6.75 -> 6.86; 4 of up to 37, of 224, 8.4 -> 8.8).
+    constexpr bool kPagesFirst = kE2m1 || kForm || (kE4m3 ? kDC < 128 || (kDC == 256 && kSplitQ)
+                                                          : kDC == 192 || (kDC == 256 && kFull));
     // Whether a tile's next loads are sent in any case, see below.  Not where that
-    // is more than it gives: in bf16 up to 128 columns, where no scales are waited
-    // for (at 256 806 -> 774 us, but 31 sequences of 1024 tokens of 128 32 -> 33), and
-    // without formed scores at 192 (31 of up to 1013, 32 heads, 76.2 -> 80.1), and in
-    // e4m3 at 64 without formed scores (31 of up to 1013, 32 heads, 20.9 -> 21.9; with
-    // a bias by distance 16 of up to 8191 67.7 -> 65.2; at 96 64 of up to 16381 160 ->
-    // 157).
-    constexpr bool kAlways = kPagesFirst && (kE2m1 || kDC == 256 || (kForm && kDC > 128) || (kE4m3 && (kForm || kDC > 64)));
+    // is more than it gives: in bf16 without formed scores (at 256 32 of up to 8192
+    // 216 -> 220, 16 of up to 300 18.6 -> 19.4, with formed ones up to 128, where no
+    // scales are waited for) and in e4m3 at 64 without them (31 of up to 1013, 32
+    // heads, 20.9 -> 21.9; with a bias by distance 16 of up to 8191 67.7 -> 65.2; at
+    // 96 64 of up to 16381 160 -> 157, at 256 with fp32 queries 392 -> 360).
+    constexpr bool kAlways = kPagesFirst && (kE2m1 || (kForm && kDC > 128) || (kE4m3 && (kForm || kDC > 64)));
     constexpr int NR = kTight ? (NS + kWaves - 1) / kWaves : NS;  // k-steps whose queries a wave loads
 
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6);
