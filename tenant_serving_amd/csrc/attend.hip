@@ -52,7 +52,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args p) {
             for (int w = w0 + set; w <= w1; w += sets) {
                 const float* part = place(p, w, w == w0 ? which0 : 0);
                 const float2 ml = *reinterpret_cast<const float2*>(part + 2 * q);
-                const float4 x = *reinterpret_cast<const float4*>(part + 2 * p.s.cols + q * p.s.dim + d);
+                const float4 x = *reinterpret_cast<const float4*>(part + 32 + q * p.s.dim + d);
                 add_part(p.c, M, L, o, ml.x, ml.y, x);
             }
         }
@@ -119,7 +119,6 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     s.magic = s.pg8 == 1 ? 0 : (int32_t)(uint32_t)((uint64_t(1) << 32) / s.pg8 + 1);
     s.group = (int32_t)(Hq / H);
     s.tiles = (s.group + 15) / 16;
-    s.cols = D <= 64 || s.group >= 16 ? 16 : (s.group + 1) / 2 * 2;
     s.rows = s.heads * s.tiles;
     s.capacity = (int32_t)(page_size * max_pages);
     s.whole = is_whole(B, B * s.rows, s.capacity, D);
@@ -130,7 +129,7 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
     // there are two.  (16 heads to a key-value head, 64 sequences of up to 16381
     // tokens, 8 heads of 128, with two and three: 133 and 128 us, 32 of up to 8192
     // 41.2 and 40.7, 16 of up to 4099 21.7 and 22.4.)
-    const int64_t most = s.whole ? int64_t(1) << 20 : kCUs * (D > 64 && per_cu * s.cols > 32 ? std::min(per_cu, 2) : per_cu);
+    const int64_t most = s.whole ? int64_t(1) << 20 : kCUs * (D > 64 && per_cu * heads_of_place(s.dim, s.group) > 32 ? std::min(per_cu, 2) : per_cu);
     s.groups = (int32_t)(units < most ? units : most);
     s.ordered = s.whole && s.capacity > kUnit && B <= kSorted && s.groups == B * s.rows && s.groups > kCUs * per_cu;
     s.by_row = B * s.rows <= s.groups;
@@ -139,7 +138,7 @@ Shape shape_of(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t page_size, i
 }
 
 size_t workspace_of(const Shape& s, int32_t crosses) {
-    return s.whole ? 0 : (size_t)crosses * sizeof(Cross) + (size_t)s.groups * 2 * s.cols * (s.dim + 2) * sizeof(float);
+    return s.whole ? 0 : (size_t)crosses * sizeof(Cross) + (size_t)s.groups * 2 * numbers_of_place(s.dim, s.group) * sizeof(float);
 }
 
 }  // namespace

@@ -97,7 +97,6 @@ constexpr float kLeastC = 0x1p-149f;
 struct Shape {
     int32_t heads, dim, page_size, pg8, magic;  // pg8: groups of 8 tokens in a page
     int32_t group, tiles;                       // query heads per kv head, and tiles of 16 of them
-    int32_t cols;                               // heads that a place of the workspace has room for, an even number
     int32_t rows;                               // rows of units per sequence: heads * tiles
     int32_t capacity, groups;                   // tokens a table row holds; workgroups launched
     int32_t crosses, by_row;                    // entries of the workspace's table
@@ -256,8 +255,8 @@ struct Cut {
 };
 
 // The workspace: a table of Cross, then each workgroup's partial results, two
-// places (the first row it works on and the last one) of a row's heads' (maximum,
-// sum) and unnormalised outputs.
+// places (the first row it works on and the last one) of 16 (maximum, sum) and a
+// row's heads' unnormalised outputs.
 //
 // Cross: a row of units that starts in one workgroup and goes on in the next
 // ones.  The table has an entry per row of the batch where these are fewer
@@ -269,8 +268,12 @@ struct Cross {
     int32_t last;   // the workgroup it ends in
     int32_t pad;
 };
+// Numbers of a place, whose heads are 16, or past 64 columns no more than a row's
+// (see shape_of).
+__host__ __device__ __forceinline__ constexpr int heads_of_place(int dim, int group) { return dim <= 64 || group >= 16 ? 16 : group; }
+__host__ __device__ __forceinline__ constexpr int numbers_of_place(int dim, int group) { return 32 + heads_of_place(dim, group) * dim; }
 __device__ __forceinline__ float* place(const Args& p, int w, int which) {
-    return p.a.part + (int64_t)p.s.crosses * 4 + ((int64_t)w * 2 + which) * (p.s.cols * (p.s.dim + 2));
+    return p.a.part + (int64_t)p.s.crosses * 4 + ((int64_t)w * 2 + which) * numbers_of_place(p.s.dim, p.s.group);
 }
 
 // Page lookups: token group g8 (8 tokens, which no page boundary cuts) of a
@@ -959,7 +962,7 @@ __global__ __launch_bounds__(kWaves * 64, per_cu(kDC, kSplitQ, kHeld)) void atte
                 if (p.a.lse && d == 0)
                     p.a.lse[at] = now.len <= 0 ? kNegInf : lse_of(p, M, L);
             } else {
-                *reinterpret_cast<float4*>(part + 2 * p.s.cols + q * p.s.dim + d) = o;
+                *reinterpret_cast<float4*>(part + 32 + q * p.s.dim + d) = o;
                 if (d == 0) part[2 * q] = M, part[2 * q + 1] = L;
             }
         }
