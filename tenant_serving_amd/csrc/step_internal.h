@@ -158,8 +158,7 @@ inline Form form_of(float scale, float cap) {
 }
 // A slope in these units; finite, so that it takes nothing off at no distance.
 __device__ __forceinline__ float slope_in(float slope, float unit) {
-    const float b = slope / unit;
-    return __builtin_isinf(b) ? __builtin_copysignf(0x1.fffffep127f, b) : b;
+    return __builtin_amdgcn_fmed3f(slope / unit, -0x1.fffffep127f, 0x1.fffffep127f);
 }
 
 // ---------------------------------------------------------------------------
