@@ -64,11 +64,11 @@ constexpr int keys_of(int width) { return width <= 128 ? 64 : 32; }
 // since a tile of 256 rows has half the conversions for each of them, else two
 // workgroups of 4 to a CU, which drift into turns by themselves (a whole prompt
 // of 8192 tokens, 64 query heads of 128 columns over 8, with 4 and with 8: bf16
-// 1054 and 1081 us, e4m3 1248 and 1158, 4-bit codes capped 1836 and 1717; 64
+// 1054 and 1081 us, e4m3 1248 and 1158, 4-bit codes capped 1790 and 1702; 64
 // columns 724 and 788, with e4m3 codes 779 and 782; 192 columns 1460 and 1557,
 // with codes 1647 and 1561; a chunk of 512 tokens on 32768 4-bit ones 656 and
 // 574; 15 tokens on 48000 bf16 ones 48 and 63).  Formed scores at 192 columns spill
-// with 8 (capped, e4m3 1999 and 2132, 4-bit codes 2109 and 2454).  At 256 columns a
+// with 8 (capped, e4m3 2094 and 2312, 4-bit codes 2211 and 2620).  At 256 columns a
 // workgroup of 4 takes a CU's registers.
 constexpr int waves_of(int width, int held, bool form) {
     return held == BD_BF16 || width == 64 || width == 256 || (width == 192 && form) ? 4 : 8;
