@@ -78,7 +78,7 @@ constexpr int width_of(int dim, int held) {
 // tokens, two would take 86 -> 107).  Of 4-bit codes with bf16 queries three up
 // to 128, whose loads in flight are small (64 sequences of up to 16381 tokens, 64
 // heads of 128 over 8, 132 -> 123 us, with a cap 141 -> 134; one of 131071 35.0 ->
-// 35.4).
+// 35.4); shape_of says where they are launched.
 constexpr int kCUs = 256;
 constexpr int per_cu(int width, bool split_q, int held) {
     return width <= 64 || (width <= 128 && held == BD_E2M1 && !split_q) ? 3 : width <= 192 || (held != BD_BF16 && !split_q) ? 2 : 1;
